@@ -335,3 +335,281 @@ def loop_floor(device: int, batch: int, iterations: int, stream=None):
     _check(_loop_floor(device, batch, iterations, _stream_ptr(stream), ctypes.byref(ms), ctypes.byref(n)),
            "tc_loop_floor")
     return float(ms.value), int(n.value)
+
+
+# ------------------------------------------------- paged cache (include/tcd_cache.h)
+
+DT_BF16, DT_F16 = 0, 1
+TREE_MAX_WORDS, PATH_MAX = 4, 256
+
+
+class _Kv(ctypes.Structure):
+    _fields_ = [("pool", _vp), ("device", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layers", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class _Tokens(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("cu_tokens", _vp), ("ctx_lens", _vp),
+                ("page_table", _vp), ("table_width", ctypes.c_int32)]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = [("qkv", _vp), ("qkv_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("q_weight", _vp),
+                ("k_weight", _vp), ("eps", ctypes.c_float), ("rope", _vp), ("rope_len", ctypes.c_int32),
+                ("positions", _vp), ("interleaved", ctypes.c_int32), ("q_out", _vp), ("q_out_stride", ctypes.c_int64)]
+
+
+class _Attend(ctypes.Structure):
+    _fields_ = [("q", _vp), ("q_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("tree", _vp), ("tree_words", ctypes.c_int32), ("out", _vp),
+                ("out_stride", ctypes.c_int64), ("lse", _vp)]
+
+
+_kvp, _tokp = ctypes.POINTER(_Kv), ctypes.POINTER(_Tokens)
+_kv_append = _decl("tc_kv_append", ctypes.c_int, [_kvp, ctypes.c_int32, _tokp, ctypes.POINTER(_Append), _vp, _vp])
+_attend = _decl("tc_attend", ctypes.c_int, [_kvp, ctypes.c_int32, _tokp, ctypes.POINTER(_Attend), _vp, ctypes.c_int64,
+                                            _vp, _vp])
+_attend_workspace = _decl("tc_attend_workspace", ctypes.c_int, [_kvp, _i64p])
+_tree_masks = _decl("tc_tree_masks", ctypes.c_int, [_tokp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp])
+_kv_copy_pages = _decl("tc_kv_copy_pages", ctypes.c_int, [_kvp, _vp, _vp, ctypes.c_int32, _vp, _vp])
+_kv_compact = _decl("tc_kv_compact", ctypes.c_int, [_kvp, _tokp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp])
+_pages_create = _decl("tc_pages_create", ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_vp)])
+_pages_destroy = _decl("tc_pages_destroy", None, [_vp])
+_pages_open = _decl("tc_pages_open", ctypes.c_int, [_vp, _i32p])
+_pages_close = _decl("tc_pages_close", ctypes.c_int, [_vp, ctypes.c_int32])
+_pages_reserve = _decl("tc_pages_reserve", ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _i32p,
+                                                          _i32p, _i32p])
+_pages_fork = _decl("tc_pages_fork", ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64, _i32p])
+_pages_trim = _decl("tc_pages_trim", ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64])
+_pages_row = _decl("tc_pages_row", ctypes.c_int, [_vp, ctypes.c_int32, _i32p, ctypes.c_int32, _i32p])
+_pages_free_count = _decl("tc_pages_free_count", ctypes.c_int, [_vp, _i32p])
+
+
+def _rows(t, dtype, device, what: str, heads: int, head_dim: int):
+    """Row stride (elements) of packed rows [n, heads * head_dim] or [n, heads, head_dim]; the rows may be slices
+    of wider ones."""
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{what} must be {dtype} on {device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == head_dim and stride[2] == 1 and (heads == 1 or stride[1] == head_dim)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * head_dim and stride[1] == 1
+    if not ok:
+        raise ValueError(f"{what} must hold rows of {heads} heads of {head_dim} contiguous elements")
+    # (the stride of a single row says nothing: torch keeps whatever it was)
+    return stride[0] if shape[0] > 1 else heads * head_dim
+
+
+def _ints(t, shape, device, what: str):
+    import torch
+    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+class KvCache:
+    """A paged key-value cache over a torch CUDA tensor
+    [layers, pages, 2 (keys, values), kv_heads, page_size, head_dim], bf16 or f16.
+
+    The object holds no cache state: the caller owns the pool, the page tables
+    and the lengths.  ``status`` arguments are int32 tensors, one code per
+    sequence (per pair for copy_pages); left out, they go to a buffer of the
+    object that raise_on_error() reads.  Calls on one object use its buffers
+    (that status, and a workspace per stream) and belong to one host thread.
+    """
+
+    def __init__(self, pool):
+        import torch
+        types = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+        if not (pool.is_cuda and pool.dtype in types and pool.dim() == 6 and pool.shape[2] == 2 and
+                pool.is_contiguous()):
+            raise ValueError("pool must be a contiguous bfloat16 or float16 CUDA tensor "
+                             "[layers, pages, 2, kv_heads, page_size, head_dim]")
+        self.pool, self.dtype, self.device = pool, pool.dtype, pool.device
+        self.layers, self.pages, _, self.kv_heads, self.page_size, self.head_dim = pool.shape
+        self._kv = _Kv(pool.data_ptr(), pool.device.index, types[pool.dtype], self.layers, self.pages, self.kv_heads,
+                       self.page_size, self.head_dim)
+        self._kvp = ctypes.byref(self._kv)
+        need = ctypes.c_int64()
+        _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
+        self._ws_bytes, self._ws = need.value, {}
+        self._status = torch.zeros(64, dtype=torch.int32, device=pool.device)
+        self._n_status = 0
+
+    def _stream(self, stream):
+        if stream is None:
+            import torch
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _codes(self, status, n: int):
+        if status is not None:
+            return _ints(status, (n,), self.device, "status")
+        if n > self._status.numel():
+            import torch
+            self._status = torch.zeros(2 * n, dtype=torch.int32, device=self.device)
+        self._n_status = n
+        return self._status.data_ptr()
+
+    def _tokens(self, n, cu, ctx_lens, page_table):
+        batch = ctx_lens.shape[0]
+        return _Tokens(batch, n, None if cu is None else _ints(cu, (batch + 1,), self.device, "cu_tokens"),
+                       _ints(ctx_lens, (batch,), self.device, "ctx_lens"),
+                       _ints(page_table, (batch, page_table.shape[-1]), self.device, "page_table"),
+                       page_table.shape[-1])
+
+    def append(self, layer: int, qkv, cu_tokens, ctx_lens, page_table, q_out, q_weight=None, k_weight=None,
+               eps: float = 1e-6, rope=None, positions=None, interleaved: bool = False, status=None, stream=None):
+        """tc_kv_append: qkv [n, (q_heads + 2 kv_heads) * head_dim], q_out [n, q_heads, head_dim]; rope float32
+        [positions, head_dim / 2, 2] (cosine, sine)."""
+        import torch
+        d, n = self.head_dim, qkv.shape[0]
+        hq = q_out.shape[1] if q_out.dim() == 3 else q_out.shape[1] // d
+        if q_out.shape[0] != n:
+            raise ValueError("q_out must have as many rows as qkv")
+        a = _Append(qkv.data_ptr(), _rows(qkv, self.dtype, self.device, "qkv", hq + 2 * self.kv_heads, d), hq, None,
+                    None, eps, None, 0, None, bool(interleaved), q_out.data_ptr(),
+                    _rows(q_out, self.dtype, self.device, "q_out", hq, d))
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                if w.dtype is not self.dtype or w.device != self.device or w.shape != (d,) or not w.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous {self.dtype} tensor of {d} elements")
+                setattr(a, name, w.data_ptr())
+        if rope is not None:
+            if (rope.dtype is not torch.float32 or rope.device != self.device or rope.dim() != 3 or
+                    rope.shape[1:] != (d // 2, 2) or not rope.is_contiguous()):
+                raise ValueError(f"rope must be a contiguous float32 tensor [positions, {d // 2}, 2]")
+            a.rope, a.rope_len = rope.data_ptr(), rope.shape[0]
+        if positions is not None:
+            a.positions = _ints(positions, (n,), self.device, "positions")
+        t = self._tokens(n, cu_tokens, ctx_lens, page_table)
+        _check(_kv_append(self._kvp, layer, ctypes.byref(t), ctypes.byref(a), self._codes(status, t.batch),
+                          self._stream(stream)), "tc_kv_append")
+
+    def attend(self, layer: int, q, cu_tokens, ctx_lens, page_table, out, max_tokens: int, scale=None, tree=None,
+               lse=None, status=None, stream=None):
+        """tc_attend: q and out [n, q_heads, head_dim]; tree int64 [n, words] (tree_masks) or None for the causal
+        mask; scale defaults to head_dim ** -0.5; lse float32 [n, q_heads] or None."""
+        import torch
+        d, n = self.head_dim, q.shape[0]
+        hq = q.shape[1] if q.dim() == 3 else q.shape[1] // d
+        if out.shape[0] != n:
+            raise ValueError("out must have as many rows as q")
+        a = _Attend(q.data_ptr(), _rows(q, self.dtype, self.device, "q", hq, d), hq, max_tokens,
+                    d ** -0.5 if scale is None else scale, None, 0, out.data_ptr(),
+                    _rows(out, self.dtype, self.device, "out", hq, d), None)
+        if tree is not None:
+            if (tree.dtype is not torch.int64 or tree.device != self.device or tree.dim() != 2 or
+                    tree.shape[0] != n or not tree.is_contiguous()):
+                raise ValueError("tree must be a contiguous int64 tensor [tokens, words]")
+            # (a call without tokens has no mask to point at)
+            a.tree, a.tree_words = tree.data_ptr() or None, tree.shape[1]
+        if lse is not None:
+            if lse.dtype is not torch.float32 or lse.device != self.device or lse.shape != (n, hq) or \
+                    not lse.is_contiguous():
+                raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
+            a.lse = lse.data_ptr()
+        t = self._tokens(n, cu_tokens, ctx_lens, page_table)
+        s = self._stream(stream)
+        ws = self._ws.get(s)
+        if ws is None:
+            ws = self._ws[s] = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        _check(_attend(self._kvp, layer, ctypes.byref(t), ctypes.byref(a), ws.data_ptr(), self._ws_bytes,
+                       self._codes(status, t.batch), s), "tc_attend")
+
+    def copy_pages(self, src, dst, status=None, stream=None):
+        """tc_kv_copy_pages: page dst[i] becomes page src[i] in every layer."""
+        n = src.shape[0]
+        _check(_kv_copy_pages(self._kvp, _ints(src, (n,), self.device, "src"), _ints(dst, (n,), self.device, "dst"), n,
+                              self._codes(status, n), self._stream(stream)), "tc_kv_copy_pages")
+
+    def compact(self, page_table, ctx_lens, path, n_path, lens_out, status=None, stream=None):
+        """tc_kv_compact: slot ctx_lens[b] + i takes what slot ctx_lens[b] + path[b, i] holds, i < n_path[b];
+        lens_out = ctx_lens + n_path."""
+        t = self._tokens(0, None, ctx_lens, page_table)
+        b = t.batch
+        _check(_kv_compact(self._kvp, ctypes.byref(t), _ints(path, (b, path.shape[-1]), self.device, "path"),
+                           path.shape[-1], _ints(n_path, (b,), self.device, "n_path"),
+                           _ints(lens_out, (b,), self.device, "lens_out"), self._codes(status, b),
+                           self._stream(stream)), "tc_kv_compact")
+
+    def raise_on_error(self):
+        """Wait for the device and raise the first error of the last call made without `status`."""
+        for b, code in enumerate(self._status[:self._n_status].tolist()):
+            if code != TC_OK:
+                raise TcError(code, f"sequence {b}")
+
+
+def tree_masks(parents, cu_tokens, ctx_lens, masks, positions=None, status=None, stream=None):
+    """tc_tree_masks: parents int32 [n] -> masks int64 [n, words] and positions int32 [n]."""
+    import torch
+    n, dev, batch = parents.shape[0], parents.device, ctx_lens.shape[0]
+    if masks.dtype is not torch.int64 or masks.device != dev or masks.dim() != 2 or masks.shape[0] != n or \
+            not masks.is_contiguous():
+        raise ValueError("masks must be a contiguous int64 tensor [tokens, words]")
+    if status is None:
+        status = torch.empty(batch, dtype=torch.int32, device=dev)
+    t = _Tokens(batch, n, _ints(cu_tokens, (batch + 1,), dev, "cu_tokens"), _ints(ctx_lens, (batch,), dev, "ctx_lens"),
+                None, 0)
+    with torch.cuda.device(dev):
+        _check(_tree_masks(ctypes.byref(t), _ints(parents, (n,), dev, "parents"), masks.shape[1], masks.data_ptr(),
+                           None if positions is None else _ints(positions, (n,), dev, "positions"),
+                           _ints(status, (batch,), dev, "status"), _stream_ptr(stream)), "tc_tree_masks")
+    return status
+
+
+class PagePool:
+    """Which pages of a cache belong to which sequence (tc_pages; host only)."""
+
+    def __init__(self, pages: int, page_size: int):
+        self._h = None
+        h = _vp()
+        _check(_pages_create(pages, page_size, ctypes.byref(h)), "tc_pages_create")
+        self._h, self.page_size = h, page_size
+
+    def open(self) -> int:
+        seq = ctypes.c_int32()
+        _check(_pages_open(self._h, ctypes.byref(seq)), "tc_pages_open")
+        return seq.value
+
+    def close_seq(self, seq: int):
+        _check(_pages_close(self._h, seq), "tc_pages_close")
+
+    def reserve(self, seq: int, start: int, end: int) -> list:
+        """Room for slots [start, end); returns the copies to make first: [(source page, new page)]."""
+        src, dst, n = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
+        _check(_pages_reserve(self._h, seq, start, end, ctypes.byref(src), ctypes.byref(dst), ctypes.byref(n)),
+               "tc_pages_reserve")
+        return [(src.value, dst.value)] if n.value else []
+
+    def fork(self, seq: int, length: int) -> int:
+        child = ctypes.c_int32()
+        _check(_pages_fork(self._h, seq, length, ctypes.byref(child)), "tc_pages_fork")
+        return child.value
+
+    def trim(self, seq: int, length: int):
+        _check(_pages_trim(self._h, seq, length), "tc_pages_trim")
+
+    def row(self, seq: int, width: int) -> np.ndarray:
+        out, n = np.zeros(max(width, 1), dtype=np.int32), ctypes.c_int32()
+        _check(_pages_row(self._h, seq, out.ctypes.data_as(_i32p), width, ctypes.byref(n)), "tc_pages_row")
+        return out[:width]
+
+    @property
+    def free(self) -> int:
+        n = ctypes.c_int32()
+        _check(_pages_free_count(self._h, ctypes.byref(n)), "tc_pages_free_count")
+        return n.value
+
+    def close(self):
+        if self._h:
+            _pages_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

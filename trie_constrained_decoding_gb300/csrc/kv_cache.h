@@ -1,0 +1,105 @@
+// Definitions shared by the kernels of the paged cache and of its attention.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "tcd_cache.h"
+#include "tcd_internal.h"
+
+namespace tcd {
+
+// One layer of a cache as the kernels see it.
+struct KvView {
+  uint8_t* base;      // the layer's first page
+  int32_t pages;
+  int32_t kv_heads;
+  int32_t page_size;  // a power of two
+  int32_t page_shift; // its logarithm
+};
+
+// The tokens of a call (tc_tokens_t by value).
+struct TokensView {
+  const int32_t* cu;
+  const int32_t* ctx;
+  const int32_t* table;
+  int32_t batch, n_tokens, width;
+};
+
+// 16-bit element types: pairs to and from 32-bit floats.
+struct Bf16 {
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+struct F16 {
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+
+// Rows, context and slots of sequence b.  False where they are out of range:
+// rows outside the packed arrays, or more slots than the page table has.
+struct SeqSpan {
+  int32_t row0, n, ctx;
+};
+__device__ __forceinline__ bool seq_span(const TokensView& t, int page_size, int b, SeqSpan* s) {
+  const int32_t lo = __ldg(t.cu + b), hi = __ldg(t.cu + b + 1), c = __ldg(t.ctx + b);
+  s->row0 = lo;
+  s->n = hi - lo;
+  s->ctx = c;
+  return lo >= 0 && hi >= lo && hi <= t.n_tokens && c >= 0 &&
+         (int64_t)c + (hi - lo) <= (int64_t)t.width * page_size;
+}
+
+// ------------------------------------------------------------ host helpers
+
+inline tc_status kv_fail(tc_status code, const std::string& msg) {
+  set_error_message(msg);
+  return code;
+}
+
+inline tc_status kv_cuda_fail(cudaError_t e, const char* what) {
+  set_error_message(std::string(what) + ": " + cudaGetErrorString(e));
+  cudaGetLastError();
+  return e == cudaErrorMemoryAllocation ? TC_ERR_OOM : TC_ERR_CUDA;
+}
+
+inline bool kv_misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Makes the cache's device current for the length of a call.
+struct KvDevice {
+  int prev = -1;
+  bool ok = false;
+  explicit KvDevice(int dev) {
+    ok = cudaGetDevice(&prev) == cudaSuccess && (prev == dev || cudaSetDevice(dev) == cudaSuccess);
+    if (prev == dev) prev = -1;
+    if (!ok) cudaGetLastError();
+  }
+  ~KvDevice() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+tc_status kv_check(const char* who, const tc_kv_t* kv);
+tc_status kv_check_tokens(const char* who, const tc_tokens_t* t, bool rows);
+KvView kv_view(const tc_kv_t* kv, int32_t layer);
+inline TokensView tokens_view(const tc_tokens_t* t) {
+  return TokensView{t->cu_tokens, t->ctx_lens, t->page_table, t->batch, t->n_tokens, t->table_width};
+}
+
+}  // namespace tcd
