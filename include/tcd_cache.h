@@ -178,6 +178,8 @@ typedef struct tc_attend_t {
   void* out;
   int64_t out_stride;
   float* lse;
+  int64_t wait_polls;  /* polls of one wait inside the kernel before it gives up; 0: the default (seconds) */
+  int32_t withhold;    /* 0; tests: the kernel leaves out its first load, so that its waits run out */
 } tc_attend_t;
 
 tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* args,

@@ -343,6 +343,21 @@ def test_refusals(tcd):
     assert not out.any()
 
 
+@pytest.mark.parametrize("shape", [([2, 1], [300, 40]), ([400], [0])])
+def test_wait_timeout_is_reported_and_the_next_call_works(tcd, shape):
+    """A load that never comes (left out by the test switch): the bounded waits
+    run out, the kernel returns, every sequence gets the error; then all is well."""
+    w = Batch(tcd, shape[0], shape[1], "bf16", 2, 128, 64, seed=37)
+    kv = w.fill()
+    q, q64 = w.normal(w.n, 4, 128)
+    w.cache.attend_wait_test(True, 2000)
+    run(w, q)
+    assert w.status.cpu().tolist() == [tcd.TC_ERR_DEVICE_TIMEOUT] * len(w.tokens)
+    w.cache.attend_wait_test(False, 0)
+    out, _ = run(w, q)
+    check(w, kv, q64, out)
+
+
 def test_long_cache_passes_32_bits(tcd):
     """A pool of more than 2^32 elements, its far end the sequence's pages."""
     torch = torch_mod()

@@ -363,7 +363,8 @@ class _Append(ctypes.Structure):
 class _Attend(ctypes.Structure):
     _fields_ = [("q", _vp), ("q_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("tree", _vp), ("tree_words", ctypes.c_int32), ("out", _vp),
-                ("out_stride", ctypes.c_int64), ("lse", _vp)]
+                ("out_stride", ctypes.c_int64), ("lse", _vp), ("wait_polls", ctypes.c_int64),
+                ("withhold", ctypes.c_int32)]
 
 
 _kvp, _tokp = ctypes.POINTER(_Kv), ctypes.POINTER(_Tokens)
@@ -435,6 +436,7 @@ class KvCache:
         need = ctypes.c_int64()
         _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
         self._ws_bytes, self._ws = need.value, {}
+        self._wait_test = (0, 0)
         self._status = torch.zeros(64, dtype=torch.int32, device=pool.device)
         self._n_status = 0
 
@@ -511,6 +513,7 @@ class KvCache:
                     not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
             a.lse = lse.data_ptr()
+        a.wait_polls, a.withhold = self._wait_test
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
         s = self._stream(stream)
         ws = self._ws.get(s)
@@ -518,6 +521,11 @@ class KvCache:
             ws = self._ws[s] = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
         _check(_attend(self._kvp, layer, ctypes.byref(t), ctypes.byref(a), ws.data_ptr(), self._ws_bytes,
                        self._codes(status, t.batch), s), "tc_attend")
+
+    def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
+        """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)
+        restores."""
+        self._wait_test = (int(wait_polls), int(bool(withhold)))
 
     def copy_pages(self, src, dst, status=None, stream=None):
         """tc_kv_copy_pages: page dst[i] becomes page src[i] in every layer."""

@@ -1,5 +1,48 @@
 // Attention of a call's tokens (a prompt, a drafted tree, single tokens) over
-// the paged cache.
+// the paged cache, on the tensor cores.
+//
+// Rows.  The queries of all heads that share a key-value head see the same
+// keys, so they are rows of one product: row r of an M tile is token r / G,
+// query head r % G of the group (G = q_heads / kv_heads), 128 / G whole tokens
+// a tile.  A single token of a decode step is a tile of G rows; a drafted tree
+// or a prompt fills tiles of 128.
+//
+// Work.  An item is one sequence, one key-value head and up to two M tiles;
+// its units are 128-slot tiles of the cache.  The units of all items form one
+// line that is cut into equal parts, one per CTA (one CTA per SM), whatever
+// the mixture of lengths: a long context is split over many CTAs, many short
+// ones share one.  Every CTA works its part out from the lengths on the
+// device, so the launch depends on none of them and can be captured.  An item
+// that a cut falls into leaves unnormalised partial results, at most two per
+// CTA, which a second kernel joins.
+//
+// One CTA, 12 warps:
+//  - warp 0 loads: queries, then key and value tiles, into a ring of 128 x
+//    head_dim tiles by TMA (128-byte swizzle; one copy per page piece and 64
+//    columns; pages past the sequence's end are not loaded);
+//  - warp 1, one thread, issues the products on the tensor cores: S = Q K^T
+//    (both operands in shared memory) and O += P V with P in tensor memory;
+//  - warp 2 hands out the CTA's segments (an item's part) through a small ring;
+//  - warps 4-7 and 8-11 are two softmax groups, one row per thread: a thread
+//    reads its row of S from tensor memory, keeps the row's maximum and sum in
+//    32 bits, and writes the weights P over S in the cache's type.
+// The two groups always alternate with the tensor cores: with two M tiles each
+// takes one and both use every key-value tile; with one M tile they take the
+// even and the odd tiles of the cache and are joined at the end.
+//
+// The maximum that the weights refer to is only moved when a row's maximum
+// has grown by more than 2^8 (the sums hold weights up to 2^8 in 32 bits, and
+// the types' relative precision does not depend on the scale): the
+// accumulator in tensor memory is rescaled then and rarely otherwise.
+//
+// A tile that some row does not see entirely (the end of the sequence, the
+// drafted tokens, the diagonal of a prompt) takes the masked path: a 128-bit
+// mask per row; and, as a weight of zero times an infinity would be NaN,
+// infinities and NaN among the values of slots that only some rows see are
+// taken out of the tile and added at the end to the rows that see them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <climits>
 
 #include "kv_cache.h"
@@ -7,97 +50,1152 @@
 namespace tcd {
 namespace {
 
+constexpr int kTile = 128;                  // slots of a key-value tile, rows of an M tile
+constexpr int kThreads = 384;
+constexpr uint32_t kHalfBytes = kTile * 128; // 128 rows of 64 elements
+constexpr float kRescale = 8.f;             // log2 of the growth that moves the reference maximum
+constexpr int kSegs = 4;                    // segments ahead of the softmax groups
+constexpr long long kWaitLimit = 1ll << 22; // default polls of one wait before giving up
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+};
+
+// A CTA's part of an item.
+struct Seg {
+  int32_t valid;     // 0: no more
+  int32_t seq, row0, n, ctx, head;
+  int32_t tok0;      // the item's first token
+  int32_t t0, t1;    // its key-value tiles [t0, t1)
+  int32_t two;       // two M tiles
+  int32_t part;      // -1: the whole item; else the slot of the partial result
+  int32_t last;      // (slot 1) the last worker that has a part of the item
+};
+
 struct AttendParams {
   KvView kv;
   TokensView tok;
-  const uint8_t* q;
-  int64_t q_stride;
-  int32_t q_heads;
+  int32_t q_heads, group, tile_tokens;  // tile_tokens = 128 / group
   int32_t max_tokens;
-  float scale_log2;
+  int32_t q_rows;                       // rows of one query load
+  float c;                              // |scale| log2(e), the factor of the exponents
+  int32_t negate;                       // the scale is negative
   const int64_t* tree;
   int32_t words;
   uint8_t* out;
   int64_t out_stride;
   float* lse;
   int32_t* status;
+  int32_t workers;
+  Seg* descs;        // [workers] item that starts in a worker and goes on in the next (valid = 0: none)
+  int32_t* errs;     // [workers] a wait ran out
+  float2* part_ml;   // [workers][2][256] maximum and sum of each row
+  float* part_o;     // [workers][2][256][D]
+  long long wait_limit;
+  int32_t withhold;  // test switch: the first worker's first load is not issued
 };
 
-// One warp per token and query head: one pass over the slots with the running
-// maximum and sum of the softmax, the row's elements spread over the lanes.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_rows_kernel(const AttendParams p) {
-  constexpr int E = D / 64;  // 32-bit words (two elements) per lane
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t n_work = (int64_t)p.tok.n_tokens * p.q_heads;
-  if (w >= n_work) {
-    const int64_t b = w - n_work;
-    if (b >= p.tok.batch) return;
-    SeqSpan s;
-    bool ok = seq_span(p.tok, p.kv.page_size, (int)b, &s) && s.n <= p.max_tokens;
-    if (ok && s.n > 0)
-      for (int i = lane; i <= (s.ctx + s.n - 1) >> p.kv.page_shift; i += 32)
-        ok &= (uint32_t)__ldg(p.tok.table + b * p.tok.width + i) < (uint32_t)p.kv.pages;
-    ok = __all_sync(0xffffffffu, ok);
-    if (lane == 0) p.status[b] = ok ? TC_OK : TC_ERR_BOUNDS;
+constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile; }
+
+struct Hdr {
+  uint64_t full[10], empty[10];      // key-value ring
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_ready[2], pv_done[2], o_full[2];
+  uint64_t o_free;                   // both groups have read the accumulators
+  uint64_t meet;                     // both groups
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int32_t abort;
+  int64_t total;                     // units of the call
+  int64_t off0;                      // the worker's first unit within its sequence
+  int32_t seq0;
+  uint32_t bad[2][8];                // tokens whose values are not finite, by segment parity
+  Seg seg[kSegs];
+  float2 ml[2][kTile];
+  int64_t scan[kThreads / 32];
+};
+template <int D>
+constexpr size_t smem_bytes() {
+  return (2 + Cfg<D>::kStages) * (size_t)Cfg<D>::kTileBytes + sizeof(Hdr);
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of one CTA");
+
+// -------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for a phase, at most `limit` polls; false if it gave up or another
+// wait of the CTA has.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long long limit, volatile int32_t* abort) {
+  for (long long i = 0; i < limit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63) == 63 && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+__device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page,
+                                       uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(head), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptors, 128-byte swizzle.  K-major (queries,
+// keys): rows of 128 bytes, groups of 8 rows 1024 bytes apart.  N-major
+// (values: a row is one slot, the columns are N): groups of 8 slots 1024 bytes
+// apart (stride offset), blocks of 64 columns a half tile apart (leading
+// offset).
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t a) {
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t a) {
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(kHalfBytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor of kind::f16: 32-bit accumulator, M = 128.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major) {
+  const uint32_t ty = T::kMma;
+  return (1u << 4) | (ty << 7) | (ty << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 32 columns of the warp's 32 rows (issued only: wait with tmem_ld_wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Ties the registers of a load to the wait before it, so that no use of them
+// can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_arrived(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unf2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ------------------------------------------------------------ the work's line
+
+// sum over i < n of floor((a i + b) / m), in O(log m) steps (Euclid's scheme).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t ans = 0;
+  while (n > 0) {
+    if (a >= m) {
+      ans += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return ans;
+}
+
+// Items and units of one sequence's key-value head.
+struct Line {
+  int n, ctx, step;  // tokens, cached tokens, tokens of an item
+  bool causal;
+  __device__ int items() const { return (n + step - 1) / step; }
+  // tiles of item i
+  __device__ int tiles(int i) const {
+    const int64_t end = causal ? min((int64_t)n, (int64_t)(i + 1) * step) : n;
+    return (int)((ctx + end + kTile - 1) / kTile);
+  }
+  // tiles of the items before item i
+  __device__ int64_t before(int i) const {
+    if (!causal) return (int64_t)i * tiles(0);
+    return floor_sum(i, kTile, step, (int64_t)ctx + step + kTile - 1);
+  }
+  __device__ int64_t units() const { return n > 0 ? before(items() - 1) + tiles(items() - 1) : 0; }
+  // the item that unit u is in
+  __device__ int item_of(int64_t u) const {
+    if (!causal) return (int)(u / tiles(0));
+    int lo = 0, hi = items();
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before(mid) <= u) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+};
+
+__device__ __forceinline__ bool line_of(const AttendParams& p, int b, SeqSpan* s, Line* l) {
+  const bool ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
+  l->n = ok ? s->n : 0;
+  l->ctx = ok ? s->ctx : 0;
+  l->step = 2 * p.tile_tokens;
+  l->causal = p.tree == nullptr;
+  return ok;
+}
+
+__device__ __forceinline__ int64_t worker_start(const AttendParams& p, int64_t total, int active, int w) {
+  return total * w / active;
+}
+
+// Which slots of a tile a row sees, 128 bits.
+__device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, int tok, int tile, uint32_t (&m)[4]) {
+  const int start = tile * kTile;
+  if (!p.tree) {
+    const int lim = g.ctx + tok + 1 - start;  // slots seen
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int k = lim - 32 * w;
+      m[w] = k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
+    }
     return;
   }
-  const int i = (int)(w / p.q_heads), h = (int)(w % p.q_heads);
-  int lo = 0, hi = p.tok.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(p.tok.cu + mid) <= i) lo = mid; else hi = mid;
-  }
-  SeqSpan s;
-  if (!seq_span(p.tok, p.kv.page_size, lo, &s) || s.n > p.max_tokens || i < s.row0 || i >= s.row0 + s.n) return;
-  const int t = i - s.row0, g = h / (p.q_heads / p.kv.kv_heads);
-  const int64_t head_words = (int64_t)p.kv.page_size * (D / 2);
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(p.q) + ((int64_t)i * p.q_stride + (int64_t)h * D) / 2;
-  float2 qf[E], o[E];
+  const uint32_t* row = reinterpret_cast<const uint32_t*>(p.tree) + (int64_t)(g.row0 + tok) * p.words * 2;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qf[e] = T::unpack(__ldg(q + e * 32 + lane));
-    o[e] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-  const int last = p.tree ? s.ctx + s.n : s.ctx + t + 1;
-  for (int j = 0; j < last; ++j) {
-    const int x = j - s.ctx;
-    if (x >= 0 && p.tree && ((x >> 6) >= p.words || !((p.tree[(int64_t)i * p.words + (x >> 6)] >> (x & 63)) & 1)))
-      continue;
-    const int page = __ldg(p.tok.table + (int64_t)lo * p.tok.width + (j >> p.kv.page_shift));
-    if ((uint32_t)page >= (uint32_t)p.kv.pages) continue;
-    const uint32_t* k = reinterpret_cast<const uint32_t*>(p.kv.base) +
-                        ((int64_t)page * 2 * p.kv.kv_heads + g) * head_words +
-                        (int64_t)(j & (p.kv.page_size - 1)) * (D / 2);
-    float dot = 0.f;
-    float2 v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 kf = T::unpack(__ldg(k + e * 32 + lane));
-      v[e] = T::unpack(__ldg(k + p.kv.kv_heads * head_words + e * 32 + lane));
-      dot = fmaf(qf[e].x, kf.x, fmaf(qf[e].y, kf.y, dot));
+  for (int w = 0; w < 4; ++w) {
+    const int x = start + 32 * w - g.ctx;  // drafted token of the word's first slot
+    uint32_t v;
+    if (x <= -32) {
+      v = 0xffffffffu;
+    } else {
+      const int i = x < 0 ? -1 : x >> 5;   // mask word that holds bit x (-1: the cached slots)
+      const uint32_t lo = i < 0 ? 0xffffffffu : i < 2 * p.words ? __ldg(row + i) : 0u;
+      const uint32_t hi = i + 1 < 2 * p.words ? __ldg(row + i + 1) : 0u;
+      v = __funnelshift_r(lo, hi, (uint32_t)x & 31u);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    dot *= p.scale_log2;
-    const float m2 = fmaxf(m, dot), ref = m2 == -INFINITY ? 0.f : m2;
-    const float a = exp2f(m - ref), w2 = exp2f(dot - ref);
-    l = l * a + w2;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[e].x = fmaf(w2, v[e].x, o[e].x * a);
-      o[e].y = fmaf(w2, v[e].y, o[e].y * a);
-    }
-    m = m2;
+    const int left = g.ctx + g.n - (start + 32 * w);  // slots of the word that the sequence has
+    m[w] = left <= 0 ? 0u : left >= 32 ? v : v & ((1u << left) - 1u);
   }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out) + ((int64_t)i * p.out_stride + (int64_t)h * D) / 2;
+}
+
+// The first slot of an item that some row of it does not see.
+__device__ __forceinline__ int first_hidden(const AttendParams& p, const Seg& g) {
+  return p.tree ? g.ctx : g.ctx + g.tok0 + 1;
+}
+
+template <typename T>
+__device__ __forceinline__ bool finite2(uint32_t v) {
+  return (v & T::kExp) != T::kExp && (v & (T::kExp << 16)) != (T::kExp << 16);
+}
+// One element of a pair: zero unless it is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ float2 non_finite(uint32_t v) {
+  const float2 f = T::unpack(v);
+  return make_float2((v & T::kExp) == T::kExp ? f.x : 0.f, (v & (T::kExp << 16)) == (T::kExp << 16) ? f.y : 0.f);
+}
+
+// ------------------------------------------------------------------- kernel
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap map_kv,
+                  const __grid_constant__ CUtensorMap map_q) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Hdr* hdr = reinterpret_cast<Hdr*>(smem + (2 + NS) * (size_t)C::kTileBytes);
+  const uint32_t q_s = smem_u32(smem), kv_s = q_s + 2 * C::kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int worker = blockIdx.x;
+  volatile int32_t* abort = &hdr->abort;
+  const long long wl = p.wait_limit;
+
+  // The swizzle wants tiles on 1024-byte boundaries; dynamic shared memory
+  // starts on one where a kernel has no other.
+  if (q_s & 1023u) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) {
+      p.descs[worker].valid = 0;
+      p.errs[worker] = 1;
+    }
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&hdr->full[i]), 1);
+      mbar_init(smem_u32(&hdr->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&hdr->q_full[i]), 1);
+      mbar_init(smem_u32(&hdr->q_empty[i]), 1);
+      mbar_init(smem_u32(&hdr->s_full[i]), 1);
+      mbar_init(smem_u32(&hdr->p_ready[i]), kTile);
+      mbar_init(smem_u32(&hdr->pv_done[i]), 1);
+      mbar_init(smem_u32(&hdr->o_full[i]), 1);
+    }
+    mbar_init(smem_u32(&hdr->o_free), 2 * kTile);
+    mbar_init(smem_u32(&hdr->meet), 2 * kTile);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(smem_u32(&hdr->seg_full[i]), 1);
+      mbar_init(smem_u32(&hdr->seg_empty[i]), 2 + 8);  // loader, issuer, eight softmax warps
+    }
+    mbar_init(smem_u32(&hdr->drain), 1);
+    hdr->abort = 0;
+    hdr->seq0 = -1;
+    for (int i = 0; i < 16; ++i) hdr->bad[i >> 3][i & 7] = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_kv)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+  }
+  if (warp == 3) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hdr->tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // The setup above touches only this CTA; everything read or written from
+  // here on may belong to the kernel before.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // Units of every sequence: thread i counts a run of them, then a scan over
+  // the CTA gives the total and who holds this worker's first unit.
+  const int run = (p.tok.batch + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int i = 0; i < run; ++i) {
+    const int b = tid * run + i;
+    SeqSpan s;
+    Line l;
+    if (b < p.tok.batch && line_of(p, b, &s, &l)) mine += l.units() * p.kv.kv_heads;
+  }
+  int64_t incl = mine;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e * 32 + lane] = T::pack(o[e].x * r, o[e].y * r);
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)i * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) hdr->scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t total = 0, start_of_warp = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) start_of_warp += hdr->scan[i];
+    total += hdr->scan[i];
+  }
+  const int active = (int)min((int64_t)p.workers, total);
+  const int64_t begin = worker < active ? worker_start(p, total, active, worker) : 0;
+  const int64_t end = worker < active ? worker_start(p, total, active, worker + 1) : 0;
+  const int64_t excl = start_of_warp + incl - mine;
+  if (begin < end && begin >= excl && begin < excl + mine) {
+    int64_t at = excl;
+    for (int i = 0; i < run; ++i) {
+      const int b = tid * run + i;
+      SeqSpan s;
+      Line l;
+      if (b >= p.tok.batch || !line_of(p, b, &s, &l)) continue;
+      const int64_t u = l.units() * p.kv.kv_heads;
+      if (begin < at + u) {
+        hdr->seq0 = b;
+        hdr->off0 = begin - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = hdr->tmem_base;
+  const bool held = p.withhold != 0 && worker == 0;
+  uint32_t armed = 0;  // loader: key-value stages armed, for the exit path
+  uint32_t q_armed = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- loader
+    uint32_t it = 0, qi = 0;
+    const int box = min(p.kv.page_size, kTile), pieces = kTile / box;
+    const int piece = lane / C::kHalves, half = lane % C::kHalves;
+    bool stop = false;
+    for (int k = 0; !stop; ++k) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort))) break;
+      const Seg g = hdr->seg[k % kSegs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
+      if (!g.valid) break;
+      for (int m = 0; m <= g.two; ++m, ++qi) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->q_empty[qi & 1]), ((qi >> 1) & 1) ^ 1, wl, abort))) {
+          stop = true;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&hdr->q_full[qi & 1]);
+          mbar_expect_tx(bar, (uint32_t)p.q_rows * 128u * C::kHalves);
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_q(q_s + (qi & 1) * C::kTileBytes + h * kHalfBytes, &map_q, h * 64, g.head * p.group,
+                  g.row0 + g.tok0 + m * p.tile_tokens, bar);
+        }
+        ++q_armed;
+      }
+      if (stop) break;
+      const int n = g.t1 - g.t0;
+      const int slots = g.ctx + g.n;  // (a causal item reads less: its last tile ends there too)
+      const int32_t* row = p.tok.table + (int64_t)g.seq * p.tok.width;
+      // Order of use: keys one tile ahead of the values with one M tile (the
+      // groups take turns), together with two.
+      for (int j = 0; j < 2 * n && !stop; ++j, ++it) {
+        int tile, is_v;
+        if (g.two) {
+          tile = j >> 1;
+          is_v = j & 1;
+        } else if (j == 0) {
+          tile = 0;
+          is_v = 0;
+        } else if (j == 2 * n - 1) {
+          tile = n - 1;
+          is_v = 1;
+        } else {
+          is_v = (j & 1) ^ 1;              // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
+          tile = is_v ? (j >> 1) - 1 : (j + 1) >> 1;
+        }
+        const int slot = (g.t0 + tile) * kTile + piece * box;
+        const bool load = piece < pieces && slot < slots;
+        const int page = load ? __ldg(row + (slot >> p.kv.page_shift)) : 0;
+        const int stage = (int)(it % NS);
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->empty[stage]), ((it / NS) & 1) ^ 1, wl, abort))) {
+          stop = true;
+          break;
+        }
+        const uint32_t bar = smem_u32(&hdr->full[stage]);
+        const int count = __popc(__ballot_sync(0xffffffffu, load));
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(count * box * 128));
+        __syncwarp();
+        if (load && !(held && it == 0))
+          tma_kv(kv_s + stage * C::kTileBytes + half * kHalfBytes + piece * box * 128, &map_kv, half * 64,
+                 slot & (p.kv.page_size - 1), is_v * p.kv.kv_heads + g.head, page, bar);
+        ++armed;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- issuer
+    if (lane == 0) {
+      uint32_t it = 0, qi = 0, n_pr[2] = {0, 0}, n_pv[2] = {0, 0};
+      constexpr uint32_t id_s = idesc<T>(kTile, false), id_o = idesc<T>(D, true);
+      bool ok = true;
+      // S_slot = Q K^T from a ring stage
+      auto scores = [&](int slot, uint32_t q_buf, uint32_t stage) {
+        const uint32_t a = q_s + q_buf * C::kTileBytes, b = kv_s + stage * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (uint32_t)(k >> 2) * kHalfBytes + (uint32_t)(k & 3) * 32;
+          mma_ss(tmem + slot * kTile, desc_k_major(a + o), desc_k_major(b + o), id_s, k > 0);
+        }
+        mma_commit(smem_u32(&hdr->s_full[slot]));
+      };
+      // O_slot += P V
+      auto outputs = [&](int slot, uint32_t stage, bool first) {
+        const uint32_t b = kv_s + stage * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(tmem + 2 * kTile + slot * 128, tmem + slot * kTile + k * 8, desc_n_major(b + k * 2048), id_o,
+                 !first || k > 0);
+        mma_commit(smem_u32(&hdr->pv_done[slot]));
+        ++n_pv[slot];
+      };
+      auto wait_kv = [&](uint32_t i) {
+        ok = ok && mbar_wait(smem_u32(&hdr->full[i % NS]), (i / NS) & 1, wl, abort);
+        tc_fence_after();
+        return ok;
+      };
+      auto wait_p = [&](int slot) {
+        ok = ok && mbar_wait(smem_u32(&hdr->p_ready[slot]), n_pr[slot] & 1, wl, abort);
+        ++n_pr[slot];
+        tc_fence_after();
+        return ok;
+      };
+      // the last P V of a slot has been done: its scores' place is free
+      auto wait_pv = [&](int slot) {
+        ok = ok && (n_pv[slot] == 0 ||
+                    mbar_wait(smem_u32(&hdr->pv_done[slot]), (n_pv[slot] - 1) & 1, wl, abort));
+        tc_fence_after();
+        return ok;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
+        const Seg g = hdr->seg[k % kSegs];
+        mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
+        if (!g.valid) break;
+        const int n = g.t1 - g.t0;
+        const uint32_t q0 = qi & 1, q1 = (qi + 1) & 1;
+        for (int m = 0; m <= g.two; ++m) {
+          const uint32_t x = qi + m;
+          ok = ok && mbar_wait(smem_u32(&hdr->q_full[x & 1]), (x >> 1) & 1, wl, abort);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        qi += 1 + g.two;
+        // The accumulators of the segment before have been read (waited for
+        // just before the first P V: the scores may start earlier).
+        auto wait_o = [&]() {
+          ok = ok && (k == 0 || mbar_wait(smem_u32(&hdr->o_free), (uint32_t)(k - 1) & 1, wl, abort));
+          tc_fence_after();
+          return ok;
+        };
+        if (g.two) {
+          if (!wait_kv(it) || !wait_pv(0)) break;
+          scores(0, q0, it % NS);
+          if (!wait_pv(1)) break;
+          scores(1, q1, it % NS);
+          mma_commit(smem_u32(&hdr->empty[it % NS]));
+          if (n == 1) {
+            mma_commit(smem_u32(&hdr->q_empty[q0]));
+            mma_commit(smem_u32(&hdr->q_empty[q1]));
+          }
+          if (!wait_o()) break;
+          for (int i = 0; i < n; ++i) {
+            const uint32_t v = it + 2 * i + 1, kn = v + 1;
+            if (!wait_p(0) || !wait_kv(v)) break;
+            outputs(0, v % NS, i == 0);
+            if (!wait_p(1)) break;
+            outputs(1, v % NS, i == 0);
+            mma_commit(smem_u32(&hdr->empty[v % NS]));
+            if (i + 1 < n) {
+              if (!wait_kv(kn) || !wait_pv(0)) break;
+              scores(0, q0, kn % NS);
+              if (!wait_pv(1)) break;
+              scores(1, q1, kn % NS);
+              mma_commit(smem_u32(&hdr->empty[kn % NS]));
+              if (i + 2 == n) {
+                mma_commit(smem_u32(&hdr->q_empty[q0]));
+                mma_commit(smem_u32(&hdr->q_empty[q1]));
+              }
+            }
+          }
+          if (!ok) break;
+          mma_commit(smem_u32(&hdr->o_full[0]));
+          mma_commit(smem_u32(&hdr->o_full[1]));
+        } else {
+          // K0 K1 V0 K2 V1 ...: place of K(i) and V(i) in the ring
+          auto k_at = [&](int i) { return it + (i == 0 ? 0 : 2 * i - 1); };
+          auto v_at = [&](int i) { return it + (i + 1 < n ? 2 * i + 2 : 2 * n - 1); };
+          auto next_scores = [&](int i) {
+            if (!wait_kv(k_at(i)) || !wait_pv(i & 1)) return false;
+            scores(i & 1, q0, k_at(i) % NS);
+            mma_commit(smem_u32(&hdr->empty[k_at(i) % NS]));
+            if (i + 1 == n) mma_commit(smem_u32(&hdr->q_empty[q0]));
+            return true;
+          };
+          if (!next_scores(0)) break;
+          if (n > 1 && !next_scores(1)) break;
+          if (!wait_o()) break;
+          for (int i = 0; i < n; ++i) {
+            const int slot = i & 1;
+            if (!wait_p(slot) || !wait_kv(v_at(i))) break;
+            outputs(slot, v_at(i) % NS, i < 2);
+            mma_commit(smem_u32(&hdr->empty[v_at(i) % NS]));
+            if (i + 2 < n && !next_scores(i + 2)) break;
+          }
+          if (!ok) break;
+          mma_commit(smem_u32(&hdr->o_full[0]));
+          mma_commit(smem_u32(&hdr->o_full[1]));
+        }
+        it += 2 * n;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- segments
+    if (lane == 0) {
+      int64_t left = end - begin, off = hdr->off0;
+      int b = hdr->seq0, k = 0;
+      bool open_end = false, ok = true;
+      if (b < 0) left = 0;
+      Seg d{};
+      while (ok) {
+        Seg g{};
+        if (left > 0) {
+          SeqSpan s;
+          Line l;
+          // (sequences without units are passed over)
+          int64_t per = 0;
+          while (b < p.tok.batch) {
+            if (line_of(p, b, &s, &l) && (per = l.units()) * p.kv.kv_heads > off) break;
+            off = 0;
+            ++b;
+          }
+          if (b >= p.tok.batch) break;  // (cannot be: the units add up)
+          const int head = (int)(off / per);
+          int64_t r = off % per;
+          int item = l.item_of(r);
+          r -= l.before(item);
+          // the rest of this sequence, segment by segment
+          int h = head;
+          while (left > 0 && h < p.kv.kv_heads) {
+            const int tiles = l.tiles(item);
+            const int64_t take = min((int64_t)tiles - r, left);
+            g.valid = 1;
+            g.seq = b;
+            g.row0 = s.row0;
+            g.n = s.n;
+            g.ctx = s.ctx;
+            g.head = h;
+            g.tok0 = item * l.step;
+            g.t0 = (int)r;
+            g.t1 = (int)(r + take);
+            g.two = s.n - g.tok0 > p.tile_tokens;
+            g.part = take == tiles ? -1 : r > 0 ? 0 : 1;
+            g.last = worker;
+            if (g.part == 1) {
+              // the item's last unit lies with the worker that this finds
+              const int64_t last_unit = end - left + tiles - 1;
+              int w = worker + 1;
+              while (worker_start(p, total, active, w + 1) <= last_unit) ++w;
+              g.last = w;
+              d = g;
+              open_end = true;
+            }
+            if (!mbar_wait(smem_u32(&hdr->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1, wl, abort)) {
+              ok = false;
+              break;
+            }
+            hdr->seg[k % kSegs] = g;
+            mbar_arrive(smem_u32(&hdr->seg_full[k % kSegs]));
+            ++k;
+            left -= take;
+            r = 0;
+            if (++item == l.items()) {
+              item = 0;
+              ++h;
+            }
+          }
+          off = 0;
+          ++b;
+        } else {
+          if (mbar_wait(smem_u32(&hdr->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1, wl, abort)) {
+            hdr->seg[k % kSegs].valid = 0;
+            mbar_arrive(smem_u32(&hdr->seg_full[k % kSegs]));
+          }
+          break;
+        }
+      }
+      d.valid = open_end;
+      p.descs[worker] = d;
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ----------------------------------------------------- softmax groups
+    const int grp = (warp - 4) >> 2;               // which slot
+    const int r = tid - 128 - grp * kTile;         // row of the M tile (TMEM lane)
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + grp * kTile;
+    const uint32_t t_o = tmem + lane_base + 2 * kTile;  // both accumulators
+    uint32_t n_s = 0, n_meet = 0, it = 0;
+    auto meet = [&]() {
+      mbar_arrive(smem_u32(&hdr->meet));
+      const bool ok = mbar_wait(smem_u32(&hdr->meet), n_meet & 1, wl, abort);
+      ++n_meet;
+      return (bool)__all_sync(0xffffffffu, ok);
+    };
+    for (int k = 0;; ++k) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort))) break;
+      const Seg g = hdr->seg[k % kSegs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
+      if (!g.valid) break;
+      const int n = g.t1 - g.t0;
+      const int tok = g.tok0 + (g.two ? grp * p.tile_tokens : 0) + r / p.group;
+      const bool live = r < p.tile_tokens * p.group && tok < g.n;
+      const bool any = __any_sync(0xffffffffu, live);
+      const int hidden = first_hidden(p, g);
+      uint32_t* bad = hdr->bad[k & 1];
+      float m = -INFINITY, l = 0.f;
+      bool stop = false;
+      for (int i = g.two ? 0 : grp; i < n; i += g.two ? 1 : 2) {
+        const int tile = g.t0 + i;
+        const bool edge = (tile + 1) * kTile > hidden;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort))) {
+          stop = true;
+          break;
+        }
+        ++n_s;
+        tc_fence_after();
+        if (any) {
+          uint32_t s[kTile];
+          tmem_ld32(t_s, s);
+          tmem_ld32(t_s + 32, s + 32);
+          tmem_ld32(t_s + 64, s + 64);
+          tmem_ld32(t_s + 96, s + 96);
+          tmem_ld_wait();
+          tmem_arrived(s);
+          tmem_arrived(s + 32);
+          tmem_arrived(s + 64);
+          tmem_arrived(s + 96);
+          if (p.negate) {
+#pragma unroll
+            for (int j = 0; j < kTile; ++j) s[j] ^= 0x80000000u;
+          }
+          if (edge) {
+            uint32_t mask[4] = {0u, 0u, 0u, 0u};
+            if (live) row_mask(p, g, tok, tile, mask);
+#pragma unroll
+            for (int j = 0; j < kTile; ++j)
+              s[j] = (mask[j >> 5] >> (j & 31)) & 1u ? s[j] : 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
+#pragma unroll
+          for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // Move the reference maximum only for a large growth (or the first
+          // finite score); the accumulator exists from the second tile on.
+          const bool first = i < (g.two ? 1 : 2);
+          const bool grow = first || (top - m) * p.c > kRescale;
+          if (__any_sync(0xffffffffu, grow) && !first) {
+            const float f = grow ? ex2((m - top) * p.c) : 1.f;
+            // (the P V of the tile before is complete: the scores just read were issued after it)
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + grp * 128 + c, o);
+              tmem_ld_wait();
+              tmem_arrived(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(t_o + grp * 128 + c, o);
+              tmem_st16(t_o + grp * 128 + c + 16, o + 16);
+            }
+            l *= f;
+          }
+          if (grow) m = top;
+          const float off = m == -INFINITY ? 0.f : -m * p.c;
+          const uint64_t c2 = f2(p.c, p.c), off2 = f2(off, off);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = unf2(fma2(f2(__uint_as_float(s[q * 32 + 2 * j]), __uint_as_float(s[q * 32 + 2 * j + 1])),
+                                         c2, off2));
+              const float a = ex2(x.x), b = ex2(x.y);
+              sum[j & 1] = add2(sum[j & 1], f2(a, b));
+              pk[j] = T::pack(a, b);
+            }
+            tmem_st16(t_s + q * 16, pk);
+          }
+          const float2 t = unf2(add2(sum[0], sum[1]));
+          l += t.x + t.y;
+          tmem_st_wait();
+        }
+        if (edge) {
+          // Values of slots that some row must not see: zero past the end of
+          // the sequence, and infinities and NaN out (kept in `bad`).
+          const uint32_t vi = it + (g.two ? 2 * i + 1 : i + 1 < n ? 2 * i + 2 : 2 * n - 1);
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->full[vi % NS]), (vi / NS) & 1, wl, abort))) {
+            stop = true;
+            break;
+          }
+          const int slot = tile * kTile + r;
+          const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + r * 128;
+          // (with two M tiles each group looks at half of the rows)
+          if (slot >= hidden && (!g.two || r / 64 == grp)) {
+            bool found = false;
+#pragma unroll 1
+            for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch) {
+                const uint32_t a = row + h * kHalfBytes + ((ch ^ (r & 7)) << 4);
+                if (slot >= g.ctx + g.n) {
+                  sts128(a, make_uint4(0u, 0u, 0u, 0u));
+                } else {
+                  uint4 v = lds128(a);
+                  if (!(finite2<T>(v.x) && finite2<T>(v.y) && finite2<T>(v.z) && finite2<T>(v.w))) {
+                    found = true;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                      uint32_t& x = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+                      if ((x & T::kExp) == T::kExp) x &= 0xffff0000u;
+                      if ((x & (T::kExp << 16)) == (T::kExp << 16)) x &= 0x0000ffffu;
+                    }
+                    sts128(a, v);
+                  }
+                }
+              }
+            if (found) {
+              const int x = slot - hidden;  // (an item or a tree has at most 256 tokens: no row sees later ones)
+              if (x < 256) atomicOr(&bad[x >> 5], 1u << (x & 31));
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (g.two && !meet()) {
+            stop = true;
+            break;
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&hdr->p_ready[grp]));
+      }
+      if (stop) break;
+      it += 2 * n;
+      // ------------------------------------------------ end of the segment
+      if (!g.two) hdr->ml[grp][r] = make_float2(m, l);
+      if (tid == 128)
+        for (int i = 0; i < 8; ++i) hdr->bad[(k & 1) ^ 1][i] = 0u;  // (last read before the groups' last meeting)
+      if (!meet()) break;
+      const bool used1 = g.two || n > 1;
+      bool ok = mbar_wait(smem_u32(&hdr->o_full[0]), k & 1, wl, abort);
+      ok = ok && mbar_wait(smem_u32(&hdr->o_full[1]), k & 1, wl, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      // Factors of the two accumulators (one M tile: both are this row's; two: only the group's own).
+      float f0 = 1.f, f1 = 1.f;
+      if (!g.two) {
+        const float2 a = hdr->ml[0][r], b = hdr->ml[1][r];
+        m = fmaxf(a.x, b.x);
+        f0 = m == -INFINITY ? 0.f : ex2((a.x - m) * p.c);
+        f1 = m == -INFINITY ? 0.f : ex2((b.x - m) * p.c);
+        l = a.y * f0 + b.y * f1;
+      }
+      uint32_t any_bad = 0;
+      for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+      const int head = g.head * p.group + r % p.group;
+      const int64_t out_row = (int64_t)(g.row0 + tok);
+      const float norm = g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
+      const size_t part = g.part >= 0 ? ((size_t)worker * 2 + g.part) * 2 * kTile + (g.two ? grp * kTile : 0) + r : 0;
+      if (any) {
+        // columns: all of the group's own accumulator, or half of both
+        const int c_lo = g.two ? 0 : grp * (D / 2), c_hi = g.two ? D : c_lo + D / 2;
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_o + (g.two ? grp * 128 : 0) + c, o);
+          tmem_ld_wait();
+          tmem_arrived(o);
+          float v[32];
+          if (g.two) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;
+            if (used1) {
+              tmem_ld32(t_o + 128 + c, o);
+              tmem_ld_wait();
+              tmem_arrived(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o[j]), f1, v[j]);
+            }
+          }
+          if (live) {
+            if (any_bad) {
+              // Infinities and NaN that were taken out, for the rows that see their slot.
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i)
+#pragma unroll 1
+                for (uint32_t w = bad[i]; w; w &= w - 1) {
+                  const int slot = hidden + i * 32 + __ffs(w) - 1, tile = slot / kTile;
+                  uint32_t mask[4];
+                  row_mask(p, g, tok, tile, mask);
+                  const int j = slot % kTile;
+                  const uint32_t mw = j < 32 ? mask[0] : j < 64 ? mask[1] : j < 96 ? mask[2] : mask[3];
+                  if (!((mw >> (j & 31)) & 1u)) continue;
+                  const int page = __ldg(p.tok.table + (int64_t)g.seq * p.tok.width + (slot >> p.kv.page_shift));
+                  if ((uint32_t)page >= (uint32_t)p.kv.pages) continue;
+                  const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                      p.kv.base + ((((int64_t)page * 2 + 1) * p.kv.kv_heads + g.head) * p.kv.page_size +
+                                   (slot & (p.kv.page_size - 1))) * D * 2 + c * 2);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const float2 x = non_finite<T>(__ldg(src + e));
+                    v[2 * e] += x.x;
+                    v[2 * e + 1] += x.y;
+                  }
+                }
+            }
+            if (g.part < 0) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + (out_row * p.out_stride + (int64_t)head * D + c) * 2);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                dst[j] = make_uint4(T::pack(v[8 * j] * norm, v[8 * j + 1] * norm),
+                                    T::pack(v[8 * j + 2] * norm, v[8 * j + 3] * norm),
+                                    T::pack(v[8 * j + 4] * norm, v[8 * j + 5] * norm),
+                                    T::pack(v[8 * j + 6] * norm, v[8 * j + 7] * norm));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+          }
+        }
+        if (live && (g.two || grp == 0)) {
+          if (g.part >= 0)
+            p.part_ml[part] = make_float2(m, l);
+          else if (p.lse)
+            p.lse[out_row * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&hdr->o_free));
+      if (!meet()) break;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (hdr->abort) {
+    // A wait ran out.  Everything this CTA started has to end before it
+    // leaves (waits bounded again): the products that were issued, and the
+    // loads of stages that no product has consumed.
+    if (warp == 1 && lane == 0) {
+      mma_commit(smem_u32(&hdr->drain));
+      int32_t none = 0;
+      mbar_wait(smem_u32(&hdr->drain), 0u, wl, &none);
+    }
+    if (warp == 0 && lane == 0) {
+      int32_t none = 0;
+      for (uint32_t j = armed > (uint32_t)NS ? armed - NS : 0; j < armed; ++j)
+        if (!(held && j == 0)) mbar_wait(smem_u32(&hdr->full[j % NS]), (j / NS) & 1, wl, &none);
+      for (uint32_t j = q_armed > 2 ? q_armed - 2 : 0; j < q_armed; ++j)
+        mbar_wait(smem_u32(&hdr->q_full[j & 1]), (j >> 1) & 1, wl, &none);
+    }
+    __syncwarp();
+  }
+  if (tid == 0) p.errs[worker] = hdr->abort;
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ------------------------------------------------------------ joining kernel
+
+constexpr int kJoinRows = 8;  // rows of an item joined by one block at a time (a warp each)
+
+// Blocks (w, y), w < workers: the item that starts in worker w and goes on in
+// the next; its rows y * 8 + warp, y * 8 + warp + 8 * gridDim.y, ...  The parts
+// are added in the order of the workers: the result does not depend on timing.
+// Blocks past the workers write the status of eight sequences each.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinRows * 32) attend_join_kernel(const AttendParams p) {
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x >= (unsigned)p.workers) {
+    const int b = (blockIdx.x - p.workers) * kJoinRows + warp;
+    if (blockIdx.y != 0 || b >= p.tok.batch) return;
+    SeqSpan s;
+    bool ok = seq_span(p.tok, p.kv.page_size, b, &s) && s.n <= p.max_tokens;
+    if (ok && s.n > 0)
+      for (int i = lane; i <= (s.ctx + s.n - 1) >> p.kv.page_shift; i += 32)
+        ok &= (uint32_t)__ldg(p.tok.table + (int64_t)b * p.tok.width + i) < (uint32_t)p.kv.pages;
+    bool late = false;
+    for (int i = lane; i < p.workers; i += 32) late |= p.errs[i] != 0;
+    ok = __all_sync(0xffffffffu, ok);
+    late = __any_sync(0xffffffffu, late);
+    if (lane == 0) p.status[b] = late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS;
+    return;
+  }
+  const Seg g = p.descs[blockIdx.x];
+  if (!g.valid) return;
+  const int rows = (g.two ? 2 : 1) * kTile;
+  for (int rr = blockIdx.y * kJoinRows + warp; rr < rows; rr += gridDim.y * kJoinRows) {
+    const int r = rr % kTile, tok = g.tok0 + rr / kTile * p.tile_tokens + r / p.group;
+    if (r >= p.tile_tokens * p.group || tok >= g.n) continue;
+    auto at = [&](int w) { return ((size_t)w * 2 + (w == (int)blockIdx.x)) * 2 * kTile + rr; };
+    float m = -INFINITY;
+    for (int w = blockIdx.x + lane; w <= g.last; w += 32) m = fmaxf(m, p.part_ml[at(w)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
+#pragma unroll 4
+    for (int w = blockIdx.x; w <= g.last; ++w) {
+      const float2 ml = p.part_ml[at(w)];
+      const float f = m == -INFINITY ? 0.f : ex2((ml.x - m) * p.c);
+      const float* src = p.part_o + at(w) * D + lane * E;
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = fmaf(src[e], f, v[e]);
+    }
+    const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    const int head = g.head * p.group + r % p.group;
+    const int64_t row = g.row0 + tok;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.out_stride + (int64_t)head * D + lane * E) * 2);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = T::pack(v[2 * e] * norm, v[2 * e + 1] * norm);
+    if (p.lse && lane == 0)
+      p.lse[row * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
+  }
+}
+
+// --------------------------------------------------------------------- host
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return fn && fn(m, dtype == TC_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+// SMs of a device (asked once).
+int sm_count(int device) {
+  static int known[kMaxDevices];  // (a race writes the same value)
+  if (device < 0 || device >= kMaxDevices) return 0;
+  if (!known[device]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[device] = n;
+  }
+  return known[device];
+}
+
+size_t workspace_bytes(int workers, int head_dim) {
+  return (size_t)workers * (sizeof(Seg) + 16) + part_rows(workers) * (sizeof(float2) + sizeof(float) * head_dim) + 64;
+}
+
+template <typename T, int D>
+cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q, cudaStream_t s) {
+  static bool ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)p.workers);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D>();
+  e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D>, p, kv, q);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(p.workers + (p.tok.batch + kJoinRows - 1) / kJoinRows), 8);
+  cfg.blockDim = dim3(kJoinRows * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p);
 }
 
 }  // namespace
@@ -109,7 +1207,9 @@ extern "C" tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes) {
   const tc_status rc = kv_check("tc_attend_workspace", kv);
   if (rc != TC_OK) return rc;
   if (!bytes) return kv_fail(TC_ERR_INVALID_ARG, "tc_attend_workspace: bytes is NULL");
-  *bytes = 16;
+  const int sms = sm_count(kv->device);
+  if (sms < 1) return kv_fail(TC_ERR_CUDA, "tc_attend_workspace: no such device");
+  *bytes = (int64_t)workspace_bytes(sms, kv->head_dim);
   return TC_OK;
 }
 
@@ -140,29 +1240,57 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
                    "a row");
   KvDevice dev(kv->device);
   if (!dev.ok) return kv_fail(TC_ERR_CUDA, "tc_attend: cannot use the cache's device");
-  AttendParams p;
-  p.kv = kv_view(kv, layer);
+  // Keys and values of the layer: [page][keys or values, head][slot][element].
+  const KvView v = kv_view(kv, layer);
+  const cuuint64_t d = (cuuint64_t)kv->head_dim, sz = (cuuint64_t)kv->page_size;
+  const cuuint64_t kv_dims[4] = {d, sz, (cuuint64_t)2 * kv->kv_heads, (cuuint64_t)kv->pages};
+  const cuuint64_t kv_strides[3] = {d * 2, sz * d * 2, (cuuint64_t)2 * kv->kv_heads * sz * d * 2};
+  const cuuint32_t kv_box[4] = {64, (cuuint32_t)kv->page_size, 1, 1};
+  const int group = a->q_heads / kv->kv_heads, tile_tokens = kTile / group;
+  // Queries: rows (token, head of the group) of one M tile, at most max_tokens of them.
+  const int q_tokens = a->max_tokens < 1 ? 1 : a->max_tokens < tile_tokens ? a->max_tokens : tile_tokens;
+  const bool none = tokens->n_tokens == 0;  // (no queries: the map is not used, any valid one does)
+  const cuuint64_t q_dims[3] = {d, (cuuint64_t)(none ? group : a->q_heads), (cuuint64_t)(none ? 1 : tokens->n_tokens)};
+  const cuuint64_t q_strides[2] = {d * 2, (cuuint64_t)(none ? row : a->q_stride) * 2};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)group, (cuuint32_t)q_tokens};
+  CUtensorMap map_kv, map_q;
+  if (!encode(&map_kv, kv->dtype, 4, v.base, kv_dims, kv_strides, kv_box) ||
+      !encode(&map_q, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, q_box))
+    return kv_fail(TC_ERR_UNSUPPORTED, "tc_attend: the sizes or strides do not fit a tensor map");
+  AttendParams p{};
+  p.kv = v;
   p.tok = tokens_view(tokens);
-  p.q = static_cast<const uint8_t*>(a->q);
-  p.q_stride = a->q_stride;
   p.q_heads = a->q_heads;
+  p.group = group;
+  p.tile_tokens = tile_tokens;
   p.max_tokens = a->max_tokens;
-  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.q_rows = group * q_tokens;
+  // A scale of zero weighs all slots alike; as a factor so small that every
+  // product with a score is nothing, it keeps -inf times the factor -inf.
+  p.c = fmaxf(fabsf(a->scale) * 1.4426950408889634f, 1e-30f);
+  p.negate = a->scale < 0.f;
   p.tree = a->tree;
   p.words = a->tree ? a->tree_words : 0;
   p.out = static_cast<uint8_t*>(a->out);
   p.out_stride = a->out_stride;
   p.lse = a->lse;
   p.status = status;
+  p.workers = sm_count(kv->device);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  ws += part_rows(p.workers) * sizeof(float) * kv->head_dim;
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += part_rows(p.workers) * sizeof(float2);
+  p.descs = reinterpret_cast<Seg*>(ws);
+  ws += (size_t)p.workers * sizeof(Seg);
+  p.errs = reinterpret_cast<int32_t*>(ws);
+  p.wait_limit = a->wait_polls > 0 ? a->wait_polls : kWaitLimit;
+  p.withhold = a->withhold;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)(((int64_t)tokens->n_tokens * a->q_heads + tokens->batch + 7) / 8);
-  if (kv->dtype == TC_DT_BF16) {
-    if (kv->head_dim == 128) attend_rows_kernel<Bf16, 128><<<grid, 256, 0, s>>>(p);
-    else attend_rows_kernel<Bf16, 64><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (kv->head_dim == 128) attend_rows_kernel<F16, 128><<<grid, 256, 0, s>>>(p);
-    else attend_rows_kernel<F16, 64><<<grid, 256, 0, s>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (kv->dtype == TC_DT_BF16)
+    e = kv->head_dim == 128 ? launch<Bf16, 128>(p, map_kv, map_q, s) : launch<Bf16, 64>(p, map_kv, map_q, s);
+  else
+    e = kv->head_dim == 128 ? launch<F16, 128>(p, map_kv, map_q, s) : launch<F16, 64>(p, map_kv, map_q, s);
   return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_attend");
 }

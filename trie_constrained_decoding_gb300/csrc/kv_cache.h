@@ -32,6 +32,8 @@ struct TokensView {
 
 // 16-bit element types: pairs to and from 32-bit floats.
 struct Bf16 {
+  static constexpr uint32_t kMma = 1;       // operand type of a tensor-core instruction
+  static constexpr uint32_t kExp = 0x7f80;  // exponent bits
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
@@ -42,6 +44,8 @@ struct Bf16 {
   }
 };
 struct F16 {
+  static constexpr uint32_t kMma = 0;
+  static constexpr uint32_t kExp = 0x7c00;
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
   }
