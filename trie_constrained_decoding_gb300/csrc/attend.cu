@@ -20,15 +20,18 @@
 //  - warp 0 loads: queries, then key and value tiles, into a ring of 128 x
 //    head_dim tiles by TMA (128-byte swizzle; one copy per page piece and 64
 //    columns; pages past the sequence's end are not loaded);
-//  - warp 1, one thread, issues the products on the tensor cores: S = Q K^T
-//    (both operands in shared memory) and O += P V with P in tensor memory;
+//  - warps 1 and 3, one thread each, issue the products of one softmax group on
+//    the tensor cores: S = Q K^T (both operands in shared memory) and O += P V
+//    with P in tensor memory;
 //  - warp 2 hands out the CTA's segments (an item's part) through a small ring;
 //  - warps 4-7 and 8-11 are two softmax groups, one row per thread: a thread
 //    reads its row of S from tensor memory, keeps the row's maximum and sum in
 //    32 bits, and writes the weights P over S in the cache's type.
 // The two groups always alternate with the tensor cores: with two M tiles each
 // takes one and both use every key-value tile; with one M tile they take the
-// even and the odd tiles of the cache and are joined at the end.
+// even and the odd tiles of the cache and are joined at the end.  Each group
+// has an issuer of its own, so that one group's wait for its weights does not
+// hold up the other's products.
 //
 // The maximum that the weights refer to is only moved when a row's maximum
 // has grown by more than 2^8 (the sums hold weights up to 2^8 in 32 bits, and
@@ -94,7 +97,7 @@ struct AttendParams {
   Seg* descs;        // [workers] item that starts in a worker and goes on in the next (valid = 0: none)
   int32_t* errs;     // [workers] a wait ran out
   float2* part_ml;   // [workers][2][256] maximum and sum of each row
-  float* part_o;     // [workers][2][256][D]
+  float* part_o;     // [workers][2][D / 4][256][4]
   long long wait_limit;
   int32_t withhold;  // test switch: the first worker's first load is not issued
 };
@@ -104,7 +107,7 @@ constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile
 struct Hdr {
   uint64_t full[10], empty[10];      // key-value ring
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_ready[2], pv_done[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_ready[2], pv_done[2], o_full[2];
   uint64_t o_free;                   // both groups have read the accumulators
   uint64_t meet;                     // both groups
   uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -135,6 +138,9 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -246,6 +252,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint64_t f2(float x, float y) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -277,22 +288,29 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 
 // ------------------------------------------------------------ the work's line
 
+// Division of non-negative 64-bit numbers that mostly fit 32 bits.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // sum over i < n of floor((a i + b) / m), in O(log m) steps (Euclid's scheme).
 __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t ans = 0;
   while (n > 0) {
     if (a >= m) {
-      ans += n * (n - 1) / 2 * (a / m);
-      a %= m;
+      const int64_t q = div64(a, m);
+      ans += n * (n - 1) / 2 * q;
+      a -= q * m;
     }
     if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
+      const int64_t q = div64(b, m);
+      ans += n * q;
+      b -= q * m;
     }
     const int64_t y = a * n + b;
     if (y < m) break;
-    n = y / m;
-    b = y % m;
+    n = div64(y, m);
+    b = y - n * m;
     const int64_t t = m;
     m = a;
     a = t;
@@ -312,13 +330,13 @@ struct Line {
   }
   // tiles of the items before item i
   __device__ int64_t before(int i) const {
-    if (!causal) return (int64_t)i * tiles(0);
+    if (!causal || i == 0) return (int64_t)i * tiles(0);
     return floor_sum(i, kTile, step, (int64_t)ctx + step + kTile - 1);
   }
   __device__ int64_t units() const { return n > 0 ? before(items() - 1) + tiles(items() - 1) : 0; }
   // the item that unit u is in
   __device__ int item_of(int64_t u) const {
-    if (!causal) return (int)(u / tiles(0));
+    if (!causal) return (int)div64(u, tiles(0));
     int lo = 0, hi = items();
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -337,9 +355,14 @@ __device__ __forceinline__ bool line_of(const AttendParams& p, int b, SeqSpan* s
   return ok;
 }
 
-__device__ __forceinline__ int64_t worker_start(const AttendParams& p, int64_t total, int active, int w) {
-  return total * w / active;
-}
+// The first unit of worker w: total * w / active, in two parts that need no
+// long division.
+struct Cut {
+  int64_t q;
+  uint32_t r, active;
+  __device__ Cut(int64_t total, int n) : q(n ? div64(total, n) : 0), r((uint32_t)(total - q * n)), active(n) {}
+  __device__ int64_t start(int w) const { return q * w + r * (uint32_t)w / active; }
+};
 
 // Which slots of a tile a row sees, 128 bits.
 __device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, int tok, int tile, uint32_t (&m)[4]) {
@@ -354,21 +377,42 @@ __device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, in
     return;
   }
   const uint32_t* row = reinterpret_cast<const uint32_t*>(p.tree) + (int64_t)(g.row0 + tok) * p.words * 2;
+  // The tile's first slot as a drafted token's number, and the row's words
+  // from the one that holds its bit: all ones before the first, none after the
+  // last.  Five loads that do not wait for one another.
+  const int x = start - g.ctx, first = x >> 5;
+  uint32_t v[5];
+#pragma unroll
+  for (int w = 0; w < 5; ++w) {
+    const int i = first + w;
+    v[w] = i < 0 ? 0xffffffffu : 0u;
+    if (i >= 0 && i < 2 * p.words) v[w] = __ldg(row + i);
+  }
+  const int left = g.ctx + g.n - start;  // slots of the tile that the sequence has
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const int x = start + 32 * w - g.ctx;  // drafted token of the word's first slot
-    uint32_t v;
-    if (x <= -32) {
-      v = 0xffffffffu;
-    } else {
-      const int i = x < 0 ? -1 : x >> 5;   // mask word that holds bit x (-1: the cached slots)
-      const uint32_t lo = i < 0 ? 0xffffffffu : i < 2 * p.words ? __ldg(row + i) : 0u;
-      const uint32_t hi = i + 1 < 2 * p.words ? __ldg(row + i + 1) : 0u;
-      v = __funnelshift_r(lo, hi, (uint32_t)x & 31u);
-    }
-    const int left = g.ctx + g.n - (start + 32 * w);  // slots of the word that the sequence has
-    m[w] = left <= 0 ? 0u : left >= 32 ? v : v & ((1u << left) - 1u);
+    const int k = left - 32 * w;
+    m[w] = __funnelshift_r(v[w], v[w + 1], (uint32_t)x & 31u) &
+           (k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u);
   }
+}
+
+// What the ring holds at place j of a segment of n tiles, in the order of use:
+// K0 V0 K1 V1 ... with two M tiles; K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1) with
+// one, whose tiles the groups take in turn.
+struct RingItem {
+  int tile;
+  bool value;
+};
+__device__ __forceinline__ RingItem ring_item(int j, int n, bool two) {
+  if (two) return {j >> 1, (j & 1) != 0};
+  if (j == 0) return {0, false};
+  if (j == 2 * n - 1) return {n - 1, true};
+  return (j & 1) ? RingItem{(j + 1) >> 1, false} : RingItem{(j >> 1) - 1, true};
+}
+// The place of tile i's values in it.
+__device__ __forceinline__ int value_place(int i, int n, bool two) {
+  return two ? 2 * i + 1 : i + 1 < n ? 2 * i + 2 : 2 * n - 1;
 }
 
 // The first slot of an item that some row of it does not see.
@@ -380,11 +424,46 @@ template <typename T>
 __device__ __forceinline__ bool finite2(uint32_t v) {
   return (v & T::kExp) != T::kExp && (v & (T::kExp << 16)) != (T::kExp << 16);
 }
-// One element of a pair: zero unless it is infinite or NaN.
+// A pair with zeros for what is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t only_finite(uint32_t v) {
+  if ((v & T::kExp) == T::kExp) v &= 0xffff0000u;
+  if ((v & (T::kExp << 16)) == (T::kExp << 16)) v &= 0x0000ffffu;
+  return v;
+}
+// What only_finite takes out.
 template <typename T>
 __device__ __forceinline__ float2 non_finite(uint32_t v) {
   const float2 f = T::unpack(v);
   return make_float2((v & T::kExp) == T::kExp ? f.x : 0.f, (v & (T::kExp << 16)) == (T::kExp << 16) ? f.y : 0.f);
+}
+
+// Adds to 32 columns of a row the infinities and NaN that were taken out of the
+// values of slots it sees (from the cache itself; rare).
+template <typename T, int D>
+__device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& g, const uint32_t* bad, int hidden,
+                                           int tok, int c, float (&v)[32]) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+#pragma unroll 1
+    for (uint32_t w = bad[i]; w; w &= w - 1) {
+      const int slot = hidden + i * 32 + __ffs(w) - 1, j = slot % kTile;
+      uint32_t mask[4];
+      row_mask(p, g, tok, slot / kTile, mask);
+      const uint32_t mw = j < 32 ? mask[0] : j < 64 ? mask[1] : j < 96 ? mask[2] : mask[3];
+      if (!((mw >> (j & 31)) & 1u)) continue;
+      const int page = __ldg(p.tok.table + (int64_t)g.seq * p.tok.width + (slot >> p.kv.page_shift));
+      if ((uint32_t)page >= (uint32_t)p.kv.pages) continue;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.kv.base + ((((int64_t)page * 2 + 1) * p.kv.kv_heads + g.head) * p.kv.page_size +
+                       (slot & (p.kv.page_size - 1))) * D * 2 + c * 2);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 x = non_finite<T>(__ldg(src + e));
+        v[2 * e] += x.x;
+        v[2 * e + 1] += x.y;
+      }
+    }
 }
 
 // ------------------------------------------------------------------- kernel
@@ -416,12 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(&hdr->full[i]), 1);
-      mbar_init(smem_u32(&hdr->empty[i]), 1);
+      mbar_init(smem_u32(&hdr->empty[i]), 2);    // both issuers (a commit each, or an arrival where it is not theirs)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&hdr->q_full[i]), 1);
-      mbar_init(smem_u32(&hdr->q_empty[i]), 1);
+      mbar_init(smem_u32(&hdr->q_empty[i]), 8);  // eight softmax warps (four of them twice)
       mbar_init(smem_u32(&hdr->s_full[i]), 1);
+      mbar_init(smem_u32(&hdr->p_half[i]), kTile);
       mbar_init(smem_u32(&hdr->p_ready[i]), kTile);
       mbar_init(smem_u32(&hdr->pv_done[i]), 1);
       mbar_init(smem_u32(&hdr->o_full[i]), 1);
@@ -430,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&hdr->meet), 2 * kTile);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(smem_u32(&hdr->seg_full[i]), 1);
-      mbar_init(smem_u32(&hdr->seg_empty[i]), 2 + 8);  // loader, issuer, eight softmax warps
+      mbar_init(smem_u32(&hdr->seg_empty[i]), 3 + 8);  // loader, issuers, eight softmax warps
     }
-    mbar_init(smem_u32(&hdr->drain), 1);
+    mbar_init(smem_u32(&hdr->drain), 2);
     hdr->abort = 0;
     hdr->seq0 = -1;
     for (int i = 0; i < 16; ++i) hdr->bad[i >> 3][i & 7] = 0u;
@@ -440,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_kv)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
   }
-  if (warp == 3) {
+  if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hdr->tmem_base)),
                  "r"(512)
                  : "memory");
@@ -477,8 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += hdr->scan[i];
   }
   const int active = (int)min((int64_t)p.workers, total);
-  const int64_t begin = worker < active ? worker_start(p, total, active, worker) : 0;
-  const int64_t end = worker < active ? worker_start(p, total, active, worker + 1) : 0;
+  const Cut cut(total, active);
+  const int64_t begin = worker < active ? cut.start(worker) : 0;
+  const int64_t end = worker < active ? cut.start(worker + 1) : 0;
   const int64_t excl = start_of_warp + incl - mine;
   if (begin < end && begin >= excl && begin < excl + mine) {
     int64_t at = excl;
@@ -501,7 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool held = p.withhold != 0 && worker == 0;
   uint32_t armed = 0;  // loader: key-value stages armed, for the exit path
   uint32_t q_armed = 0;
+  // Registers: 384 threads launch with 168 each, 64,512 together; a softmax
+  // thread holds a row of 128 scores and takes 200, the others keep 96
+  // (96 * 128 + 200 * 256 = 63,488).
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   if (warp == 0) {
     // ------------------------------------------------------------- loader
     uint32_t it = 0, qi = 0;
@@ -532,24 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = g.t1 - g.t0;
       const int slots = g.ctx + g.n;  // (a causal item reads less: its last tile ends there too)
       const int32_t* row = p.tok.table + (int64_t)g.seq * p.tok.width;
-      // Order of use: keys one tile ahead of the values with one M tile (the
-      // groups take turns), together with two.
       for (int j = 0; j < 2 * n && !stop; ++j, ++it) {
-        int tile, is_v;
-        if (g.two) {
-          tile = j >> 1;
-          is_v = j & 1;
-        } else if (j == 0) {
-          tile = 0;
-          is_v = 0;
-        } else if (j == 2 * n - 1) {
-          tile = n - 1;
-          is_v = 1;
-        } else {
-          is_v = (j & 1) ^ 1;              // K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1)
-          tile = is_v ? (j >> 1) - 1 : (j + 1) >> 1;
-        }
-        const int slot = (g.t0 + tile) * kTile + piece * box;
+        const RingItem x = ring_item(j, n, g.two);
+        const int slot = (g.t0 + x.tile) * kTile + piece * box;
         const bool load = piece < pieces && slot < slots;
         const int page = load ? __ldg(row + (slot >> p.kv.page_shift)) : 0;
         const int stage = (int)(it % NS);
@@ -563,134 +634,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (load && !(held && it == 0))
           tma_kv(kv_s + stage * C::kTileBytes + half * kHalfBytes + piece * box * 128, &map_kv, half * 64,
-                 slot & (p.kv.page_size - 1), is_v * p.kv.kv_heads + g.head, page, bar);
+                 slot & (p.kv.page_size - 1), (x.value ? p.kv.kv_heads : 0) + g.head, page, bar);
         ++armed;
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- issuer
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ issuers
     if (lane == 0) {
-      uint32_t it = 0, qi = 0, n_pr[2] = {0, 0}, n_pv[2] = {0, 0};
+      const int slot = warp >> 1;  // which group's products
+      const uint32_t t_s = tmem + slot * kTile, t_o = tmem + 2 * kTile + slot * 128;
+      uint32_t it = 0, qi = 0, n_pv = 0;
       constexpr uint32_t id_s = idesc<T>(kTile, false), id_o = idesc<T>(D, true);
       bool ok = true;
-      // S_slot = Q K^T from a ring stage
-      auto scores = [&](int slot, uint32_t q_buf, uint32_t stage) {
-        const uint32_t a = q_s + q_buf * C::kTileBytes, b = kv_s + stage * C::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (uint32_t)(k >> 2) * kHalfBytes + (uint32_t)(k & 3) * 32;
-          mma_ss(tmem + slot * kTile, desc_k_major(a + o), desc_k_major(b + o), id_s, k > 0);
-        }
-        mma_commit(smem_u32(&hdr->s_full[slot]));
-      };
-      // O_slot += P V
-      auto outputs = [&](int slot, uint32_t stage, bool first) {
-        const uint32_t b = kv_s + stage * C::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 2 * kTile + slot * 128, tmem + slot * kTile + k * 8, desc_n_major(b + k * 2048), id_o,
-                 !first || k > 0);
-        mma_commit(smem_u32(&hdr->pv_done[slot]));
-        ++n_pv[slot];
-      };
-      auto wait_kv = [&](uint32_t i) {
-        ok = ok && mbar_wait(smem_u32(&hdr->full[i % NS]), (i / NS) & 1, wl, abort);
-        tc_fence_after();
-        return ok;
-      };
-      auto wait_p = [&](int slot) {
-        ok = ok && mbar_wait(smem_u32(&hdr->p_ready[slot]), n_pr[slot] & 1, wl, abort);
-        ++n_pr[slot];
-        tc_fence_after();
-        return ok;
-      };
-      // the last P V of a slot has been done: its scores' place is free
-      auto wait_pv = [&](int slot) {
-        ok = ok && (n_pv[slot] == 0 ||
-                    mbar_wait(smem_u32(&hdr->pv_done[slot]), (n_pv[slot] - 1) & 1, wl, abort));
-        tc_fence_after();
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait(smem_u32(bar), parity & 1, wl, abort);
         return ok;
       };
       for (int k = 0; ok; ++k) {
-        if (!mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
+        if (!wait(&hdr->seg_full[k % kSegs], k / kSegs)) break;
         const Seg g = hdr->seg[k % kSegs];
         mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
         if (!g.valid) break;
         const int n = g.t1 - g.t0;
-        const uint32_t q0 = qi & 1, q1 = (qi + 1) & 1;
-        for (int m = 0; m <= g.two; ++m) {
-          const uint32_t x = qi + m;
-          ok = ok && mbar_wait(smem_u32(&hdr->q_full[x & 1]), (x >> 1) & 1, wl, abort);
-        }
-        if (!ok) break;
-        tc_fence_after();
+        // (both issuers look at every phase of every barrier they wait on, their
+        // own turn or not: a parity says nothing about a phase further back)
+        const uint32_t q = qi + (g.two ? slot : 0);
+        if (!wait(&hdr->q_full[qi & 1], qi >> 1)) break;
+        if (g.two && !wait(&hdr->q_full[(qi + 1) & 1], (qi + 1) >> 1)) break;
         qi += 1 + g.two;
-        // The accumulators of the segment before have been read (waited for
-        // just before the first P V: the scores may start earlier).
-        auto wait_o = [&]() {
-          ok = ok && (k == 0 || mbar_wait(smem_u32(&hdr->o_free), (uint32_t)(k - 1) & 1, wl, abort));
+        const uint64_t q_desc = desc_k_major(q_s + (q & 1) * C::kTileBytes);
+        // S = Q K^T.  The weights P of the group's tile before lie in the same
+        // place: its P V has to be done.
+        auto scores = [&](uint32_t stage) {
+          if (n_pv > 0 && !wait(&hdr->pv_done[slot], n_pv - 1)) return;
           tc_fence_after();
-          return ok;
+          const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes);
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t o = ((uint32_t)(e >> 2) * kHalfBytes + (uint32_t)(e & 3) * 32) >> 4;
+            mma_ss(t_s, q_desc + o, b + o, id_s, e > 0);
+          }
+          mma_commit(smem_u32(&hdr->s_full[slot]));
+          mma_commit(smem_u32(&hdr->empty[stage]));
         };
-        if (g.two) {
-          if (!wait_kv(it) || !wait_pv(0)) break;
-          scores(0, q0, it % NS);
-          if (!wait_pv(1)) break;
-          scores(1, q1, it % NS);
-          mma_commit(smem_u32(&hdr->empty[it % NS]));
-          if (n == 1) {
-            mma_commit(smem_u32(&hdr->q_empty[q0]));
-            mma_commit(smem_u32(&hdr->q_empty[q1]));
+        // O += P V, in two halves of the slots as their weights come.
+        auto outputs = [&](uint32_t stage, bool first) {
+          if (!wait(&hdr->p_half[slot], n_pv)) return;
+          tc_fence_after();
+          const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes);
+#pragma unroll
+          for (int e = 0; e < kTile / 32; ++e) mma_ts(t_o, t_s + e * 8, b + e * (2048 >> 4), id_o, !first || e > 0);
+          if (!wait(&hdr->p_ready[slot], n_pv)) return;
+          tc_fence_after();
+#pragma unroll
+          for (int e = kTile / 32; e < kTile / 16; ++e) mma_ts(t_o, t_s + e * 8, b + e * (2048 >> 4), id_o, 1);
+          mma_commit(smem_u32(&hdr->pv_done[slot]));
+          mma_commit(smem_u32(&hdr->empty[stage]));
+          ++n_pv;
+        };
+        bool first = true;  // no P V of this segment yet
+        for (int j = 0; j < 2 * n; ++j, ++it) {
+          const RingItem x = ring_item(j, n, g.two);
+          const uint32_t stage = it % NS;
+          if (!wait(&hdr->full[stage], it / NS)) break;
+          if (!g.two && (x.tile & 1) != slot) {
+            mbar_arrive(smem_u32(&hdr->empty[stage]));  // the other group's
+            continue;
           }
-          if (!wait_o()) break;
-          for (int i = 0; i < n; ++i) {
-            const uint32_t v = it + 2 * i + 1, kn = v + 1;
-            if (!wait_p(0) || !wait_kv(v)) break;
-            outputs(0, v % NS, i == 0);
-            if (!wait_p(1)) break;
-            outputs(1, v % NS, i == 0);
-            mma_commit(smem_u32(&hdr->empty[v % NS]));
-            if (i + 1 < n) {
-              if (!wait_kv(kn) || !wait_pv(0)) break;
-              scores(0, q0, kn % NS);
-              if (!wait_pv(1)) break;
-              scores(1, q1, kn % NS);
-              mma_commit(smem_u32(&hdr->empty[kn % NS]));
-              if (i + 2 == n) {
-                mma_commit(smem_u32(&hdr->q_empty[q0]));
-                mma_commit(smem_u32(&hdr->q_empty[q1]));
-              }
-            }
-          }
-          if (!ok) break;
-          mma_commit(smem_u32(&hdr->o_full[0]));
-          mma_commit(smem_u32(&hdr->o_full[1]));
-        } else {
-          // K0 K1 V0 K2 V1 ...: place of K(i) and V(i) in the ring
-          auto k_at = [&](int i) { return it + (i == 0 ? 0 : 2 * i - 1); };
-          auto v_at = [&](int i) { return it + (i + 1 < n ? 2 * i + 2 : 2 * n - 1); };
-          auto next_scores = [&](int i) {
-            if (!wait_kv(k_at(i)) || !wait_pv(i & 1)) return false;
-            scores(i & 1, q0, k_at(i) % NS);
-            mma_commit(smem_u32(&hdr->empty[k_at(i) % NS]));
-            if (i + 1 == n) mma_commit(smem_u32(&hdr->q_empty[q0]));
-            return true;
-          };
-          if (!next_scores(0)) break;
-          if (n > 1 && !next_scores(1)) break;
-          if (!wait_o()) break;
-          for (int i = 0; i < n; ++i) {
-            const int slot = i & 1;
-            if (!wait_p(slot) || !wait_kv(v_at(i))) break;
-            outputs(slot, v_at(i) % NS, i < 2);
-            mma_commit(smem_u32(&hdr->empty[v_at(i) % NS]));
-            if (i + 2 < n && !next_scores(i + 2)) break;
+          if (!x.value) {
+            scores(stage);
+          } else {
+            // (the accumulators of the segment before have been read)
+            if (first && k > 0 && !wait(&hdr->o_free, k - 1)) break;
+            outputs(stage, first);
+            first = false;
           }
           if (!ok) break;
-          mma_commit(smem_u32(&hdr->o_full[0]));
-          mma_commit(smem_u32(&hdr->o_full[1]));
         }
-        it += 2 * n;
+        if (first && k > 0) wait(&hdr->o_free, k - 1);
+        if (!ok) break;
+        mma_commit(smem_u32(&hdr->o_full[slot]));
       }
     }
     __syncwarp();
@@ -715,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++b;
           }
           if (b >= p.tok.batch) break;  // (cannot be: the units add up)
-          const int head = (int)(off / per);
-          int64_t r = off % per;
+          const int head = (int)div64(off, per);
+          int64_t r = off - head * per;
           int item = l.item_of(r);
           r -= l.before(item);
           // the rest of this sequence, segment by segment
@@ -740,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // the item's last unit lies with the worker that this finds
               const int64_t last_unit = end - left + tiles - 1;
               int w = worker + 1;
-              while (worker_start(p, total, active, w + 1) <= last_unit) ++w;
+              while (cut.start(w + 1) <= last_unit) ++w;
               g.last = w;
               d = g;
               open_end = true;
@@ -773,14 +796,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       p.descs[worker] = d;
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
     // ----------------------------------------------------- softmax groups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int grp = (warp - 4) >> 2;               // which slot
     const int r = tid - 128 - grp * kTile;         // row of the M tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + grp * kTile;
     const uint32_t t_o = tmem + lane_base + 2 * kTile;  // both accumulators
-    uint32_t n_s = 0, n_meet = 0, it = 0;
+    uint32_t n_s = 0, n_meet = 0, it = 0, qi = 0;
     auto meet = [&]() {
       mbar_arrive(smem_u32(&hdr->meet));
       const bool ok = mbar_wait(smem_u32(&hdr->meet), n_meet & 1, wl, abort);
@@ -836,8 +861,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
 #pragma unroll
-          for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int j = 4; j < kTile - 4; j += 2)
+            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          mx[0] = max3(mx[0], __uint_as_float(s[kTile - 4]), __uint_as_float(s[kTile - 3]));
+          mx[1] = max3(mx[1], __uint_as_float(s[kTile - 2]), __uint_as_float(s[kTile - 1]));
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           // Move the reference maximum only for a large growth (or the first
           // finite score); the accumulator exists from the second tile on.
           const bool first = i < (g.two ? 1 : 2);
@@ -874,6 +902,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[j] = T::pack(a, b);
             }
             tmem_st16(t_s + q * 16, pk);
+            if (q == 1 && !edge) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(smem_u32(&hdr->p_half[grp]));
+            }
           }
           const float2 t = unf2(add2(sum[0], sum[1]));
           l += t.x + t.y;
@@ -882,37 +915,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge) {
           // Values of slots that some row must not see: zero past the end of
           // the sequence, and infinities and NaN out (kept in `bad`).
-          const uint32_t vi = it + (g.two ? 2 * i + 1 : i + 1 < n ? 2 * i + 2 : 2 * n - 1);
+          const uint32_t vi = it + value_place(i, n, g.two);
           if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->full[vi % NS]), (vi / NS) & 1, wl, abort))) {
             stop = true;
             break;
           }
-          const int slot = tile * kTile + r;
+          // (with two M tiles each group takes half of the columns)
+          constexpr int CH = D / 8;  // 16-byte words of a row
+          const int slot = tile * kTile + r, ch0 = g.two ? grp * (CH / 2) : 0, ch1 = g.two ? ch0 + CH / 2 : CH;
           const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + r * 128;
-          // (with two M tiles each group looks at half of the rows)
-          if (slot >= hidden && (!g.two || r / 64 == grp)) {
+          if (slot >= g.ctx + g.n) {
+#pragma unroll 4
+            for (int c = ch0; c < ch1; ++c)
+              sts128(row + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+          } else if (slot >= hidden) {
             bool found = false;
 #pragma unroll 1
-            for (int h = 0; h < C::kHalves; ++h)
+            for (int c = ch0; c < ch1; c += 4) {
+              uint4 v[4];
 #pragma unroll
-              for (int ch = 0; ch < 8; ++ch) {
-                const uint32_t a = row + h * kHalfBytes + ((ch ^ (r & 7)) << 4);
-                if (slot >= g.ctx + g.n) {
-                  sts128(a, make_uint4(0u, 0u, 0u, 0u));
-                } else {
-                  uint4 v = lds128(a);
-                  if (!(finite2<T>(v.x) && finite2<T>(v.y) && finite2<T>(v.z) && finite2<T>(v.w))) {
-                    found = true;
+              for (int j = 0; j < 4; ++j)
+                v[j] = lds128(row + ((c + j) >> 3) * kHalfBytes + ((((c + j) ^ r) & 7) << 4));
+              bool fine = true;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                      uint32_t& x = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
-                      if ((x & T::kExp) == T::kExp) x &= 0xffff0000u;
-                      if ((x & (T::kExp << 16)) == (T::kExp << 16)) x &= 0x0000ffffu;
-                    }
-                    sts128(a, v);
-                  }
-                }
+              for (int j = 0; j < 4; ++j)
+                fine &= finite2<T>(v[j].x) && finite2<T>(v[j].y) && finite2<T>(v[j].z) && finite2<T>(v[j].w);
+              if (!fine) {
+                found = true;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  sts128(row + ((c + j) >> 3) * kHalfBytes + ((((c + j) ^ r) & 7) << 4),
+                         make_uint4(only_finite<T>(v[j].x), only_finite<T>(v[j].y), only_finite<T>(v[j].z),
+                                    only_finite<T>(v[j].w)));
               }
+            }
             if (found) {
               const int x = slot - hidden;  // (an item or a tree has at most 256 tokens: no row sees later ones)
               if (x < 256) atomicOr(&bad[x >> 5], 1u << (x & 31));
@@ -925,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
+        if (edge || !any) mbar_arrive(smem_u32(&hdr->p_half[grp]));
         mbar_arrive(smem_u32(&hdr->p_ready[grp]));
       }
       if (stop) break;
@@ -951,12 +988,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t any_bad = 0;
       for (int i = 0; i < 8; ++i) any_bad |= bad[i];
       const int head = g.head * p.group + r % p.group;
-      const int64_t out_row = (int64_t)(g.row0 + tok);
+      const int64_t out_at = ((int64_t)(g.row0 + tok) * p.out_stride + (int64_t)head * D) * 2;  // bytes
       const float norm = g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
-      const size_t part = g.part >= 0 ? ((size_t)worker * 2 + g.part) * 2 * kTile + (g.two ? grp * kTile : 0) + r : 0;
+      const int rr = (g.two ? grp * kTile : 0) + r;
+      const size_t part = ((size_t)worker * 2 + (g.part > 0)) * 2 * kTile;
+      // Columns: all of the group's own accumulator, or half of both.
+      const int c_lo = g.two ? 0 : grp * (D / 2), c_hi = g.two ? D : c_lo + D / 2;
+      // The item's query tile is done with: finished rows pass through its
+      // place, 16-byte words exclusive-ored with the row as in the swizzle.
+      const uint32_t q_buf = (qi + (g.two ? grp : 0)) & 1, stage = q_s + q_buf * C::kTileBytes;
       if (any) {
-        // columns: all of the group's own accumulator, or half of both
-        const int c_lo = g.two ? 0 : grp * (D / 2), c_hi = g.two ? D : c_lo + D / 2;
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
           uint32_t o[32];
@@ -978,56 +1019,53 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o[j]), f1, v[j]);
             }
           }
-          if (live) {
-            if (any_bad) {
-              // Infinities and NaN that were taken out, for the rows that see their slot.
-#pragma unroll 1
-              for (int i = 0; i < 8; ++i)
-#pragma unroll 1
-                for (uint32_t w = bad[i]; w; w &= w - 1) {
-                  const int slot = hidden + i * 32 + __ffs(w) - 1, tile = slot / kTile;
-                  uint32_t mask[4];
-                  row_mask(p, g, tok, tile, mask);
-                  const int j = slot % kTile;
-                  const uint32_t mw = j < 32 ? mask[0] : j < 64 ? mask[1] : j < 96 ? mask[2] : mask[3];
-                  if (!((mw >> (j & 31)) & 1u)) continue;
-                  const int page = __ldg(p.tok.table + (int64_t)g.seq * p.tok.width + (slot >> p.kv.page_shift));
-                  if ((uint32_t)page >= (uint32_t)p.kv.pages) continue;
-                  const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                      p.kv.base + ((((int64_t)page * 2 + 1) * p.kv.kv_heads + g.head) * p.kv.page_size +
-                                   (slot & (p.kv.page_size - 1))) * D * 2 + c * 2);
+          if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
+          if (g.part < 0) {
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const float2 x = non_finite<T>(__ldg(src + e));
-                    v[2 * e] += x.x;
-                    v[2 * e + 1] += x.y;
-                  }
-                }
-            }
-            if (g.part < 0) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + (out_row * p.out_stride + (int64_t)head * D + c) * 2);
+            for (int j = 0; j < 4; ++j)
+              sts128(stage + r * 128 + (c >> 6) * kHalfBytes + ((((c >> 3) + j) ^ r) & 7) * 16,
+                     make_uint4(T::pack(v[8 * j] * norm, v[8 * j + 1] * norm),
+                                T::pack(v[8 * j + 2] * norm, v[8 * j + 3] * norm),
+                                T::pack(v[8 * j + 4] * norm, v[8 * j + 5] * norm),
+                                T::pack(v[8 * j + 6] * norm, v[8 * j + 7] * norm)));
+          } else if (live) {
+            // (a warp's rows are neighbours: 512 bytes at a time)
+            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D) + (size_t)(c / 4) * (2 * kTile) + rr;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                dst[j] = make_uint4(T::pack(v[8 * j] * norm, v[8 * j + 1] * norm),
-                                    T::pack(v[8 * j + 2] * norm, v[8 * j + 3] * norm),
-                                    T::pack(v[8 * j + 4] * norm, v[8 * j + 5] * norm),
-                                    T::pack(v[8 * j + 6] * norm, v[8 * j + 7] * norm));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            }
+            for (int j = 0; j < 8; ++j)
+              dst[j * 2 * kTile] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
         }
-        if (live && (g.two || grp == 0)) {
-          if (g.part >= 0)
-            p.part_ml[part] = make_float2(m, l);
-          else if (p.lse)
-            p.lse[out_row * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
-        }
       }
+      // The accumulators have been read.
       tc_fence_before();
       mbar_arrive(smem_u32(&hdr->o_free));
+      if (any) {
+        if (live && (g.two || grp == 0)) {
+          if (g.part >= 0)
+            p.part_ml[part + rr] = make_float2(m, l);
+          else if (p.lse)
+            p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
+        }
+        if (g.part < 0) {
+          // The warp's 32 rows, 16 bytes a lane: neighbouring lanes write neighbouring words of a row.
+          __syncwarp();
+          const int words = (c_hi - c_lo) / 8;  // 4, 8 or 16 of a row
+          const int64_t mine = live ? out_at : -1;
+          for (int i = lane; i < 32 * words; i += 32) {
+            const int row = i / words, w = c_lo / 8 + i % words;
+            const int64_t at = __shfl_sync(0xffffffffu, mine, row);
+            const int rw = (warp & 3) * 32 + row;
+            if (at >= 0)
+              *reinterpret_cast<uint4*>(p.out + at + w * 16) =
+                  lds128(stage + rw * 128 + (w >> 3) * kHalfBytes + ((w ^ rw) & 7) * 16);
+          }
+        }
+      }
+      qi += 1 + g.two;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the loader writes the place next)
+      __syncwarp();
+      if (lane == 0) mbar_arrive_n(smem_u32(&hdr->q_empty[q_buf]), g.two ? 2 : 1);
       if (!meet()) break;
     }
   }
@@ -1038,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A wait ran out.  Everything this CTA started has to end before it
     // leaves (waits bounded again): the products that were issued, and the
     // loads of stages that no product has consumed.
-    if (warp == 1 && lane == 0) {
+    if ((warp == 1 || warp == 3) && lane == 0) {
       mma_commit(smem_u32(&hdr->drain));
       int32_t none = 0;
       mbar_wait(smem_u32(&hdr->drain), 0u, wl, &none);
@@ -1054,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) p.errs[worker] = hdr->abort;
   __syncthreads();
-  if (warp == 3) {
+  if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
@@ -1062,19 +1100,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------ joining kernel
 
-constexpr int kJoinRows = 8;  // rows of an item joined by one block at a time (a warp each)
+constexpr int kJoinThreads = 256, kJoinBlocks = 8;
 
 // Blocks (w, y), w < workers: the item that starts in worker w and goes on in
-// the next; its rows y * 8 + warp, y * 8 + warp + 8 * gridDim.y, ...  The parts
-// are added in the order of the workers: the result does not depend on timing.
-// Blocks past the workers write the status of eight sequences each.
+// the next.  A thread joins four columns of a row (the parts are laid out by
+// columns, so neighbouring rows are neighbours); the parts are added in the
+// order of the workers: the result does not depend on timing.  Blocks past the
+// workers write the status of eight sequences each.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinRows * 32) attend_join_kernel(const AttendParams p) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x >= (unsigned)p.workers) {
-    const int b = (blockIdx.x - p.workers) * kJoinRows + warp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = (blockIdx.x - p.workers) * (kJoinThreads / 32) + warp;
     if (blockIdx.y != 0 || b >= p.tok.batch) return;
     SeqSpan s;
     bool ok = seq_span(p.tok, p.kv.page_size, b, &s) && s.n <= p.max_tokens;
@@ -1088,36 +1126,37 @@ __global__ void __launch_bounds__(kJoinRows * 32) attend_join_kernel(const Atten
     if (lane == 0) p.status[b] = late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS;
     return;
   }
-  const Seg g = p.descs[blockIdx.x];
+  const int w0 = blockIdx.x;
+  const Seg g = p.descs[w0];
   if (!g.valid) return;
-  const int rows = (g.two ? 2 : 1) * kTile;
-  for (int rr = blockIdx.y * kJoinRows + warp; rr < rows; rr += gridDim.y * kJoinRows) {
-    const int r = rr % kTile, tok = g.tok0 + rr / kTile * p.tile_tokens + r / p.group;
-    if (r >= p.tile_tokens * p.group || tok >= g.n) continue;
-    auto at = [&](int w) { return ((size_t)w * 2 + (w == (int)blockIdx.x)) * 2 * kTile + rr; };
+  const int full = p.tile_tokens * p.group, left = (g.n - g.tok0) * p.group;
+  const int v0 = min(left, full), rows = g.two ? min(left, 2 * full) : v0;  // rows of the first M tile, of both
+  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * (D / 4); i += kJoinBlocks * kJoinThreads) {
+    const int c = i / rows, k = i % rows;            // columns 4 c .. 4 c + 3 of row k
+    const int rr = k < v0 ? k : kTile + k - v0;      // its place in a part
+    auto at = [&](int w) { return ((size_t)w * 2 + (w == w0)) * 2 * kTile; };
     float m = -INFINITY;
-    for (int w = blockIdx.x + lane; w <= g.last; w += 32) m = fmaxf(m, p.part_ml[at(w)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 4
-    for (int w = blockIdx.x; w <= g.last; ++w) {
-      const float2 ml = p.part_ml[at(w)];
+    for (int w = w0; w <= g.last; ++w) m = fmaxf(m, __ldcg(&p.part_ml[at(w) + rr].x));
+    float l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int w = w0; w <= g.last; ++w) {
+      const float2 ml = __ldcg(p.part_ml + at(w) + rr);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(w) * D) + (size_t)c * (2 * kTile) + rr);
       const float f = m == -INFINITY ? 0.f : ex2((ml.x - m) * p.c);
-      const float* src = p.part_o + at(w) * D + lane * E;
       l = fmaf(ml.y, f, l);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = fmaf(src[e], f, v[e]);
+      v.x = fmaf(o.x, f, v.x);
+      v.y = fmaf(o.y, f, v.y);
+      v.z = fmaf(o.z, f, v.z);
+      v.w = fmaf(o.w, f, v.w);
     }
     const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    const int head = g.head * p.group + r % p.group;
+    const int tok = g.tok0 + k / p.group, head = g.head * p.group + k % p.group;
     const int64_t row = g.row0 + tok;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.out_stride + (int64_t)head * D + lane * E) * 2);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = T::pack(v[2 * e] * norm, v[2 * e + 1] * norm);
-    if (p.lse && lane == 0)
+    *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + (int64_t)head * D + 4 * c) * 2) =
+        make_uint2(T::pack(v.x * norm, v.y * norm), T::pack(v.z * norm, v.w * norm));
+    if (p.lse && c == 0)
       p.lse[row * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
   }
 }
@@ -1192,8 +1231,9 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorM
   cfg.dynamicSmemBytes = smem_bytes<D>();
   e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D>, p, kv, q);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(p.workers + (p.tok.batch + kJoinRows - 1) / kJoinRows), 8);
-  cfg.blockDim = dim3(kJoinRows * 32);
+  constexpr int per = kJoinThreads / 32;
+  cfg.gridDim = dim3((unsigned)(p.workers + (p.tok.batch + per - 1) / per), kJoinBlocks);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p);
 }
