@@ -22,16 +22,25 @@
 //    columns; pages past the sequence's end are not loaded);
 //  - warps 1 and 3, one thread each, issue the products of one softmax group on
 //    the tensor cores: S = Q K^T (both operands in shared memory) and O += P V
-//    with P in tensor memory;
+//    with P in tensor memory, in steps of 64 slots (head_dim 128) or 128 (64);
 //  - warp 2 hands out the CTA's segments (an item's part) through a small ring;
 //  - warps 4-7 and 8-11 are two softmax groups, one row per thread: a thread
 //    reads its row of S from tensor memory, keeps the row's maximum and sum in
-//    32 bits, and writes the weights P over S in the cache's type.
+//    32 bits, and writes the weights P beside it in the cache's type.
 // The two groups always alternate with the tensor cores: with two M tiles each
 // takes one and both use every key-value tile; with one M tile they take the
 // even and the odd tiles of the cache and are joined at the end.  Each group
 // has an issuer of its own, so that one group's wait for its weights does not
 // hold up the other's products.
+//
+// Tensor memory, 512 columns of 32 bits: each group has its scores S, its
+// weights P and its accumulator O, 64 + 32 + 128 columns (head_dim 128) or
+// 128 + 64 + 64 (64).  S and P are apart, so that the next step's scores are
+// computed while the group works on this one's weights; with both in one place
+// (steps of 128 slots) a step is one chain of products and softmax.  At
+// head_dim 128 that leaves steps of 64 slots, whose scores read 6 KB of shared
+// memory for 32 cycles of products and take 50; beside the other product,
+// which reads less, a step takes 576 cycles instead of 512 (measured).
 //
 // The maximum that the weights refer to is only moved when a row's maximum
 // has grown by more than 2^8 (the sums hold weights up to 2^8 in 32 bits, and
@@ -66,6 +75,11 @@ struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
   static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kStep = D == 128 ? 64 : 128;  // slots of a step
+  static constexpr int kSteps = kTile / kStep;       // steps of a tile
+  // Tensor memory of a group: scores, weights, accumulator.
+  static constexpr uint32_t kP = kStep, kO = kP + kStep / 2, kCols = 256;
+  static_assert(kO + D <= kCols, "tensor memory of a group");
 };
 
 // A CTA's part of an item.
@@ -74,6 +88,7 @@ struct Seg {
   int32_t seq, row0, n, ctx, head;
   int32_t tok0;      // the item's first token
   int32_t t0, t1;    // its key-value tiles [t0, t1)
+  int32_t end;       // no row of the item sees this slot or a later one
   int32_t two;       // two M tiles
   int32_t part;      // -1: the whole item; else the slot of the partial result
   int32_t last;      // (slot 1) the last worker that has a part of the item
@@ -107,7 +122,7 @@ constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile
 struct Hdr {
   uint64_t full[10], empty[10];      // key-value ring
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_half[2], p_ready[2], pv_done[2], o_full[2];
+  uint64_t s_full[2], s_read[2], p_ready[2], pv_done[2], o_full[2];
   uint64_t o_free;                   // both groups have read the accumulators
   uint64_t meet;                     // both groups
   uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -144,6 +159,15 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
 }
 // Waits for a phase, at most `limit` polls; false if it gave up or another
 // wait of the CTA has.
@@ -364,60 +388,42 @@ struct Cut {
   __device__ int64_t start(int w) const { return q * w + r * (uint32_t)w / active; }
 };
 
-// Which slots of a tile a row sees, 128 bits.
-__device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, int tok, int tile, uint32_t (&m)[4]) {
-  const int start = tile * kTile;
-  if (!p.tree) {
-    const int lim = g.ctx + tok + 1 - start;  // slots seen
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int k = lim - 32 * w;
-      m[w] = k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
-    }
-    return;
-  }
-  const uint32_t* row = reinterpret_cast<const uint32_t*>(p.tree) + (int64_t)(g.row0 + tok) * p.words * 2;
-  // The tile's first slot as a drafted token's number, and the row's words
-  // from the one that holds its bit: all ones before the first, none after the
-  // last.  Five loads that do not wait for one another.
+// Which of the 32 NW slots from `start` a row sees.
+template <int NW>
+__device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, int tok, int start, uint32_t (&m)[NW]) {
+  int left = g.end - start;  // slots from `start` that any row sees
+  if (!p.tree) left = g.ctx + tok + 1 - start;
+  uint32_t v[NW + 1];
+  // The first slot as a drafted token's number, and the row's words from the
+  // one that holds its bit: all ones before the first, none after the last.
+  // The loads do not wait for one another.
   const int x = start - g.ctx, first = x >> 5;
-  uint32_t v[5];
+  if (p.tree) {
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(p.tree) + (int64_t)(g.row0 + tok) * p.words * 2;
 #pragma unroll
-  for (int w = 0; w < 5; ++w) {
-    const int i = first + w;
-    v[w] = i < 0 ? 0xffffffffu : 0u;
-    if (i >= 0 && i < 2 * p.words) v[w] = __ldg(row + i);
+    for (int w = 0; w <= NW; ++w) {
+      const int i = first + w;
+      v[w] = i < 0 ? 0xffffffffu : 0u;
+      if (i >= 0 && i < 2 * p.words) v[w] = __ldg(row + i);
+    }
   }
-  const int left = g.ctx + g.n - start;  // slots of the tile that the sequence has
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NW; ++w) {
     const int k = left - 32 * w;
-    m[w] = __funnelshift_r(v[w], v[w + 1], (uint32_t)x & 31u) &
-           (k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+    m[w] = k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
+    if (p.tree) m[w] &= __funnelshift_r(v[w], v[w + 1], (uint32_t)x & 31u);
   }
-}
-
-// What the ring holds at place j of a segment of n tiles, in the order of use:
-// K0 V0 K1 V1 ... with two M tiles; K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1) with
-// one, whose tiles the groups take in turn.
-struct RingItem {
-  int tile;
-  bool value;
-};
-__device__ __forceinline__ RingItem ring_item(int j, int n, bool two) {
-  if (two) return {j >> 1, (j & 1) != 0};
-  if (j == 0) return {0, false};
-  if (j == 2 * n - 1) return {n - 1, true};
-  return (j & 1) ? RingItem{(j + 1) >> 1, false} : RingItem{(j >> 1) - 1, true};
-}
-// The place of tile i's values in it.
-__device__ __forceinline__ int value_place(int i, int n, bool two) {
-  return two ? 2 * i + 1 : i + 1 < n ? 2 * i + 2 : 2 * n - 1;
 }
 
 // The first slot of an item that some row of it does not see.
 __device__ __forceinline__ int first_hidden(const AttendParams& p, const Seg& g) {
   return p.tree ? g.ctx : g.ctx + g.tok0 + 1;
+}
+
+// Steps of a tile (the last one of an item may end in its first half).
+template <int D>
+__device__ __forceinline__ int steps_of(const Seg& g, int tile) {
+  return min(Cfg<D>::kSteps, (g.end - tile * kTile + Cfg<D>::kStep - 1) / Cfg<D>::kStep);
 }
 
 template <typename T>
@@ -447,11 +453,10 @@ __device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& 
   for (int i = 0; i < 8; ++i)
 #pragma unroll 1
     for (uint32_t w = bad[i]; w; w &= w - 1) {
-      const int slot = hidden + i * 32 + __ffs(w) - 1, j = slot % kTile;
-      uint32_t mask[4];
-      row_mask(p, g, tok, slot / kTile, mask);
-      const uint32_t mw = j < 32 ? mask[0] : j < 64 ? mask[1] : j < 96 ? mask[2] : mask[3];
-      if (!((mw >> (j & 31)) & 1u)) continue;
+      const int slot = hidden + i * 32 + __ffs(w) - 1;
+      uint32_t mask[1];
+      row_mask<1>(p, g, tok, slot, mask);
+      if (!(mask[0] & 1u)) continue;
       const int page = __ldg(p.tok.table + (int64_t)g.seq * p.tok.width + (slot >> p.kv.page_shift));
       if ((uint32_t)page >= (uint32_t)p.kv.pages) continue;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
@@ -464,6 +469,19 @@ __device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& 
         v[2 * e + 1] += x.y;
       }
     }
+}
+
+// Writes a warp's 32 finished rows, WORDS 16-byte words of each from word `w0`,
+// from shared memory to byte `at` of the output (< 0: not a row).
+template <int WORDS>
+__device__ __forceinline__ void flush_rows(uint8_t* out, uint32_t stage, int row0, int w0, int64_t at, int lane) {
+#pragma unroll 4
+  for (int i = 0; i < WORDS; ++i) {
+    const int row = (i * 32 + lane) / WORDS, w = w0 + lane % WORDS, rw = row0 + row;
+    const int64_t a = __shfl_sync(0xffffffffu, at, row);
+    const uint4 v = lds128(stage + rw * 128 + (w >> 3) * kHalfBytes + ((w ^ rw) & 7) * 16);
+    if (a >= 0) *reinterpret_cast<uint4*>(out + a + w * 16) = v;
+  }
 }
 
 // ------------------------------------------------------------------- kernel
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&hdr->q_full[i]), 1);
       mbar_init(smem_u32(&hdr->q_empty[i]), 8);  // eight softmax warps (four of them twice)
       mbar_init(smem_u32(&hdr->s_full[i]), 1);
-      mbar_init(smem_u32(&hdr->p_half[i]), kTile);
+      mbar_init(smem_u32(&hdr->s_read[i]), kTile);
       mbar_init(smem_u32(&hdr->p_ready[i]), kTile);
       mbar_init(smem_u32(&hdr->pv_done[i]), 1);
       mbar_init(smem_u32(&hdr->o_full[i]), 1);
@@ -583,9 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t armed = 0;  // loader: key-value stages armed, for the exit path
   uint32_t q_armed = 0;
   // Registers: 384 threads launch with 168 each, 64,512 together; a softmax
-  // thread holds a row of 128 scores and takes 200, the others keep 96
-  // (96 * 128 + 200 * 256 = 63,488).
-
+  // thread holds a step's row of scores (128 at head_dim 64) and takes 200, the
+  // others keep 96 (96 * 128 + 200 * 256 = 63,488).
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   if (warp == 0) {
@@ -616,12 +633,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (stop) break;
       const int n = g.t1 - g.t0;
-      const int slots = g.ctx + g.n;  // (a causal item reads less: its last tile ends there too)
       const int32_t* row = p.tok.table + (int64_t)g.seq * p.tok.width;
       for (int j = 0; j < 2 * n && !stop; ++j, ++it) {
-        const RingItem x = ring_item(j, n, g.two);
-        const int slot = (g.t0 + x.tile) * kTile + piece * box;
-        const bool load = piece < pieces && slot < slots;
+        const int slot = (g.t0 + (j >> 1)) * kTile + piece * box;  // K0 V0 K1 V1 ...
+        const bool load = piece < pieces && slot < g.end;
         const int page = load ? __ldg(row + (slot >> p.kv.page_shift)) : 0;
         const int stage = (int)(it % NS);
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->empty[stage]), ((it / NS) & 1) ^ 1, wl, abort))) {
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (load && !(held && it == 0))
           tma_kv(kv_s + stage * C::kTileBytes + half * kHalfBytes + piece * box * 128, &map_kv, half * 64,
-                 slot & (p.kv.page_size - 1), (x.value ? p.kv.kv_heads : 0) + g.head, page, bar);
+                 slot & (p.kv.page_size - 1), ((j & 1) ? p.kv.kv_heads : 0) + g.head, page, bar);
         ++armed;
       }
     }
@@ -642,9 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ issuers
     if (lane == 0) {
       const int slot = warp >> 1;  // which group's products
-      const uint32_t t_s = tmem + slot * kTile, t_o = tmem + 2 * kTile + slot * 128;
-      uint32_t it = 0, qi = 0, n_pv = 0;
-      constexpr uint32_t id_s = idesc<T>(kTile, false), id_o = idesc<T>(D, true);
+      const uint32_t t_s = tmem + slot * C::kCols, t_p = t_s + C::kP, t_o = t_s + C::kO;
+      constexpr uint32_t id_s = idesc<T>(C::kStep, false), id_o = idesc<T>(D, true);
+      // Ring places looked at, query tiles, score and output products issued.
+      // Every phase of a barrier that this thread waits on is looked at in
+      // order, its own turn or not: a parity says nothing about a phase
+      // further back.
+      uint32_t seen = 0, qi = 0, n_s = 0, n_o = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && mbar_wait(smem_u32(bar), parity & 1, wl, abort);
@@ -655,64 +674,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Seg g = hdr->seg[k % kSegs];
         mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
         if (!g.valid) break;
-        const int n = g.t1 - g.t0;
-        // (both issuers look at every phase of every barrier they wait on, their
-        // own turn or not: a parity says nothing about a phase further back)
+        const int n = g.t1 - g.t0, hop = g.two ? 1 : 2;
         const uint32_t q = qi + (g.two ? slot : 0);
         if (!wait(&hdr->q_full[qi & 1], qi >> 1)) break;
         if (g.two && !wait(&hdr->q_full[(qi + 1) & 1], (qi + 1) >> 1)) break;
         qi += 1 + g.two;
         const uint64_t q_desc = desc_k_major(q_s + (q & 1) * C::kTileBytes);
-        // S = Q K^T.  The weights P of the group's tile before lie in the same
-        // place: its P V has to be done.
-        auto scores = [&](uint32_t stage) {
-          if (n_pv > 0 && !wait(&hdr->pv_done[slot], n_pv - 1)) return;
-          tc_fence_after();
-          const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes);
-#pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            const uint32_t o = ((uint32_t)(e >> 2) * kHalfBytes + (uint32_t)(e & 3) * 32) >> 4;
-            mma_ss(t_s, q_desc + o, b + o, id_s, e > 0);
+        const uint32_t at0 = seen, at1 = seen + 2 * n;  // the segment's ring places
+        // The next score product and the next output product: tile, step of
+        // the tile, steps of the tile.  Whichever can go goes.
+        const int i0 = g.two ? 0 : slot;
+        int is = i0, us = 0, io = i0, uo = 0;
+        int steps_s = is < n ? steps_of<D>(g, g.t0 + is) : 0, steps_o = steps_s;
+        bool o_free = k == 0;
+        long long idle = 0;
+        while (io < n || seen < at1) {
+          bool moved = false;
+          if (seen < at1 && mbar_test(smem_u32(&hdr->full[seen % NS]), (seen / NS) & 1)) {
+            // (the other group's tile: nothing of it is needed here)
+            if (!g.two && (((seen - at0) >> 1) & 1) != (uint32_t)slot) mbar_arrive(smem_u32(&hdr->empty[seen % NS]));
+            ++seen;
+            moved = true;
           }
-          mma_commit(smem_u32(&hdr->s_full[slot]));
-          mma_commit(smem_u32(&hdr->empty[stage]));
-        };
-        // O += P V, in two halves of the slots as their weights come.
-        auto outputs = [&](uint32_t stage, bool first) {
-          if (!wait(&hdr->p_half[slot], n_pv)) return;
-          tc_fence_after();
-          const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes);
+          if (is < n && at0 + 2 * is < seen &&
+              (n_s == 0 || mbar_test(smem_u32(&hdr->s_read[slot]), (n_s - 1) & 1))) {
+            // S = Q K^T: the scores before have been read.
+            const uint32_t stage = (at0 + 2 * is) % NS;
+            const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + us * (C::kStep * 128));
+            tc_fence_after();
 #pragma unroll
-          for (int e = 0; e < kTile / 32; ++e) mma_ts(t_o, t_s + e * 8, b + e * (2048 >> 4), id_o, !first || e > 0);
-          if (!wait(&hdr->p_ready[slot], n_pv)) return;
-          tc_fence_after();
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t o = ((uint32_t)(e >> 2) * kHalfBytes + (uint32_t)(e & 3) * 32) >> 4;
+              mma_ss(t_s, q_desc + o, b + o, id_s, e > 0);
+            }
+            mma_commit(smem_u32(&hdr->s_full[slot]));
+            ++n_s;
+            if (++us == steps_s) {
+              mma_commit(smem_u32(&hdr->empty[stage]));
+              us = 0;
+              is += hop;
+              if (is < n) steps_s = steps_of<D>(g, g.t0 + is);
+            }
+            moved = true;
+          }
+          if (io < n && at0 + 2 * io + 1 < seen) {
+            // O += P V.  The accumulators of the segment before have been read.
+            if (!o_free) o_free = mbar_test(smem_u32(&hdr->o_free), (uint32_t)(k - 1) & 1);
+            if (o_free && mbar_test(smem_u32(&hdr->p_ready[slot]), n_o & 1)) {
+              const uint32_t stage = (at0 + 2 * io + 1) % NS;
+              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + uo * (C::kStep * 128));
+              const bool first = io == i0 && uo == 0;
+              tc_fence_after();
 #pragma unroll
-          for (int e = kTile / 32; e < kTile / 16; ++e) mma_ts(t_o, t_s + e * 8, b + e * (2048 >> 4), id_o, 1);
-          mma_commit(smem_u32(&hdr->pv_done[slot]));
-          mma_commit(smem_u32(&hdr->empty[stage]));
-          ++n_pv;
-        };
-        bool first = true;  // no P V of this segment yet
-        for (int j = 0; j < 2 * n; ++j, ++it) {
-          const RingItem x = ring_item(j, n, g.two);
-          const uint32_t stage = it % NS;
-          if (!wait(&hdr->full[stage], it / NS)) break;
-          if (!g.two && (x.tile & 1) != slot) {
-            mbar_arrive(smem_u32(&hdr->empty[stage]));  // the other group's
-            continue;
+              for (int e = 0; e < C::kStep / 16; ++e)
+                mma_ts(t_o, t_p + e * 8, b + e * (2048 >> 4), id_o, !first || e > 0);
+              mma_commit(smem_u32(&hdr->pv_done[slot]));
+              ++n_o;
+              if (++uo == steps_o) {
+                mma_commit(smem_u32(&hdr->empty[stage]));
+                uo = 0;
+                io += hop;
+                if (io < n) steps_o = steps_of<D>(g, g.t0 + io);
+              }
+              moved = true;
+            }
           }
-          if (!x.value) {
-            scores(stage);
-          } else {
-            // (the accumulators of the segment before have been read)
-            if (first && k > 0 && !wait(&hdr->o_free, k - 1)) break;
-            outputs(stage, first);
-            first = false;
+          if (moved) {
+            idle = 0;
+          } else if (++idle > wl || ((idle & 63) == 0 && *abort)) {
+            *abort = 1;
+            ok = false;
+            break;
           }
-          if (!ok) break;
         }
-        if (first && k > 0) wait(&hdr->o_free, k - 1);
-        if (!ok) break;
+        if (!ok || (!o_free && !wait(&hdr->o_free, k - 1))) break;
         mma_commit(smem_u32(&hdr->o_full[slot]));
       }
     }
@@ -757,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             g.t0 = (int)r;
             g.t1 = (int)(r + take);
             g.two = s.n - g.tok0 > p.tile_tokens;
+            g.end = s.ctx + (p.tree ? s.n : min(s.n, g.tok0 + l.step));
             g.part = take == tiles ? -1 : r > 0 ? 0 : 1;
             g.last = worker;
             if (g.part == 1) {
@@ -803,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grp = (warp - 4) >> 2;               // which slot
     const int r = tid - 128 - grp * kTile;         // row of the M tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + grp * kTile;
-    const uint32_t t_o = tmem + lane_base + 2 * kTile;  // both accumulators
+    const uint32_t t_s = tmem + lane_base + grp * C::kCols;
+    const uint32_t t_p = t_s + C::kP, t_o = t_s + C::kO, t_o0 = tmem + lane_base + C::kO;
     uint32_t n_s = 0, n_meet = 0, it = 0, qi = 0;
     auto meet = [&]() {
       mbar_arrive(smem_u32(&hdr->meet));
@@ -826,143 +862,144 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t* bad = hdr->bad[k & 1];
       float m = -INFINITY, l = 0.f;
       bool stop = false;
-      for (int i = g.two ? 0 : grp; i < n; i += g.two ? 1 : 2) {
-        const int tile = g.t0 + i;
-        const bool edge = (tile + 1) * kTile > hidden;
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort))) {
-          stop = true;
-          break;
-        }
-        ++n_s;
-        tc_fence_after();
-        if (any) {
-          uint32_t s[kTile];
-          tmem_ld32(t_s, s);
-          tmem_ld32(t_s + 32, s + 32);
-          tmem_ld32(t_s + 64, s + 64);
-          tmem_ld32(t_s + 96, s + 96);
-          tmem_ld_wait();
-          tmem_arrived(s);
-          tmem_arrived(s + 32);
-          tmem_arrived(s + 64);
-          tmem_arrived(s + 96);
-          if (p.negate) {
+      bool first = true;
+      for (int i = g.two ? 0 : grp; i < n && !stop; i += g.two ? 1 : 2) {
+        const int steps = steps_of<D>(g, g.t0 + i);
+        for (int u = 0; u < steps; ++u, ++n_s, first = false) {
+          constexpr int W = C::kStep;
+          const int start = (g.t0 + i) * kTile + u * W;  // the step's first slot
+          const bool edge = start + W > hidden;
+          uint32_t mask[W / 32];
+          if (edge && live) row_mask<W / 32>(p, g, tok, start, mask);
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort))) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          uint32_t s[W];
+          if (any) {
 #pragma unroll
-            for (int j = 0; j < kTile; ++j) s[j] ^= 0x80000000u;
+            for (int c = 0; c < W; c += 32) tmem_ld32(t_s + c, s + c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < W; c += 32) tmem_arrived(s + c);
+          }
+          tc_fence_before();
+          mbar_arrive(smem_u32(&hdr->s_read[grp]));
+          float top = -INFINITY;
+          if (any) {
+            if (p.negate) {
+#pragma unroll
+              for (int j = 0; j < W; ++j) s[j] ^= 0x80000000u;
+            }
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < W; ++j) s[j] = live && (mask[j >> 5] >> (j & 31)) & 1u ? s[j] : 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
+#pragma unroll
+            for (int j = 4; j < W; j += 2)
+              mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          }
+          // The P V of the step before is done: its weights' place is free and
+          // the accumulator at rest.
+          if (!__all_sync(0xffffffffu, n_s == 0 || mbar_wait(smem_u32(&hdr->pv_done[grp]), (n_s - 1) & 1, wl, abort))) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          if (any) {
+            // Move the reference maximum only for a large growth (or the first
+            // step's); the accumulator exists from the second step on.
+            const bool grow = first || (top - m) * p.c > kRescale;
+            if (__any_sync(0xffffffffu, grow) && !first) {
+              const float f = grow ? ex2((m - top) * p.c) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_o + c, o);
+                tmem_ld_wait();
+                tmem_arrived(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(t_o + c, o);
+                tmem_st16(t_o + c + 16, o + 16);
+              }
+              l *= f;
+            }
+            if (grow) m = top;
+            const float off = m == -INFINITY ? 0.f : -m * p.c;
+            const uint64_t c2 = f2(p.c, p.c), off2 = f2(off, off);
+            uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int q = 0; q < W / 32; ++q) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 x =
+                    unf2(fma2(f2(__uint_as_float(s[q * 32 + 2 * j]), __uint_as_float(s[q * 32 + 2 * j + 1])), c2, off2));
+                const float a = ex2(x.x), b = ex2(x.y);
+                sum[j & 1] = add2(sum[j & 1], f2(a, b));
+                pk[j] = T::pack(a, b);
+              }
+              tmem_st16(t_p + q * 16, pk);
+            }
+            const float2 t = unf2(add2(sum[0], sum[1]));
+            l += t.x + t.y;
+            tmem_st_wait();
           }
           if (edge) {
-            uint32_t mask[4] = {0u, 0u, 0u, 0u};
-            if (live) row_mask(p, g, tok, tile, mask);
-#pragma unroll
-            for (int j = 0; j < kTile; ++j)
-              s[j] = (mask[j >> 5] >> (j & 31)) & 1u ? s[j] : 0xff800000u;
-          }
-          float mx[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
-#pragma unroll
-          for (int j = 4; j < kTile - 4; j += 2)
-            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-          mx[0] = max3(mx[0], __uint_as_float(s[kTile - 4]), __uint_as_float(s[kTile - 3]));
-          mx[1] = max3(mx[1], __uint_as_float(s[kTile - 2]), __uint_as_float(s[kTile - 1]));
-          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          // Move the reference maximum only for a large growth (or the first
-          // finite score); the accumulator exists from the second tile on.
-          const bool first = i < (g.two ? 1 : 2);
-          const bool grow = first || (top - m) * p.c > kRescale;
-          if (__any_sync(0xffffffffu, grow) && !first) {
-            const float f = grow ? ex2((m - top) * p.c) : 1.f;
-            // (the P V of the tile before is complete: the scores just read were issued after it)
+            // Values of slots that some row must not see: zero past the item's
+            // end, and infinities and NaN out (kept in `bad`).
+            const uint32_t vi = it + 2 * i + 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->full[vi % NS]), (vi / NS) & 1, wl, abort))) {
+              stop = true;
+              break;
+            }
+            // A thread takes eight 16-byte words of one of the step's rows (four
+            // with two M tiles: then each group takes half).
+            const int j = r % W, slot = start + j;
+            const int c0 = r / W * 8 + (g.two ? grp * 4 : 0), c1 = c0 + (g.two ? 4 : 8);
+            const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + (u * W + j) * 128;
+            if (slot >= hidden) {
+              bool found = false;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + grp * 128 + c, o);
-              tmem_ld_wait();
-              tmem_arrived(o);
+              for (int c = c0; c < c1; c += 4) {
+                const uint32_t at = row + (c >> 3) * kHalfBytes;
+                uint4 v[4];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(t_o + grp * 128 + c, o);
-              tmem_st16(t_o + grp * 128 + c + 16, o + 16);
-            }
-            l *= f;
-          }
-          if (grow) m = top;
-          const float off = m == -INFINITY ? 0.f : -m * p.c;
-          const uint64_t c2 = f2(p.c, p.c), off2 = f2(off, off);
-          uint64_t sum[2] = {0ull, 0ull};
+                for (int e = 0; e < 4; ++e) v[e] = lds128(at + ((((c + e) ^ j) & 7) << 4));
+                bool fine = slot < g.end;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
+                for (int e = 0; e < 4; ++e)
+                  fine &= finite2<T>(v[e].x) && finite2<T>(v[e].y) && finite2<T>(v[e].z) && finite2<T>(v[e].w);
+                if (!fine) {
+                  found = true;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 x = unf2(fma2(f2(__uint_as_float(s[q * 32 + 2 * j]), __uint_as_float(s[q * 32 + 2 * j + 1])),
-                                         c2, off2));
-              const float a = ex2(x.x), b = ex2(x.y);
-              sum[j & 1] = add2(sum[j & 1], f2(a, b));
-              pk[j] = T::pack(a, b);
-            }
-            tmem_st16(t_s + q * 16, pk);
-            if (q == 1 && !edge) {
-              tmem_st_wait();
-              tc_fence_before();
-              mbar_arrive(smem_u32(&hdr->p_half[grp]));
-            }
-          }
-          const float2 t = unf2(add2(sum[0], sum[1]));
-          l += t.x + t.y;
-          tmem_st_wait();
-        }
-        if (edge) {
-          // Values of slots that some row must not see: zero past the end of
-          // the sequence, and infinities and NaN out (kept in `bad`).
-          const uint32_t vi = it + value_place(i, n, g.two);
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->full[vi % NS]), (vi / NS) & 1, wl, abort))) {
-            stop = true;
-            break;
-          }
-          // (with two M tiles each group takes half of the columns)
-          constexpr int CH = D / 8;  // 16-byte words of a row
-          const int slot = tile * kTile + r, ch0 = g.two ? grp * (CH / 2) : 0, ch1 = g.two ? ch0 + CH / 2 : CH;
-          const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + r * 128;
-          if (slot >= g.ctx + g.n) {
-#pragma unroll 4
-            for (int c = ch0; c < ch1; ++c)
-              sts128(row + (c >> 3) * kHalfBytes + (((c ^ r) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
-          } else if (slot >= hidden) {
-            bool found = false;
-#pragma unroll 1
-            for (int c = ch0; c < ch1; c += 4) {
-              uint4 v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[j] = lds128(row + ((c + j) >> 3) * kHalfBytes + ((((c + j) ^ r) & 7) << 4));
-              bool fine = true;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                fine &= finite2<T>(v[j].x) && finite2<T>(v[j].y) && finite2<T>(v[j].z) && finite2<T>(v[j].w);
-              if (!fine) {
-                found = true;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  sts128(row + ((c + j) >> 3) * kHalfBytes + ((((c + j) ^ r) & 7) << 4),
-                         make_uint4(only_finite<T>(v[j].x), only_finite<T>(v[j].y), only_finite<T>(v[j].z),
-                                    only_finite<T>(v[j].w)));
+                  for (int e = 0; e < 4; ++e)
+                    sts128(at + ((((c + e) ^ j) & 7) << 4),
+                           slot < g.end ? make_uint4(only_finite<T>(v[e].x), only_finite<T>(v[e].y),
+                                                     only_finite<T>(v[e].z), only_finite<T>(v[e].w))
+                                        : make_uint4(0u, 0u, 0u, 0u));
+                }
+              }
+              if (found && slot < g.end) {
+                const int x = slot - hidden;  // fewer than 256: an item's tokens, or a tree's
+                atomicOr(&bad[x >> 5], 1u << (x & 31));
               }
             }
-            if (found) {
-              const int x = slot - hidden;  // (an item or a tree has at most 256 tokens: no row sees later ones)
-              if (x < 256) atomicOr(&bad[x >> 5], 1u << (x & 31));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (g.two && !meet()) {
+              stop = true;
+              break;
             }
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (g.two && !meet()) {
-            stop = true;
-            break;
-          }
+          tc_fence_before();
+          mbar_arrive(smem_u32(&hdr->p_ready[grp]));
         }
-        tc_fence_before();
-        if (edge || !any) mbar_arrive(smem_u32(&hdr->p_half[grp]));
-        mbar_arrive(smem_u32(&hdr->p_ready[grp]));
       }
       if (stop) break;
       it += 2 * n;
@@ -1001,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
           uint32_t o[32];
-          tmem_ld32(t_o + (g.two ? grp * 128 : 0) + c, o);
+          tmem_ld32((g.two ? t_o : t_o0) + c, o);
           tmem_ld_wait();
           tmem_arrived(o);
           float v[32];
@@ -1012,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;
             if (used1) {
-              tmem_ld32(t_o + 128 + c, o);
+              tmem_ld32(t_o0 + C::kCols + c, o);
               tmem_ld_wait();
               tmem_arrived(o);
 #pragma unroll
@@ -1050,16 +1087,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g.part < 0) {
           // The warp's 32 rows, 16 bytes a lane: neighbouring lanes write neighbouring words of a row.
           __syncwarp();
-          const int words = (c_hi - c_lo) / 8;  // 4, 8 or 16 of a row
           const int64_t mine = live ? out_at : -1;
-          for (int i = lane; i < 32 * words; i += 32) {
-            const int row = i / words, w = c_lo / 8 + i % words;
-            const int64_t at = __shfl_sync(0xffffffffu, mine, row);
-            const int rw = (warp & 3) * 32 + row;
-            if (at >= 0)
-              *reinterpret_cast<uint4*>(p.out + at + w * 16) =
-                  lds128(stage + rw * 128 + (w >> 3) * kHalfBytes + ((w ^ rw) & 7) * 16);
-          }
+          if (g.two)
+            flush_rows<D / 8>(p.out, stage, (warp & 3) * 32, 0, mine, lane);
+          else
+            flush_rows<D / 16>(p.out, stage, (warp & 3) * 32, grp * (D / 16), mine, lane);
         }
       }
       qi += 1 + g.two;
