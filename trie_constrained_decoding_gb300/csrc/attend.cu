@@ -8,30 +8,30 @@
 // or a prompt fills tiles of 128.
 //
 // Work.  An item is one sequence, one key-value head and up to two M tiles;
-// its units are 128-slot tiles of the cache.  The units of all items form one
-// line that is cut into equal parts, one per CTA (one CTA per SM), whatever
-// the mixture of lengths: a long context is split over many CTAs, many short
-// ones share one.  Every CTA works its part out from the lengths on the
+// its units are 128-slot tiles of the cache, and a few more for its beginning
+// and end.  The units of all items form one line that is cut into equal parts,
+// one per CTA (one CTA per SM), whatever the mixture of lengths: a long context
+// is split over many CTAs, many short ones share one.  Every CTA works its part out from the lengths on the
 // device, so the launch depends on none of them and can be captured.  An item
 // that a cut falls into leaves unnormalised partial results, at most two per
 // CTA, which a second kernel joins.
 //
-// One CTA, 12 warps:
+// One CTA, 16 warps:
 //  - warp 0 loads: queries, then key and value tiles, into a ring of 128 x
 //    head_dim tiles by TMA (128-byte swizzle; one copy per page piece and 64
 //    columns; pages past the sequence's end are not loaded);
-//  - warps 1 and 3, one thread each, issue the products of one softmax group on
-//    the tensor cores: S = Q K^T (both operands in shared memory) and O += P V
-//    with P in tensor memory, in steps of 64 slots (head_dim 128) or 128 (64);
+//  - warps 1 and 3 issue the score products S = Q K^T of one softmax group each
+//    (both operands in shared memory), warps 4 and 5 the output products
+//    O += P V (P in tensor memory), in steps of 64 slots (head_dim 128) or 128
+//    (64).  One thread each, which does nothing but wait for its operands and
+//    issue: an issuer with several things to look at reacts too late;
 //  - warp 2 hands out the CTA's segments (an item's part) through a small ring;
-//  - warps 4-7 and 8-11 are two softmax groups, one row per thread: a thread
+//  - warps 8-11 and 12-15 are two softmax groups, one row per thread: a thread
 //    reads its row of S from tensor memory, keeps the row's maximum and sum in
 //    32 bits, and writes the weights P beside it in the cache's type.
 // The two groups always alternate with the tensor cores: with two M tiles each
 // takes one and both use every key-value tile; with one M tile they take the
-// even and the odd tiles of the cache and are joined at the end.  Each group
-// has an issuer of its own, so that one group's wait for its weights does not
-// hold up the other's products.
+// even and the odd tiles of the cache and are joined at the end.
 //
 // Tensor memory, 512 columns of 32 bits: each group has its scores S, its
 // weights P and its accumulator O, 64 + 32 + 128 columns (head_dim 128) or
@@ -63,10 +63,11 @@ namespace tcd {
 namespace {
 
 constexpr int kTile = 128;                  // slots of a key-value tile, rows of an M tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr uint32_t kHalfBytes = kTile * 128; // 128 rows of 64 elements
 constexpr float kRescale = 8.f;             // log2 of the growth that moves the reference maximum
 constexpr int kSegs = 4;                    // segments ahead of the softmax groups
+constexpr int kItemCost = 2;                // an item's beginning and end, in tiles
 constexpr long long kWaitLimit = 1ll << 22; // default polls of one wait before giving up
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -120,8 +121,14 @@ struct AttendParams {
 constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile; }
 
 struct Hdr {
-  uint64_t full[10], empty[10];      // key-value ring
-  uint64_t q_full[2], q_empty[2];
+  // Key-value ring (twice as many "full" barriers as stages) and query tiles
+  // (four for two places): a waiter looks at its own turns only, and a parity
+  // tells a phase from the one before only if that one is known to be over.
+  // It is: a place is filled when the one before in the same place has been
+  // handed back, so what lies a whole ring further back than the waiter's
+  // last turn is done.
+  uint64_t full[20], empty[10];
+  uint64_t q_full[4], q_empty[2];
   uint64_t s_full[2], s_read[2], p_ready[2], pv_done[2], o_full[2];
   uint64_t o_free;                   // both groups have read the accumulators
   uint64_t meet;                     // both groups
@@ -134,8 +141,7 @@ struct Hdr {
   int32_t seq0;
   uint32_t bad[2][8];                // tokens whose values are not finite, by segment parity
   Seg seg[kSegs];
-  float2 ml[2][kTile];
-  int64_t scan[kThreads / 32];
+  float2 ml[2][kTile];               // (the prologue's sums before the first segment)
 };
 template <int D>
 constexpr size_t smem_bytes() {
@@ -160,10 +166,14 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+// Up to 64 polls of a phase (each waits a while in hardware).
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 64;\n"
+      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
+      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -172,18 +182,17 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // Waits for a phase, at most `limit` polls; false if it gave up or another
 // wait of the CTA has.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long long limit, volatile int32_t* abort) {
-  for (long long i = 0; i < limit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63) == 63 && *abort) return false;
+  if (mbar_poll(bar, parity)) return true;
+  for (long long i = 64; i < limit; i += 64) {
+    if (mbar_poll(bar, parity)) return true;
+    if (*abort) return false;
   }
   *abort = 1;
   return false;
+}
+// The same for a whole warp, with one answer for all of it.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit, volatile int32_t* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
 __device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page,
                                        uint32_t bar) {
@@ -218,9 +227,9 @@ __device__ __forceinline__ uint64_t desc_n_major(uint32_t a) {
 }
 // Instruction descriptor of kind::f16: 32-bit accumulator, M = 128.
 template <typename T>
-__device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major) {
+__device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major, bool negate_a = false) {
   const uint32_t ty = T::kMma;
-  return (1u << 4) | (ty << 7) | (ty << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+  return (1u << 4) | (ty << 7) | (ty << 10) | (negate_a ? 1u << 13 : 0u) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kTile >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -346,21 +355,22 @@ __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
 struct Line {
   int n, ctx, step;  // tokens, cached tokens, tokens of an item
   bool causal;
+  int extra;         // units of an item beside its tiles, counted before them
   __device__ int items() const { return (n + step - 1) / step; }
   // tiles of item i
   __device__ int tiles(int i) const {
     const int64_t end = causal ? min((int64_t)n, (int64_t)(i + 1) * step) : n;
     return (int)((ctx + end + kTile - 1) / kTile);
   }
-  // tiles of the items before item i
+  // units of the items before item i
   __device__ int64_t before(int i) const {
-    if (!causal || i == 0) return (int64_t)i * tiles(0);
-    return floor_sum(i, kTile, step, (int64_t)ctx + step + kTile - 1);
+    if (!causal || i == 0) return (int64_t)i * (tiles(0) + extra);
+    return floor_sum(i, kTile, step, (int64_t)ctx + step + kTile - 1) + (int64_t)i * extra;
   }
-  __device__ int64_t units() const { return n > 0 ? before(items() - 1) + tiles(items() - 1) : 0; }
+  __device__ int64_t units() const { return n > 0 ? before(items() - 1) + tiles(items() - 1) + extra : 0; }
   // the item that unit u is in
   __device__ int item_of(int64_t u) const {
-    if (!causal) return (int)div64(u, tiles(0));
+    if (!causal) return (int)div64(u, tiles(0) + extra);
     int lo = 0, hi = items();
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -370,12 +380,13 @@ struct Line {
   }
 };
 
-__device__ __forceinline__ bool line_of(const AttendParams& p, int b, SeqSpan* s, Line* l) {
+__device__ __forceinline__ bool line_of(const AttendParams& p, int b, int extra, SeqSpan* s, Line* l) {
   const bool ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
   l->n = ok ? s->n : 0;
   l->ctx = ok ? s->ctx : 0;
   l->step = 2 * p.tile_tokens;
   l->causal = p.tree == nullptr;
+  l->extra = extra;
   return ok;
 }
 
@@ -420,16 +431,17 @@ __device__ __forceinline__ int first_hidden(const AttendParams& p, const Seg& g)
   return p.tree ? g.ctx : g.ctx + g.tok0 + 1;
 }
 
+// Slots of the step that starts at `start` which any row of the item sees.
+template <int D>
+__device__ __forceinline__ int step_slots(const Seg& g, int start) {
+  return min(Cfg<D>::kStep, g.end - start);
+}
 // Steps of a tile (the last one of an item may end in its first half).
 template <int D>
 __device__ __forceinline__ int steps_of(const Seg& g, int tile) {
   return min(Cfg<D>::kSteps, (g.end - tile * kTile + Cfg<D>::kStep - 1) / Cfg<D>::kStep);
 }
 
-template <typename T>
-__device__ __forceinline__ bool finite2(uint32_t v) {
-  return (v & T::kExp) != T::kExp && (v & (T::kExp << 16)) != (T::kExp << 16);
-}
 // A pair with zeros for what is infinite or NaN.
 template <typename T>
 __device__ __forceinline__ uint32_t only_finite(uint32_t v) {
@@ -511,12 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(smem_u32(&hdr->full[i]), 1);
-      mbar_init(smem_u32(&hdr->empty[i]), 2);    // both issuers (a commit each, or an arrival where it is not theirs)
-    }
+    for (int i = 0; i < 2 * NS; ++i) mbar_init(smem_u32(&hdr->full[i]), 1);
+    for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&hdr->empty[i]), 2);  // a commit per group, or two of one
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&hdr->q_full[i]), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&hdr->q_full[i]), 1);
       mbar_init(smem_u32(&hdr->q_empty[i]), 8);  // eight softmax warps (four of them twice)
       mbar_init(smem_u32(&hdr->s_full[i]), 1);
       mbar_init(smem_u32(&hdr->s_read[i]), kTile);
@@ -528,9 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&hdr->meet), 2 * kTile);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(smem_u32(&hdr->seg_full[i]), 1);
-      mbar_init(smem_u32(&hdr->seg_empty[i]), 3 + 8);  // loader, issuers, eight softmax warps
+      mbar_init(smem_u32(&hdr->seg_empty[i]), 5 + 8);  // loader, four issuers, eight softmax warps
     }
-    mbar_init(smem_u32(&hdr->drain), 2);
+    mbar_init(smem_u32(&hdr->drain), 4);
     hdr->abort = 0;
     hdr->seq0 = -1;
     for (int i = 0; i < 16; ++i) hdr->bad[i >> 3][i & 7] = 0u;
@@ -549,43 +559,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // Units of every sequence: thread i counts a run of them, then a scan over
-  // the CTA gives the total and who holds this worker's first unit.
+  // Tiles and items of every sequence: thread i counts a run of them, then a
+  // scan over the CTA gives the totals and who holds this worker's first unit.
   const int run = (p.tok.batch + kThreads - 1) / kThreads;
-  int64_t mine = 0;
+  int64_t* sums = reinterpret_cast<int64_t*>(hdr->ml);
+  int64_t tiles = 0, items = 0;
   for (int i = 0; i < run; ++i) {
     const int b = tid * run + i;
     SeqSpan s;
     Line l;
-    if (b < p.tok.batch && line_of(p, b, &s, &l)) mine += l.units() * p.kv.kv_heads;
+    if (b < p.tok.batch && line_of(p, b, 0, &s, &l) && s.n > 0) {
+      tiles += l.units() * p.kv.kv_heads;
+      items += (int64_t)l.items() * p.kv.kv_heads;
+    }
   }
-  int64_t incl = mine;
+  int64_t tiles_to = tiles, items_to = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
+    const int64_t x = __shfl_up_sync(0xffffffffu, tiles_to, o), y = __shfl_up_sync(0xffffffffu, items_to, o);
+    if (lane >= o) {
+      tiles_to += x;
+      items_to += y;
+    }
   }
-  if (lane == 31) hdr->scan[warp] = incl;
+  if (lane == 31) {
+    sums[warp] = tiles_to;
+    sums[kThreads / 32 + warp] = items_to;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t total = 0, start_of_warp = 0;
+  int64_t all_tiles = 0, all_items = 0;
   for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) start_of_warp += hdr->scan[i];
-    total += hdr->scan[i];
+    if (i < warp) {
+      tiles_to += sums[i];
+      items_to += sums[kThreads / 32 + i];
+    }
+    all_tiles += sums[i];
+    all_items += sums[kThreads / 32 + i];
   }
+  // With little to do every worker gets tiles first of all.
+  const int extra = all_tiles >= 8 * (int64_t)p.workers ? kItemCost : 0;
+  const int64_t total = all_tiles + extra * all_items;
   const int active = (int)min((int64_t)p.workers, total);
   const Cut cut(total, active);
   const int64_t begin = worker < active ? cut.start(worker) : 0;
   const int64_t end = worker < active ? cut.start(worker + 1) : 0;
-  const int64_t excl = start_of_warp + incl - mine;
-  if (begin < end && begin >= excl && begin < excl + mine) {
+  const int64_t excl = tiles_to - tiles + extra * (items_to - items);
+  if (begin < end && begin >= excl && begin < excl + tiles + extra * items) {
     int64_t at = excl;
     for (int i = 0; i < run; ++i) {
       const int b = tid * run + i;
       SeqSpan s;
       Line l;
-      if (b >= p.tok.batch || !line_of(p, b, &s, &l)) continue;
+      if (b >= p.tok.batch || !line_of(p, b, extra, &s, &l)) continue;
       const int64_t u = l.units() * p.kv.kv_heads;
       if (begin < at + u) {
         hdr->seq0 = b;
@@ -600,11 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool held = p.withhold != 0 && worker == 0;
   uint32_t armed = 0;  // loader: key-value stages armed, for the exit path
   uint32_t q_armed = 0;
-  // Registers: 384 threads launch with 168 each, 64,512 together; a softmax
+  // Registers: 512 threads launch with 128 each, 65,536 together; a softmax
   // thread holds a step's row of scores (128 at head_dim 64) and takes 200, the
-  // others keep 96 (96 * 128 + 200 * 256 = 63,488).
-  if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  // others keep 56 (56 * 256 + 200 * 256 = 65,536).
+  if (warp < 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     // ------------------------------------------------------------- loader
     uint32_t it = 0, qi = 0;
@@ -612,18 +639,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int piece = lane / C::kHalves, half = lane % C::kHalves;
     bool stop = false;
     for (int k = 0; !stop; ++k) {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort))) break;
+      if (!warp_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
       const Seg g = hdr->seg[k % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
       if (!g.valid) break;
       for (int m = 0; m <= g.two; ++m, ++qi) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->q_empty[qi & 1]), ((qi >> 1) & 1) ^ 1, wl, abort))) {
+        if (!warp_wait(smem_u32(&hdr->q_empty[qi & 1]), ((qi >> 1) & 1) ^ 1, wl, abort)) {
           stop = true;
           break;
         }
         if (lane == 0) {
-          const uint32_t bar = smem_u32(&hdr->q_full[qi & 1]);
+          const uint32_t bar = smem_u32(&hdr->q_full[qi & 3]);
           mbar_expect_tx(bar, (uint32_t)p.q_rows * 128u * C::kHalves);
           for (int h = 0; h < C::kHalves; ++h)
             tma_q(q_s + (qi & 1) * C::kTileBytes + h * kHalfBytes, &map_q, h * 64, g.head * p.group,
@@ -639,11 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool load = piece < pieces && slot < g.end;
         const int page = load ? __ldg(row + (slot >> p.kv.page_shift)) : 0;
         const int stage = (int)(it % NS);
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->empty[stage]), ((it / NS) & 1) ^ 1, wl, abort))) {
+        if (!warp_wait(smem_u32(&hdr->empty[stage]), ((it / NS) & 1) ^ 1, wl, abort)) {
           stop = true;
           break;
         }
-        const uint32_t bar = smem_u32(&hdr->full[stage]);
+        const uint32_t bar = smem_u32(&hdr->full[it % (2 * NS)]);
         const int count = __popc(__ballot_sync(0xffffffffu, load));
         if (lane == 0) mbar_expect_tx(bar, (uint32_t)(count * box * 128));
         __syncwarp();
@@ -653,102 +680,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++armed;
       }
     }
-  } else if (warp == 1 || warp == 3) {
+  } else if (warp == 1 || warp == 3 || warp == 4 || warp == 6) {
     // ------------------------------------------------------------ issuers
     if (lane == 0) {
-      const int slot = warp >> 1;  // which group's products
+      const bool is_s = warp < 4;                          // score or output products
+      const int slot = is_s ? warp >> 1 : (warp - 4) >> 1;        // whose
       const uint32_t t_s = tmem + slot * C::kCols, t_p = t_s + C::kP, t_o = t_s + C::kO;
-      constexpr uint32_t id_s = idesc<T>(C::kStep, false), id_o = idesc<T>(D, true);
-      // Ring places looked at, query tiles, score and output products issued.
-      // Every phase of a barrier that this thread waits on is looked at in
-      // order, its own turn or not: a parity says nothing about a phase
-      // further back.
-      uint32_t seen = 0, qi = 0, n_s = 0, n_o = 0;
+      // (a negative scale is one of the negated products)
+      const uint32_t id_s = idesc<T>(C::kStep, false, p.negate != 0);
+      constexpr uint32_t id_o = idesc<T>(D, true);
+      uint32_t it = 0, qi = 0, done = 0;  // ring places, query tiles, products
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && mbar_wait(smem_u32(bar), parity & 1, wl, abort);
         return ok;
+      };
+      // The stage is handed back when the products so far are done.
+      auto release = [&](uint32_t stage, bool two) {
+        mma_commit(smem_u32(&hdr->empty[stage]));
+        if (!two) mma_commit(smem_u32(&hdr->empty[stage]));
       };
       for (int k = 0; ok; ++k) {
         if (!wait(&hdr->seg_full[k % kSegs], k / kSegs)) break;
         const Seg g = hdr->seg[k % kSegs];
         mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
         if (!g.valid) break;
-        const int n = g.t1 - g.t0, hop = g.two ? 1 : 2;
-        const uint32_t q = qi + (g.two ? slot : 0);
-        if (!wait(&hdr->q_full[qi & 1], qi >> 1)) break;
-        if (g.two && !wait(&hdr->q_full[(qi + 1) & 1], (qi + 1) >> 1)) break;
-        qi += 1 + g.two;
-        const uint64_t q_desc = desc_k_major(q_s + (q & 1) * C::kTileBytes);
-        const uint32_t at0 = seen, at1 = seen + 2 * n;  // the segment's ring places
-        // The next score product and the next output product: tile, step of
-        // the tile, steps of the tile.  Whichever can go goes.
-        const int i0 = g.two ? 0 : slot;
-        int is = i0, us = 0, io = i0, uo = 0;
-        int steps_s = is < n ? steps_of<D>(g, g.t0 + is) : 0, steps_o = steps_s;
-        bool o_free = k == 0;
-        long long idle = 0;
-        while (io < n || seen < at1) {
-          bool moved = false;
-          if (seen < at1 && mbar_test(smem_u32(&hdr->full[seen % NS]), (seen / NS) & 1)) {
-            // (the other group's tile: nothing of it is needed here)
-            if (!g.two && (((seen - at0) >> 1) & 1) != (uint32_t)slot) mbar_arrive(smem_u32(&hdr->empty[seen % NS]));
-            ++seen;
-            moved = true;
-          }
-          if (is < n && at0 + 2 * is < seen &&
-              (n_s == 0 || mbar_test(smem_u32(&hdr->s_read[slot]), (n_s - 1) & 1))) {
-            // S = Q K^T: the scores before have been read.
-            const uint32_t stage = (at0 + 2 * is) % NS;
-            const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + us * (C::kStep * 128));
-            tc_fence_after();
+        const int n = g.t1 - g.t0, hop = g.two ? 1 : 2, i0 = g.two ? 0 : slot;
+        if (is_s) {
+          const uint32_t q = qi + (g.two ? slot : 0);
+          if (!wait(&hdr->q_full[q & 3], q >> 2)) break;
+          const uint64_t q_desc = desc_k_major(q_s + (q & 1) * C::kTileBytes);
+          for (int i = i0; i < n && ok; i += hop) {
+            const uint32_t at = it + 2 * i, stage = at % NS;
+            const int steps = steps_of<D>(g, g.t0 + i);
+            if (!wait(&hdr->full[at % (2 * NS)], at / (2 * NS))) break;
+            for (int u = 0; u < steps; ++u, ++done) {
+              // (the scores before have been read)
+              if (done > 0 && !wait(&hdr->s_read[slot], done - 1)) break;
+              const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + u * (C::kStep * 128));
+              tc_fence_after();
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-              const uint32_t o = ((uint32_t)(e >> 2) * kHalfBytes + (uint32_t)(e & 3) * 32) >> 4;
-              mma_ss(t_s, q_desc + o, b + o, id_s, e > 0);
+              for (int e = 0; e < D / 16; ++e) {
+                const uint32_t o = ((uint32_t)(e >> 2) * kHalfBytes + (uint32_t)(e & 3) * 32) >> 4;
+                mma_ss(t_s, q_desc + o, b + o, id_s, e > 0);
+              }
+              mma_commit(smem_u32(&hdr->s_full[slot]));
             }
-            mma_commit(smem_u32(&hdr->s_full[slot]));
-            ++n_s;
-            if (++us == steps_s) {
-              mma_commit(smem_u32(&hdr->empty[stage]));
-              us = 0;
-              is += hop;
-              if (is < n) steps_s = steps_of<D>(g, g.t0 + is);
-            }
-            moved = true;
+            release(stage, g.two);
           }
-          if (io < n && at0 + 2 * io + 1 < seen) {
-            // O += P V.  The accumulators of the segment before have been read.
-            if (!o_free) o_free = mbar_test(smem_u32(&hdr->o_free), (uint32_t)(k - 1) & 1);
-            if (o_free && mbar_test(smem_u32(&hdr->p_ready[slot]), n_o & 1)) {
-              const uint32_t stage = (at0 + 2 * io + 1) % NS;
-              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + uo * (C::kStep * 128));
-              const bool first = io == i0 && uo == 0;
+        } else {
+          // (the accumulators of the segment before have been read)
+          if (k > 0 && !wait(&hdr->o_free, k - 1)) break;
+          for (int i = i0; i < n && ok; i += hop) {
+            const uint32_t at = it + 2 * i + 1, stage = at % NS;
+            const int steps = steps_of<D>(g, g.t0 + i);
+            if (!wait(&hdr->full[at % (2 * NS)], at / (2 * NS))) break;
+            for (int u = 0; u < steps; ++u, ++done) {
+              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + u * (C::kStep * 128));
+              // over the 16-slot groups that the step has
+              const int groups = (step_slots<D>(g, (g.t0 + i) * kTile + u * C::kStep) + 15) / 16;
+              const bool more = i > i0 || u > 0;
+              if (!wait(&hdr->p_ready[slot], done)) break;
               tc_fence_after();
 #pragma unroll
               for (int e = 0; e < C::kStep / 16; ++e)
-                mma_ts(t_o, t_p + e * 8, b + e * (2048 >> 4), id_o, !first || e > 0);
+                if (e < groups) mma_ts(t_o, t_p + e * 8, b + e * (2048 >> 4), id_o, more || e > 0);
               mma_commit(smem_u32(&hdr->pv_done[slot]));
-              ++n_o;
-              if (++uo == steps_o) {
-                mma_commit(smem_u32(&hdr->empty[stage]));
-                uo = 0;
-                io += hop;
-                if (io < n) steps_o = steps_of<D>(g, g.t0 + io);
-              }
-              moved = true;
             }
+            release(stage, g.two);
           }
-          if (moved) {
-            idle = 0;
-          } else if (++idle > wl || ((idle & 63) == 0 && *abort)) {
-            *abort = 1;
-            ok = false;
-            break;
-          }
+          mma_commit(smem_u32(&hdr->o_full[slot]));
         }
-        if (!ok || (!o_free && !wait(&hdr->o_free, k - 1))) break;
-        mma_commit(smem_u32(&hdr->o_full[slot]));
+        it += 2 * n;
+        qi += 1 + g.two;
       }
     }
     __syncwarp();
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (sequences without units are passed over)
           int64_t per = 0;
           while (b < p.tok.batch) {
-            if (line_of(p, b, &s, &l) && (per = l.units()) * p.kv.kv_heads > off) break;
+            if (line_of(p, b, extra, &s, &l) && (per = l.units()) * p.kv.kv_heads > off) break;
             off = 0;
             ++b;
           }
@@ -781,36 +785,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           int h = head;
           while (left > 0 && h < p.kv.kv_heads) {
             const int tiles = l.tiles(item);
-            const int64_t take = min((int64_t)tiles - r, left);
-            g.valid = 1;
-            g.seq = b;
-            g.row0 = s.row0;
-            g.n = s.n;
-            g.ctx = s.ctx;
-            g.head = h;
-            g.tok0 = item * l.step;
-            g.t0 = (int)r;
-            g.t1 = (int)(r + take);
-            g.two = s.n - g.tok0 > p.tile_tokens;
-            g.end = s.ctx + (p.tree ? s.n : min(s.n, g.tok0 + l.step));
-            g.part = take == tiles ? -1 : r > 0 ? 0 : 1;
-            g.last = worker;
-            if (g.part == 1) {
-              // the item's last unit lies with the worker that this finds
-              const int64_t last_unit = end - left + tiles - 1;
-              int w = worker + 1;
-              while (cut.start(w + 1) <= last_unit) ++w;
-              g.last = w;
-              d = g;
-              open_end = true;
+            const int64_t take = min((int64_t)extra + tiles - r, left);
+            g.t0 = (int)max(r - extra, (int64_t)0);
+            g.t1 = (int)max(r + take - extra, (int64_t)0);
+            if (g.t1 > g.t0) {
+              g.valid = 1;
+              g.seq = b;
+              g.row0 = s.row0;
+              g.n = s.n;
+              g.ctx = s.ctx;
+              g.head = h;
+              g.tok0 = item * l.step;
+              g.two = s.n - g.tok0 > p.tile_tokens;
+              g.end = s.ctx + (p.tree ? s.n : min(s.n, g.tok0 + l.step));
+              g.part = g.t1 - g.t0 == tiles ? -1 : g.t0 > 0 ? 0 : 1;
+              g.last = worker;
+              if (g.part == 1) {
+                // the item's last unit lies with the worker that this finds
+                const int64_t last_unit = end - left - r + extra + tiles - 1;
+                int w = worker + 1;
+                while (cut.start(w + 1) <= last_unit) ++w;
+                g.last = w;
+                d = g;
+                open_end = true;
+              }
+              if (!mbar_wait(smem_u32(&hdr->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1, wl, abort)) {
+                ok = false;
+                break;
+              }
+              hdr->seg[k % kSegs] = g;
+              mbar_arrive(smem_u32(&hdr->seg_full[k % kSegs]));
+              ++k;
             }
-            if (!mbar_wait(smem_u32(&hdr->seg_empty[k % kSegs]), ((k / kSegs) & 1) ^ 1, wl, abort)) {
-              ok = false;
-              break;
-            }
-            hdr->seg[k % kSegs] = g;
-            mbar_arrive(smem_u32(&hdr->seg_full[k % kSegs]));
-            ++k;
             left -= take;
             r = 0;
             if (++item == l.items()) {
@@ -836,20 +842,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ----------------------------------------------------- softmax groups
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    const int grp = (warp - 4) >> 2;               // which slot
-    const int r = tid - 128 - grp * kTile;         // row of the M tile (TMEM lane)
+    const int grp = (warp - 8) >> 2;               // which slot
+    const int r = tid - 256 - grp * kTile;         // row of the M tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + grp * C::kCols;
     const uint32_t t_p = t_s + C::kP, t_o = t_s + C::kO, t_o0 = tmem + lane_base + C::kO;
     uint32_t n_s = 0, n_meet = 0, it = 0, qi = 0;
     auto meet = [&]() {
       mbar_arrive(smem_u32(&hdr->meet));
-      const bool ok = mbar_wait(smem_u32(&hdr->meet), n_meet & 1, wl, abort);
+      const bool ok = warp_wait(smem_u32(&hdr->meet), n_meet & 1, wl, abort);
       ++n_meet;
-      return (bool)__all_sync(0xffffffffu, ok);
+      return ok;
     };
     for (int k = 0;; ++k) {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort))) break;
+      if (!warp_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
       const Seg g = hdr->seg[k % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
@@ -862,109 +868,161 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t* bad = hdr->bad[k & 1];
       float m = -INFINITY, l = 0.f;
       bool stop = false;
-      bool first = true;
-      for (int i = g.two ? 0 : grp; i < n && !stop; i += g.two ? 1 : 2) {
-        const int steps = steps_of<D>(g, g.t0 + i);
-        for (int u = 0; u < steps; ++u, ++n_s, first = false) {
-          constexpr int W = C::kStep;
-          const int start = (g.t0 + i) * kTile + u * W;  // the step's first slot
-          const bool edge = start + W > hidden;
-          uint32_t mask[W / 32];
-          if (edge && live) row_mask<W / 32>(p, g, tok, start, mask);
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort))) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          uint32_t s[W];
-          if (any) {
+      constexpr int W = C::kStep;
+      const int hop = g.two ? 1 : 2;
+      const uint64_t c2 = f2(p.c, p.c);
+      float off = 0.f;     // -m c, or 0 while m is -inf
+      bool first = true;   // no step of this segment yet
+      // The scores of a step, read and handed back.
+      auto load = [&](uint32_t(&s)[W]) {
 #pragma unroll
-            for (int c = 0; c < W; c += 32) tmem_ld32(t_s + c, s + c);
-            tmem_ld_wait();
+        for (int c = 0; c < W; c += 32) tmem_ld32(t_s + c, s + c);
+        tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < W; c += 32) tmem_arrived(s + c);
-          }
-          tc_fence_before();
-          mbar_arrive(smem_u32(&hdr->s_read[grp]));
-          float top = -INFINITY;
-          if (any) {
-            if (p.negate) {
+        for (int c = 0; c < W; c += 32) tmem_arrived(s + c);
+        tc_fence_before();
+        mbar_arrive(smem_u32(&hdr->s_read[grp]));
+      };
+      // The P V of the step before is done: its weights' place is free and the
+      // accumulator at rest.  (Warps without rows wait as well: a warp must not
+      // announce a step's weights before the group's others have the last one's.)
+      auto rested = [&]() {
+        return n_s == 0 || mbar_wait(smem_u32(&hdr->pv_done[grp]), (n_s - 1) & 1, wl, abort);
+      };
+      // Weights of a step's scores.
+      auto weigh = [&](const uint32_t(&s)[W]) {
+        float mx[4];
 #pragma unroll
-              for (int j = 0; j < W; ++j) s[j] ^= 0x80000000u;
-            }
-            if (edge) {
+        for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
 #pragma unroll
-              for (int j = 0; j < W; ++j) s[j] = live && (mask[j >> 5] >> (j & 31)) & 1u ? s[j] : 0xff800000u;
-            }
-            float mx[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(s[j]);
-#pragma unroll
-            for (int j = 4; j < W; j += 2)
-              mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          }
-          // The P V of the step before is done: its weights' place is free and
-          // the accumulator at rest.
-          if (!__all_sync(0xffffffffu, n_s == 0 || mbar_wait(smem_u32(&hdr->pv_done[grp]), (n_s - 1) & 1, wl, abort))) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          if (any) {
-            // Move the reference maximum only for a large growth (or the first
-            // step's); the accumulator exists from the second step on.
-            const bool grow = first || (top - m) * p.c > kRescale;
-            if (__any_sync(0xffffffffu, grow) && !first) {
-              const float f = grow ? ex2((m - top) * p.c) : 1.f;
+        for (int j = 4; j < W; j += 2)
+          mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const bool ok = rested();
+        tc_fence_after();
+        // Move the reference maximum only for a large growth (the first finite
+        // score's among them); the accumulator exists from the second step on.
+        const bool grow = (top - m) * p.c > kRescale;
+        if (__any_sync(0xffffffffu, grow)) {
+          if (!first) {
+            const float f = grow ? ex2((m - top) * p.c) : 1.f;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(t_o + c, o);
-                tmem_ld_wait();
-                tmem_arrived(o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c, o);
+              tmem_ld_wait();
+              tmem_arrived(o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(t_o + c, o);
-                tmem_st16(t_o + c + 16, o + 16);
-              }
-              l *= f;
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(t_o + c, o);
+              tmem_st16(t_o + c + 16, o + 16);
             }
-            if (grow) m = top;
-            const float off = m == -INFINITY ? 0.f : -m * p.c;
-            const uint64_t c2 = f2(p.c, p.c), off2 = f2(off, off);
-            uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-            for (int q = 0; q < W / 32; ++q) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 x =
-                    unf2(fma2(f2(__uint_as_float(s[q * 32 + 2 * j]), __uint_as_float(s[q * 32 + 2 * j + 1])), c2, off2));
-                const float a = ex2(x.x), b = ex2(x.y);
-                sum[j & 1] = add2(sum[j & 1], f2(a, b));
-                pk[j] = T::pack(a, b);
-              }
-              tmem_st16(t_p + q * 16, pk);
-            }
-            const float2 t = unf2(add2(sum[0], sum[1]));
-            l += t.x + t.y;
-            tmem_st_wait();
+            l *= f;
           }
-          if (edge) {
+          if (grow) {
+            m = top;
+            off = -m * p.c;
+          }
+        }
+        first = false;
+        const uint64_t off2 = f2(off, off);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < W / 32; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x =
+                unf2(fma2(f2(__uint_as_float(s[q * 32 + 2 * j]), __uint_as_float(s[q * 32 + 2 * j + 1])), c2, off2));
+            const float a = ex2(x.x), b = ex2(x.y);
+            sum[j & 1] = add2(sum[j & 1], f2(a, b));
+            pk[j] = T::pack(a, b);
+          }
+          tmem_st16(t_p + q * 16, pk);
+        }
+        const float2 t = unf2(add2(sum[0], sum[1]));
+        l += t.x + t.y;
+        tmem_st_wait();
+        return ok;
+      };
+      // Steps that every row sees entirely, then those that some row does not.
+      // (In the first loop a wait that ran out is noticed at the step's end:
+      // nothing in between leaves its bounds.)
+      int i = g.two ? 0 : grp, u = 0;
+      for (; i < n && !stop; i += hop) {
+        const int steps = steps_of<D>(g, g.t0 + i);
+        const int full = min(steps, max(0, hidden - (g.t0 + i) * kTile) / W);
+        for (u = 0; u < full; ++u, ++n_s) {
+          bool ok = mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort);
+          if (any) {
+            __syncwarp();
+            tc_fence_after();
+            uint32_t s[W];
+            load(s);
+            ok &= weigh(s);
+            tc_fence_before();
+          } else {
+            mbar_arrive(smem_u32(&hdr->s_read[grp]));
+            ok &= rested();
+          }
+          mbar_arrive(smem_u32(&hdr->p_ready[grp]));
+          if (!__all_sync(0xffffffffu, ok)) {
+            stop = true;
+            break;
+          }
+        }
+        if (full < steps) break;
+      }
+      if (stop) break;
+      for (; i < n && !stop; i += hop, u = 0) {
+        const int steps = steps_of<D>(g, g.t0 + i);
+        for (; u < steps; ++u, ++n_s) {
+          const int start = (g.t0 + i) * kTile + u * W;  // the step's first slot
+          const int slots = step_slots<D>(g, start);
+          uint32_t mask[W / 32];
+#pragma unroll
+          for (int c = 0; c < W / 32; ++c) mask[c] = 0u;
+          if (live) row_mask<W / 32>(p, g, tok, start, mask);
+          if (!warp_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort)) {
+            stop = true;
+            break;
+          }
+          bool ok = true;
+          if (any) {
+            tc_fence_after();
+            uint32_t s[W];
+            load(s);
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[j] = mask[j >> 5] & (1u << (j & 31)) ? s[j] : 0xff800000u;
+            ok = weigh(s);
+          } else {
+            mbar_arrive(smem_u32(&hdr->s_read[grp]));
+            ok = rested();
+          }
+          if (!__all_sync(0xffffffffu, ok)) {
+            stop = true;
+            break;
+          }
+          {
             // Values of slots that some row must not see: zero past the item's
             // end, and infinities and NaN out (kept in `bad`).
             const uint32_t vi = it + 2 * i + 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&hdr->full[vi % NS]), (vi / NS) & 1, wl, abort))) {
+            if (!warp_wait(smem_u32(&hdr->full[vi % (2 * NS)]), (vi / (2 * NS)) & 1, wl, abort)) {
               stop = true;
               break;
             }
             // A thread takes eight 16-byte words of one of the step's rows (four
-            // with two M tiles: then each group takes half).
+            // with two M tiles: then each group takes half).  Past the end, only
+            // the rest of its group of 16 slots is read.
             const int j = r % W, slot = start + j;
             const int c0 = r / W * 8 + (g.two ? grp * 4 : 0), c1 = c0 + (g.two ? 4 : 8);
             const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + (u * W + j) * 128;
-            if (slot >= hidden) {
+            if (slot >= g.end) {
+              if (j < ((slots + 15) & ~15))
+#pragma unroll 4
+                for (int c = c0; c < c1; ++c)
+                  sts128(row + (c >> 3) * kHalfBytes + (((c ^ j) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+            } else if (slot >= hidden) {
               bool found = false;
 #pragma unroll 1
               for (int c = c0; c < c1; c += 4) {
@@ -972,21 +1030,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = lds128(at + ((((c + e) ^ j) & 7) << 4));
-                bool fine = slot < g.end;
+                uint32_t odd = 0u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  fine &= finite2<T>(v[e].x) && finite2<T>(v[e].y) && finite2<T>(v[e].z) && finite2<T>(v[e].w);
-                if (!fine) {
+                  odd = T::trace(v[e].w, T::trace(v[e].z, T::trace(v[e].y, T::trace(v[e].x, odd))));
+                if (odd & 0x7fff7fffu) {
                   found = true;
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
                     sts128(at + ((((c + e) ^ j) & 7) << 4),
-                           slot < g.end ? make_uint4(only_finite<T>(v[e].x), only_finite<T>(v[e].y),
-                                                     only_finite<T>(v[e].z), only_finite<T>(v[e].w))
-                                        : make_uint4(0u, 0u, 0u, 0u));
+                           make_uint4(only_finite<T>(v[e].x), only_finite<T>(v[e].y), only_finite<T>(v[e].z),
+                                      only_finite<T>(v[e].w)));
                 }
               }
-              if (found && slot < g.end) {
+              if (found) {
                 const int x = slot - hidden;  // fewer than 256: an item's tokens, or a tree's
                 atomicOr(&bad[x >> 5], 1u << (x & 31));
               }
@@ -1005,13 +1062,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       it += 2 * n;
       // ------------------------------------------------ end of the segment
       if (!g.two) hdr->ml[grp][r] = make_float2(m, l);
-      if (tid == 128)
+      if (tid == 256)
         for (int i = 0; i < 8; ++i) hdr->bad[(k & 1) ^ 1][i] = 0u;  // (last read before the groups' last meeting)
       if (!meet()) break;
       const bool used1 = g.two || n > 1;
-      bool ok = mbar_wait(smem_u32(&hdr->o_full[0]), k & 1, wl, abort);
-      ok = ok && mbar_wait(smem_u32(&hdr->o_full[1]), k & 1, wl, abort);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!warp_wait(smem_u32(&hdr->o_full[0]), k & 1, wl, abort) ||
+          !warp_wait(smem_u32(&hdr->o_full[1]), k & 1, wl, abort))
+        break;
       tc_fence_after();
       // Factors of the two accumulators (one M tile: both are this row's; two: only the group's own).
       float f0 = 1.f, f1 = 1.f;
@@ -1037,8 +1094,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) {
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
-          uint32_t o[32];
+          uint32_t o[32], o1[32];
           tmem_ld32((g.two ? t_o : t_o0) + c, o);
+          if (!g.two && used1) tmem_ld32(t_o0 + C::kCols + c, o1);
           tmem_ld_wait();
           tmem_arrived(o);
           float v[32];
@@ -1049,11 +1107,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;
             if (used1) {
-              tmem_ld32(t_o0 + C::kCols + c, o);
-              tmem_ld_wait();
-              tmem_arrived(o);
+              tmem_arrived(o1);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o[j]), f1, v[j]);
+              for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o1[j]), f1, v[j]);
             }
           }
           if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
@@ -1108,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A wait ran out.  Everything this CTA started has to end before it
     // leaves (waits bounded again): the products that were issued, and the
     // loads of stages that no product has consumed.
-    if ((warp == 1 || warp == 3) && lane == 0) {
+    if ((warp == 1 || warp == 3 || warp == 4 || warp == 6) && lane == 0) {
       mma_commit(smem_u32(&hdr->drain));
       int32_t none = 0;
       mbar_wait(smem_u32(&hdr->drain), 0u, wl, &none);
@@ -1116,9 +1172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
       int32_t none = 0;
       for (uint32_t j = armed > (uint32_t)NS ? armed - NS : 0; j < armed; ++j)
-        if (!(held && j == 0)) mbar_wait(smem_u32(&hdr->full[j % NS]), (j / NS) & 1, wl, &none);
+        if (!(held && j == 0)) mbar_wait(smem_u32(&hdr->full[j % (2 * NS)]), (j / (2 * NS)) & 1, wl, &none);
       for (uint32_t j = q_armed > 2 ? q_armed - 2 : 0; j < q_armed; ++j)
-        mbar_wait(smem_u32(&hdr->q_full[j & 1]), (j >> 1) & 1, wl, &none);
+        mbar_wait(smem_u32(&hdr->q_full[j & 3]), (j >> 2) & 1, wl, &none);
     }
     __syncwarp();
   }

@@ -32,6 +32,12 @@ struct TokensView {
 
 // 16-bit element types: pairs to and from 32-bit floats.
 struct Bf16 {
+  // acc + 0 * v for each half: zero as long as every v is finite, else NaN.
+  static __device__ __forceinline__ uint32_t trace(uint32_t v, uint32_t acc) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0u), "r"(acc));
+    return r;
+  }
   static constexpr uint32_t kMma = 1;       // operand type of a tensor-core instruction
   static constexpr uint32_t kExp = 0x7f80;  // exponent bits
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
@@ -42,8 +48,18 @@ struct Bf16 {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
+  static __device__ __forceinline__ uint32_t packv(float lo, float hi) {
+    uint32_t r;
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
 };
 struct F16 {
+  static __device__ __forceinline__ uint32_t trace(uint32_t v, uint32_t acc) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0u), "r"(acc));
+    return r;
+  }
   static constexpr uint32_t kMma = 0;
   static constexpr uint32_t kExp = 0x7c00;
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
@@ -52,6 +68,11 @@ struct F16 {
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t packv(float lo, float hi) {
+    uint32_t r;
+    asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
 };
