@@ -388,26 +388,17 @@ _pages_free_count = _decl("tc_pages_free_count", ctypes.c_int, [_vp, _i32p])
 
 
 def _rows(t, dtype, device, what: str, heads: int, head_dim: int):
-    """Row stride (elements) of packed rows [n, heads * head_dim] or [n, heads, head_dim]; the rows may be slices
-    of wider ones."""
-    if t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{what} must be {dtype} on {device}")
+    """Address and row stride (elements) of packed rows [n, heads * head_dim] or [n, heads, head_dim]; the rows may
+    be slices of wider ones."""
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
         ok = shape[1] == heads and shape[2] == head_dim and stride[2] == 1 and (heads == 1 or stride[1] == head_dim)
     else:
         ok = len(shape) == 2 and shape[1] == heads * head_dim and stride[1] == 1
-    if not ok:
-        raise ValueError(f"{what} must hold rows of {heads} heads of {head_dim} contiguous elements")
+    if not ok or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{what} must hold rows of {heads} heads of {head_dim} contiguous {dtype} elements on {device}")
     # (the stride of a single row says nothing: torch keeps whatever it was)
-    return stride[0] if shape[0] > 1 else heads * head_dim
-
-
-def _ints(t, shape, device, what: str):
-    import torch
-    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
-    return t.data_ptr()
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * head_dim
 
 
 class KvCache:
@@ -433,6 +424,10 @@ class KvCache:
         self._kv = _Kv(pool.data_ptr(), pool.device.index, types[pool.dtype], self.layers, self.pages, self.kv_heads,
                        self.page_size, self.head_dim)
         self._kvp = ctypes.byref(self._kv)
+        self._i32, self._i64, self._f32 = torch.int32, torch.int64, torch.float32
+        # (a decode step's calls are a few microseconds long: asking for the stream object would be a good part)
+        index, raw = pool.device.index, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(index).cuda_stream)
         need = ctypes.c_int64()
         _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
         self._ws_bytes, self._ws = need.value, {}
@@ -442,13 +437,17 @@ class KvCache:
 
     def _stream(self, stream):
         if stream is None:
-            import torch
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return self._current()
         return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _ints(self, t, shape, what: str):
+        if t.dtype is not self._i32 or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {self.device}")
+        return t.data_ptr()
 
     def _codes(self, status, n: int):
         if status is not None:
-            return _ints(status, (n,), self.device, "status")
+            return self._ints(status, (n,), "status")
         if n > self._status.numel():
             import torch
             self._status = torch.zeros(2 * n, dtype=torch.int32, device=self.device)
@@ -456,71 +455,73 @@ class KvCache:
         return self._status.data_ptr()
 
     def _tokens(self, n, cu, ctx_lens, page_table):
-        batch = ctx_lens.shape[0]
-        return _Tokens(batch, n, None if cu is None else _ints(cu, (batch + 1,), self.device, "cu_tokens"),
-                       _ints(ctx_lens, (batch,), self.device, "ctx_lens"),
-                       _ints(page_table, (batch, page_table.shape[-1]), self.device, "page_table"),
-                       page_table.shape[-1])
+        batch, width = page_table.shape
+        return _Tokens(batch, n, None if cu is None else self._ints(cu, (batch + 1,), "cu_tokens"),
+                       self._ints(ctx_lens, (batch,), "ctx_lens"), self._ints(page_table, (batch, width), "page_table"),
+                       width)
 
     def append(self, layer: int, qkv, cu_tokens, ctx_lens, page_table, q_out, q_weight=None, k_weight=None,
                eps: float = 1e-6, rope=None, positions=None, interleaved: bool = False, status=None, stream=None):
         """tc_kv_append: qkv [n, (q_heads + 2 kv_heads) * head_dim], q_out [n, q_heads, head_dim]; rope float32
         [positions, head_dim / 2, 2] (cosine, sine)."""
-        import torch
         d, n = self.head_dim, qkv.shape[0]
-        hq = q_out.shape[1] if q_out.dim() == 3 else q_out.shape[1] // d
-        if q_out.shape[0] != n:
+        out = q_out.shape
+        if out[0] != n:
             raise ValueError("q_out must have as many rows as qkv")
-        a = _Append(qkv.data_ptr(), _rows(qkv, self.dtype, self.device, "qkv", hq + 2 * self.kv_heads, d), hq, None,
-                    None, eps, None, 0, None, bool(interleaved), q_out.data_ptr(),
-                    _rows(q_out, self.dtype, self.device, "q_out", hq, d))
+        hq = out[1] if len(out) == 3 else out[1] // d
+        dtype, device = self.dtype, self.device
         for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                if w.dtype is not self.dtype or w.device != self.device or w.shape != (d,) or not w.is_contiguous():
-                    raise ValueError(f"{name} must be a contiguous {self.dtype} tensor of {d} elements")
-                setattr(a, name, w.data_ptr())
+            if w is not None and (w.dtype is not dtype or w.shape != (d,) or w.device != device or
+                                  not w.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of {d} elements")
+        angles = 0
         if rope is not None:
-            if (rope.dtype is not torch.float32 or rope.device != self.device or rope.dim() != 3 or
-                    rope.shape[1:] != (d // 2, 2) or not rope.is_contiguous()):
+            angles = rope.shape[0]
+            if rope.dtype is not self._f32 or rope.shape != (angles, d // 2, 2) or rope.device != device or \
+                    not rope.is_contiguous():
                 raise ValueError(f"rope must be a contiguous float32 tensor [positions, {d // 2}, 2]")
-            a.rope, a.rope_len = rope.data_ptr(), rope.shape[0]
-        if positions is not None:
-            a.positions = _ints(positions, (n,), self.device, "positions")
+        a = _Append(*_rows(qkv, dtype, device, "qkv", hq + 2 * self.kv_heads, d), hq,
+                    None if q_weight is None else q_weight.data_ptr(),
+                    None if k_weight is None else k_weight.data_ptr(), eps,
+                    None if rope is None else rope.data_ptr(), angles,
+                    None if positions is None else self._ints(positions, (n,), "positions"), bool(interleaved),
+                    *_rows(q_out, dtype, device, "q_out", hq, d))
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
-        _check(_kv_append(self._kvp, layer, ctypes.byref(t), ctypes.byref(a), self._codes(status, t.batch),
-                          self._stream(stream)), "tc_kv_append")
+        _check(_kv_append(self._kvp, layer, t, a, self._codes(status, t.batch), self._stream(stream)),
+               "tc_kv_append")
 
     def attend(self, layer: int, q, cu_tokens, ctx_lens, page_table, out, max_tokens: int, scale=None, tree=None,
                lse=None, status=None, stream=None):
         """tc_attend: q and out [n, q_heads, head_dim]; tree int64 [n, words] (tree_masks) or None for the causal
         mask; scale defaults to head_dim ** -0.5; lse float32 [n, q_heads] or None."""
-        import torch
-        d, n = self.head_dim, q.shape[0]
-        hq = q.shape[1] if q.dim() == 3 else q.shape[1] // d
+        d, shape = self.head_dim, q.shape
+        n = shape[0]
         if out.shape[0] != n:
             raise ValueError("out must have as many rows as q")
-        a = _Attend(q.data_ptr(), _rows(q, self.dtype, self.device, "q", hq, d), hq, max_tokens,
-                    d ** -0.5 if scale is None else scale, None, 0, out.data_ptr(),
-                    _rows(out, self.dtype, self.device, "out", hq, d), None)
+        hq = shape[1] if len(shape) == 3 else shape[1] // d
+        dtype, device = self.dtype, self.device
+        masks, words = None, 0
         if tree is not None:
-            if (tree.dtype is not torch.int64 or tree.device != self.device or tree.dim() != 2 or
-                    tree.shape[0] != n or not tree.is_contiguous()):
+            if tree.dtype is not self._i64 or tree.dim() != 2 or tree.shape[0] != n or tree.device != device or \
+                    not tree.is_contiguous():
                 raise ValueError("tree must be a contiguous int64 tensor [tokens, words]")
             # (a call without tokens has no mask to point at)
-            a.tree, a.tree_words = tree.data_ptr() or None, tree.shape[1]
+            masks, words = tree.data_ptr() or None, tree.shape[1]
+        sums = None
         if lse is not None:
-            if lse.dtype is not torch.float32 or lse.device != self.device or lse.shape != (n, hq) or \
-                    not lse.is_contiguous():
+            if lse.dtype is not self._f32 or lse.shape != (n, hq) or lse.device != device or not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
-            a.lse = lse.data_ptr()
-        a.wait_polls, a.withhold = self._wait_test
+            sums = lse.data_ptr()
+        a = _Attend(*_rows(q, dtype, device, "q", hq, d), hq, max_tokens, d ** -0.5 if scale is None else scale, masks,
+                    words, *_rows(out, dtype, device, "out", hq, d), sums, *self._wait_test)
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
         s = self._stream(stream)
         ws = self._ws.get(s)
         if ws is None:
-            ws = self._ws[s] = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
-        _check(_attend(self._kvp, layer, ctypes.byref(t), ctypes.byref(a), ws.data_ptr(), self._ws_bytes,
-                       self._codes(status, t.batch), s), "tc_attend")
+            import torch
+            ws = self._ws[s] = torch.empty(self._ws_bytes, dtype=torch.uint8, device=device)
+        _check(_attend(self._kvp, layer, t, a, ws.data_ptr(), self._ws_bytes, self._codes(status, t.batch), s),
+               "tc_attend")
 
     def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
         """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)
@@ -530,24 +531,30 @@ class KvCache:
     def copy_pages(self, src, dst, status=None, stream=None):
         """tc_kv_copy_pages: page dst[i] becomes page src[i] in every layer."""
         n = src.shape[0]
-        _check(_kv_copy_pages(self._kvp, _ints(src, (n,), self.device, "src"), _ints(dst, (n,), self.device, "dst"), n,
+        _check(_kv_copy_pages(self._kvp, self._ints(src, (n,), "src"), self._ints(dst, (n,), "dst"), n,
                               self._codes(status, n), self._stream(stream)), "tc_kv_copy_pages")
 
     def compact(self, page_table, ctx_lens, path, n_path, lens_out, status=None, stream=None):
         """tc_kv_compact: slot ctx_lens[b] + i takes what slot ctx_lens[b] + path[b, i] holds, i < n_path[b];
         lens_out = ctx_lens + n_path."""
         t = self._tokens(0, None, ctx_lens, page_table)
-        b = t.batch
-        _check(_kv_compact(self._kvp, ctypes.byref(t), _ints(path, (b, path.shape[-1]), self.device, "path"),
-                           path.shape[-1], _ints(n_path, (b,), self.device, "n_path"),
-                           _ints(lens_out, (b,), self.device, "lens_out"), self._codes(status, b),
-                           self._stream(stream)), "tc_kv_compact")
+        b, wide = t.batch, path.shape[-1]
+        _check(_kv_compact(self._kvp, t, self._ints(path, (b, wide), "path"), wide,
+                           self._ints(n_path, (b,), "n_path"), self._ints(lens_out, (b,), "lens_out"),
+                           self._codes(status, b), self._stream(stream)), "tc_kv_compact")
 
     def raise_on_error(self):
         """Wait for the device and raise the first error of the last call made without `status`."""
         for b, code in enumerate(self._status[:self._n_status].tolist()):
             if code != TC_OK:
                 raise TcError(code, f"sequence {b}")
+
+
+def _int_tensor(t, shape, device, what: str):
+    import torch
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
 
 
 def tree_masks(parents, cu_tokens, ctx_lens, masks, positions=None, status=None, stream=None):
@@ -559,12 +566,12 @@ def tree_masks(parents, cu_tokens, ctx_lens, masks, positions=None, status=None,
         raise ValueError("masks must be a contiguous int64 tensor [tokens, words]")
     if status is None:
         status = torch.empty(batch, dtype=torch.int32, device=dev)
-    t = _Tokens(batch, n, _ints(cu_tokens, (batch + 1,), dev, "cu_tokens"), _ints(ctx_lens, (batch,), dev, "ctx_lens"),
+    t = _Tokens(batch, n, _int_tensor(cu_tokens, (batch + 1,), dev, "cu_tokens"), _int_tensor(ctx_lens, (batch,), dev, "ctx_lens"),
                 None, 0)
     with torch.cuda.device(dev):
-        _check(_tree_masks(ctypes.byref(t), _ints(parents, (n,), dev, "parents"), masks.shape[1], masks.data_ptr(),
-                           None if positions is None else _ints(positions, (n,), dev, "positions"),
-                           _ints(status, (batch,), dev, "status"), _stream_ptr(stream)), "tc_tree_masks")
+        _check(_tree_masks(ctypes.byref(t), _int_tensor(parents, (n,), dev, "parents"), masks.shape[1], masks.data_ptr(),
+                           None if positions is None else _int_tensor(positions, (n,), dev, "positions"),
+                           _int_tensor(status, (batch,), dev, "status"), _stream_ptr(stream)), "tc_tree_masks")
     return status
 
 

@@ -17,11 +17,13 @@
 // CTA, which a second kernel joins.
 //
 // One CTA, 16 warps:
-//  - warp 0 loads: queries, then key and value tiles, into a ring of 128 x
-//    head_dim tiles by TMA (128-byte swizzle; one copy per page piece and 64
-//    columns; pages past the sequence's end are not loaded);
+//  - warps 0, 5 and 7 load keys, values and queries by TMA (128-byte swizzle),
+//    keys and values in turn into one ring of 128 x head_dim tiles, a copy per
+//    page (per page and 64 columns where the pages are smaller than a step);
+//    pages past the sequence's end are not loaded.  A copy takes a warp long
+//    enough to issue that one warp for all three would set the pace;
 //  - warps 1 and 3 issue the score products S = Q K^T of one softmax group each
-//    (both operands in shared memory), warps 4 and 5 the output products
+//    (both operands in shared memory), warps 4 and 6 the output products
 //    O += P V (P in tensor memory), in steps of 64 slots (head_dim 128) or 128
 //    (64).  One thread each, which does nothing but wait for its operands and
 //    issue: an issuer with several things to look at reacts too late;
@@ -56,6 +58,7 @@
 #include <cudaTypedefs.h>
 
 #include <climits>
+#include <cstddef>
 
 #include "kv_cache.h"
 
@@ -79,7 +82,8 @@ struct Cfg {
   static constexpr int kStep = D == 128 ? 64 : 128;  // slots of a step
   static constexpr int kSteps = kTile / kStep;       // steps of a tile
   // Tensor memory of a group: scores, weights, accumulator.
-  static constexpr uint32_t kP = kStep, kO = kP + kStep / 2, kCols = 256;
+  static constexpr int kPs = D == 128 ? 2 : 1;  // places of the weights
+  static constexpr uint32_t kP = kStep, kO = kP + kPs * (kStep / 2), kCols = 256;
   static_assert(kO + D <= kCols, "tensor memory of a group");
 };
 
@@ -101,6 +105,10 @@ struct AttendParams {
   int32_t q_heads, group, tile_tokens;  // tile_tokens = 128 / group
   int32_t max_tokens;
   int32_t q_rows;                       // rows of one query load
+  // Places in a key-value tile of a step and of 64 columns: a copy brings all
+  // columns of a page (merged) or 64 of them.
+  int32_t merged;
+  uint32_t step_stride, half_stride;
   float c;                              // |scale| log2(e), the factor of the exponents
   int32_t negate;                       // the scale is negative
   const int64_t* tree;
@@ -121,24 +129,25 @@ struct AttendParams {
 constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile; }
 
 struct Hdr {
-  // Key-value ring (twice as many "full" barriers as stages) and query tiles
-  // (four for two places): a waiter looks at its own turns only, and a parity
+  // Key-value ring (twice as many barriers as stages) and query tiles (four for
+  // two places): a waiter looks at its own turns only, and a parity
   // tells a phase from the one before only if that one is known to be over.
   // It is: a place is filled when the one before in the same place has been
   // handed back, so what lies a whole ring further back than the waiter's
   // last turn is done.
-  uint64_t full[20], empty[10];
+  uint64_t full[20], empty[20];
   uint64_t q_full[4], q_empty[2];
-  uint64_t s_full[2], s_read[2], p_ready[2], pv_done[2], o_full[2];
+  uint64_t s_full[2], o_full[2];
+  uint64_t s_read[2], p_ready[2][2];  // (two: by step, even and odd)
+  uint64_t pv_done[2][2];
   uint64_t o_free;                   // both groups have read the accumulators
   uint64_t meet;                     // both groups
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t drain;
   uint32_t tmem_base;
   int32_t abort;
-  int64_t total;                     // units of the call
   int64_t off0;                      // the worker's first unit within its sequence
-  int32_t seq0;
+  int32_t seq0, row0, n0, ctx0;      // its sequence
   uint32_t bad[2][8];                // tokens whose values are not finite, by segment parity
   Seg seg[kSegs];
   float2 ml[2][kTile];               // (the prologue's sums before the first segment)
@@ -194,12 +203,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long lo
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit, volatile int32_t* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
-__device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap* map, int x, int slot, int head, int page,
+__device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap* map, int slot, int half, int head, int page,
                                        uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(slot), "r"(half), "r"(head), "r"(page), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar) {
@@ -215,14 +224,13 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // Shared-memory matrix descriptors, 128-byte swizzle.  K-major (queries,
 // keys): rows of 128 bytes, groups of 8 rows 1024 bytes apart.  N-major
 // (values: a row is one slot, the columns are N): groups of 8 slots 1024 bytes
-// apart (stride offset), blocks of 64 columns a half tile apart (leading
-// offset).
+// apart (stride offset), blocks of 64 columns further apart (leading offset).
 __device__ __forceinline__ uint64_t desc_k_major(uint32_t a) {
   return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t a) {
-  return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(kHalfBytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t a, uint32_t half_stride) {
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(half_stride >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // Instruction descriptor of kind::f16: 32-bit accumulator, M = 128.
@@ -367,9 +375,13 @@ struct Line {
     if (!causal || i == 0) return (int64_t)i * (tiles(0) + extra);
     return floor_sum(i, kTile, step, (int64_t)ctx + step + kTile - 1) + (int64_t)i * extra;
   }
-  __device__ int64_t units() const { return n > 0 ? before(items() - 1) + tiles(items() - 1) + extra : 0; }
+  __device__ int64_t units() const {
+    if (n <= step) return n > 0 ? tiles(0) + extra : 0;  // (one item)
+    return before(items() - 1) + tiles(items() - 1) + extra;
+  }
   // the item that unit u is in
   __device__ int item_of(int64_t u) const {
+    if (n <= step) return 0;
     if (!causal) return (int)div64(u, tiles(0) + extra);
     int lo = 0, hi = items();
     while (hi - lo > 1) {
@@ -522,29 +534,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  if (tid == 0) {
-    for (int i = 0; i < 2 * NS; ++i) mbar_init(smem_u32(&hdr->full[i]), 1);
-    for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&hdr->empty[i]), 2);  // a commit per group, or two of one
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&hdr->q_full[i]), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&hdr->q_empty[i]), 8);  // eight softmax warps (four of them twice)
-      mbar_init(smem_u32(&hdr->s_full[i]), 1);
-      mbar_init(smem_u32(&hdr->s_read[i]), kTile);
-      mbar_init(smem_u32(&hdr->p_ready[i]), kTile);
-      mbar_init(smem_u32(&hdr->pv_done[i]), 1);
-      mbar_init(smem_u32(&hdr->o_full[i]), 1);
-    }
-    mbar_init(smem_u32(&hdr->o_free), 2 * kTile);
-    mbar_init(smem_u32(&hdr->meet), 2 * kTile);
-    for (int i = 0; i < kSegs; ++i) {
-      mbar_init(smem_u32(&hdr->seg_full[i]), 1);
-      mbar_init(smem_u32(&hdr->seg_empty[i]), 5 + 8);  // loader, four issuers, eight softmax warps
-    }
-    mbar_init(smem_u32(&hdr->drain), 4);
+  // Arrivals that complete a phase of each barrier (a thread each: one thread
+  // for all of them takes a microsecond).
+  constexpr int kBars = offsetof(Hdr, tmem_base) / 8;
+  static_assert(kBars <= kThreads, "barriers");
+  if (tid < kBars) {
+    const uint32_t at = tid * 8;
+    uint32_t n = 1;
+    if (at >= offsetof(Hdr, empty) && at < offsetof(Hdr, q_full)) n = 2;      // a commit per group, or two of one
+    if (at >= offsetof(Hdr, q_empty) && at < offsetof(Hdr, s_full)) n = 8;    // softmax warps (or four, twice)
+    if (at >= offsetof(Hdr, s_read) && at < offsetof(Hdr, pv_done)) n = kTile;  // a group's threads
+    if (at >= offsetof(Hdr, o_free) && at < offsetof(Hdr, seg_full)) n = 2 * kTile;
+    if (at >= offsetof(Hdr, seg_empty) && at < offsetof(Hdr, drain)) n = 7 + 8;  // loaders, issuers, softmax warps
+    if (at == offsetof(Hdr, drain)) n = 4;
+    mbar_init(smem_u32(hdr) + at, n);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == kBars) {
     hdr->abort = 0;
     hdr->seq0 = -1;
     for (int i = 0; i < 16; ++i) hdr->bad[i >> 3][i & 7] = 0u;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_kv)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
   }
@@ -616,6 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t u = l.units() * p.kv.kv_heads;
       if (begin < at + u) {
         hdr->seq0 = b;
+        hdr->row0 = s.row0;
+        hdr->n0 = s.n;
+        hdr->ctx0 = s.ctx;
         hdr->off0 = begin - at;
         break;
       }
@@ -625,18 +637,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tmem = hdr->tmem_base;
   const bool held = p.withhold != 0 && worker == 0;
-  uint32_t armed = 0;  // loader: key-value stages armed, for the exit path
-  uint32_t q_armed = 0;
+  uint32_t armed = 0;  // loaders: tiles armed, for the exit path
   // Registers: 512 threads launch with 128 each, 65,536 together; a softmax
   // thread holds a step's row of scores (128 at head_dim 64) and takes 200, the
   // others keep 56 (56 * 256 + 200 * 256 = 65,536).
   if (warp < 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 0) {
-    // ------------------------------------------------------------- loader
-    uint32_t it = 0, qi = 0;
-    const int box = min(p.kv.page_size, kTile), pieces = kTile / box;
-    const int piece = lane / C::kHalves, half = lane % C::kHalves;
+  if (warp == 0 || warp == 5) {
+    // ------------------------------------------- loaders of keys and values
+    // The warp's t-th tile lies in place 2 t (keys) or 2 t + 1 (values) of the ring.
+    const uint32_t is_v = warp == 5;
+    const int box = p.kv.page_size, pieces = kTile / box, copies = p.merged ? 1 : C::kHalves;
+    const int piece = lane / copies, half = lane % copies;
+    const uint32_t dst = kv_s + (p.merged ? piece * box * 128 * C::kHalves : half * kHalfBytes + piece * box * 128);
+    const uint32_t bytes = (uint32_t)(box * 128 * C::kHalves / copies);  // of one copy
     bool stop = false;
     for (int k = 0; !stop; ++k) {
       if (!warp_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
@@ -644,42 +658,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
       if (!g.valid) break;
-      for (int m = 0; m <= g.two; ++m, ++qi) {
-        if (!warp_wait(smem_u32(&hdr->q_empty[qi & 1]), ((qi >> 1) & 1) ^ 1, wl, abort)) {
-          stop = true;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&hdr->q_full[qi & 3]);
-          mbar_expect_tx(bar, (uint32_t)p.q_rows * 128u * C::kHalves);
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_q(q_s + (qi & 1) * C::kTileBytes + h * kHalfBytes, &map_q, h * 64, g.head * p.group,
-                  g.row0 + g.tok0 + m * p.tile_tokens, bar);
-        }
-        ++q_armed;
-      }
-      if (stop) break;
-      const int n = g.t1 - g.t0;
       const int32_t* row = p.tok.table + (int64_t)g.seq * p.tok.width;
-      for (int j = 0; j < 2 * n && !stop; ++j, ++it) {
-        const int slot = (g.t0 + (j >> 1)) * kTile + piece * box;  // K0 V0 K1 V1 ...
-        const bool load = piece < pieces && slot < g.end;
-        const int page = load ? __ldg(row + (slot >> p.kv.page_shift)) : 0;
-        const int stage = (int)(it % NS);
-        if (!warp_wait(smem_u32(&hdr->empty[stage]), ((it / NS) & 1) ^ 1, wl, abort)) {
+      const int head = (is_v ? p.kv.kv_heads : 0) + g.head;
+      int slot = g.t0 * kTile + piece * box;
+      bool load = piece < pieces && slot < g.end;
+      int page = load ? __ldg(row + (slot >> p.kv.page_shift)) : 0;
+      for (int t = g.t0; t < g.t1; ++t, ++armed) {
+        // (the next tile's pages are looked up before this one's place is waited for)
+        const int slot2 = slot + kTile;
+        const bool load2 = piece < pieces && slot2 < g.end && t + 1 < g.t1;
+        const int page2 = load2 ? __ldg(row + (slot2 >> p.kv.page_shift)) : 0;
+        const uint32_t at = 2 * armed + is_v, before = at - NS;
+        if (at >= NS && !warp_wait(smem_u32(&hdr->empty[before % (2 * NS)]), (before / (2 * NS)) & 1, wl, abort)) {
           stop = true;
           break;
         }
-        const uint32_t bar = smem_u32(&hdr->full[it % (2 * NS)]);
-        const int count = __popc(__ballot_sync(0xffffffffu, load));
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)(count * box * 128));
+        const uint32_t bar = smem_u32(&hdr->full[at % (2 * NS)]);
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, load));
+        if (lane == 0) mbar_expect_tx(bar, count * bytes);
         __syncwarp();
-        if (load && !(held && it == 0))
-          tma_kv(kv_s + stage * C::kTileBytes + half * kHalfBytes + piece * box * 128, &map_kv, half * 64,
-                 slot & (p.kv.page_size - 1), ((j & 1) ? p.kv.kv_heads : 0) + g.head, page, bar);
-        ++armed;
+        if (load && !(held && at == 0))
+          tma_kv(dst + at % NS * C::kTileBytes, &map_kv, slot & (p.kv.page_size - 1), half, head, page, bar);
+        slot = slot2;
+        load = load2;
+        page = page2;
       }
     }
+  } else if (warp == 7) {
+    // -------------------------------------------------- loader of queries
+    if (lane == 0) {
+      bool stop = false;
+      for (int k = 0; !stop; ++k) {
+        if (!mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
+        const Seg g = hdr->seg[k % kSegs];
+        mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
+        if (!g.valid) break;
+        for (int m = 0; m <= g.two; ++m, ++armed) {
+          if (!mbar_wait(smem_u32(&hdr->q_empty[armed & 1]), ((armed >> 1) & 1) ^ 1, wl, abort)) {
+            stop = true;
+            break;
+          }
+          const uint32_t bar = smem_u32(&hdr->q_full[armed & 3]);
+          mbar_expect_tx(bar, (uint32_t)p.q_rows * 128u * C::kHalves);
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_q(q_s + (armed & 1) * C::kTileBytes + h * kHalfBytes, &map_q, h * 64, g.head * p.group,
+                  g.row0 + g.tok0 + m * p.tile_tokens, bar);
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp == 1 || warp == 3 || warp == 4 || warp == 6) {
     // ------------------------------------------------------------ issuers
     if (lane == 0) {
@@ -696,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       };
       // The stage is handed back when the products so far are done.
-      auto release = [&](uint32_t stage, bool two) {
-        mma_commit(smem_u32(&hdr->empty[stage]));
-        if (!two) mma_commit(smem_u32(&hdr->empty[stage]));
+      auto release = [&](uint32_t at, bool two) {
+        mma_commit(smem_u32(&hdr->empty[at % (2 * NS)]));
+        if (!two) mma_commit(smem_u32(&hdr->empty[at % (2 * NS)]));
       };
       for (int k = 0; ok; ++k) {
         if (!wait(&hdr->seg_full[k % kSegs], k / kSegs)) break;
@@ -717,16 +744,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < steps; ++u, ++done) {
               // (the scores before have been read)
               if (done > 0 && !wait(&hdr->s_read[slot], done - 1)) break;
-              const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + u * (C::kStep * 128));
+              const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + u * p.step_stride);
               tc_fence_after();
 #pragma unroll
               for (int e = 0; e < D / 16; ++e) {
-                const uint32_t o = ((uint32_t)(e >> 2) * kHalfBytes + (uint32_t)(e & 3) * 32) >> 4;
-                mma_ss(t_s, q_desc + o, b + o, id_s, e > 0);
+                const uint32_t o = (uint32_t)(e & 3) * 2, h = e >> 2;
+                mma_ss(t_s, q_desc + h * (kHalfBytes >> 4) + o, b + h * (p.half_stride >> 4) + o, id_s, e > 0);
               }
               mma_commit(smem_u32(&hdr->s_full[slot]));
             }
-            release(stage, g.two);
+            release(at, g.two);
           }
         } else {
           // (the accumulators of the segment before have been read)
@@ -736,18 +763,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int steps = steps_of<D>(g, g.t0 + i);
             if (!wait(&hdr->full[at % (2 * NS)], at / (2 * NS))) break;
             for (int u = 0; u < steps; ++u, ++done) {
-              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + u * (C::kStep * 128));
+              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + u * p.step_stride, p.half_stride);
               // over the 16-slot groups that the step has
               const int groups = (step_slots<D>(g, (g.t0 + i) * kTile + u * C::kStep) + 15) / 16;
               const bool more = i > i0 || u > 0;
-              if (!wait(&hdr->p_ready[slot], done)) break;
+              const uint32_t p_at = t_p + done % C::kPs * (C::kStep / 2);
+              if (!wait(&hdr->p_ready[slot][done & 1], done >> 1)) break;
               tc_fence_after();
 #pragma unroll
               for (int e = 0; e < C::kStep / 16; ++e)
-                if (e < groups) mma_ts(t_o, t_p + e * 8, b + e * (2048 >> 4), id_o, more || e > 0);
-              mma_commit(smem_u32(&hdr->pv_done[slot]));
+                if (e < groups) mma_ts(t_o, p_at + e * 8, b + e * (2048 >> 4), id_o, more || e > 0);
+              mma_commit(smem_u32(&hdr->pv_done[slot][done & 1]));
             }
-            release(stage, g.two);
+            release(at, g.two);
           }
           mma_commit(smem_u32(&hdr->o_full[slot]));
         }
@@ -767,16 +795,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok) {
         Seg g{};
         if (left > 0) {
-          SeqSpan s;
-          Line l;
-          // (sequences without units are passed over)
+          SeqSpan s{hdr->row0, hdr->n0, hdr->ctx0};
+          Line l{s.n, s.ctx, 2 * p.tile_tokens, p.tree == nullptr, extra};
           int64_t per = 0;
-          while (b < p.tok.batch) {
-            if (line_of(p, b, extra, &s, &l) && (per = l.units()) * p.kv.kv_heads > off) break;
-            off = 0;
-            ++b;
+          if (b == hdr->seq0) {
+            per = l.units();
+          } else {
+            // (sequences without units are passed over)
+            while (b < p.tok.batch && !(line_of(p, b, extra, &s, &l) && (per = l.units()) > 0)) ++b;
+            if (b >= p.tok.batch) break;  // (cannot be: the units add up)
           }
-          if (b >= p.tok.batch) break;  // (cannot be: the units add up)
           const int head = (int)div64(off, per);
           int64_t r = off - head * per;
           int item = l.item_of(r);
@@ -883,11 +911,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&hdr->s_read[grp]));
       };
-      // The P V of the step before is done: its weights' place is free and the
-      // accumulator at rest.  (Warps without rows wait as well: a warp must not
-      // announce a step's weights before the group's others have the last one's.)
-      auto rested = [&]() {
-        return n_s == 0 || mbar_wait(smem_u32(&hdr->pv_done[grp]), (n_s - 1) & 1, wl, abort);
+      // The output product `back` steps ago is done.  kPs steps ago: its weights'
+      // place is free.  (Warps without rows wait as well: a warp must not
+      // announce a step's weights before the group's others have announced those
+      // that were in the same place.)  One step ago: the accumulator is at rest.
+      auto product_done = [&](uint32_t back) {
+        const uint32_t j = n_s - back;
+        return n_s < back || mbar_wait(smem_u32(&hdr->pv_done[grp][j & 1]), (j >> 1) & 1, wl, abort);
       };
       // Weights of a step's scores.
       auto weigh = [&](const uint32_t(&s)[W]) {
@@ -898,13 +928,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 4; j < W; j += 2)
           mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        const bool ok = rested();
+        bool ok = product_done(C::kPs);
         tc_fence_after();
         // Move the reference maximum only for a large growth (the first finite
         // score's among them); the accumulator exists from the second step on.
         const bool grow = (top - m) * p.c > kRescale;
         if (__any_sync(0xffffffffu, grow)) {
           if (!first) {
+            if (C::kPs > 1) {
+              ok &= product_done(1);
+              __syncwarp();
+              tc_fence_after();
+            }
             const float f = grow ? ex2((m - top) * p.c) : 1.f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -938,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[j & 1] = add2(sum[j & 1], f2(a, b));
             pk[j] = T::pack(a, b);
           }
-          tmem_st16(t_p + q * 16, pk);
+          tmem_st16(t_p + n_s % C::kPs * (W / 2) + q * 16, pk);
         }
         const float2 t = unf2(add2(sum[0], sum[1]));
         l += t.x + t.y;
@@ -946,14 +981,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       };
       // Steps that every row sees entirely, then those that some row does not.
-      // (In the first loop a wait that ran out is noticed at the step's end:
+      // (In the first loop a wait that ran out is noticed at the tile's end:
       // nothing in between leaves its bounds.)
       int i = g.two ? 0 : grp, u = 0;
       for (; i < n && !stop; i += hop) {
         const int steps = steps_of<D>(g, g.t0 + i);
         const int full = min(steps, max(0, hidden - (g.t0 + i) * kTile) / W);
+        bool ok = true;
         for (u = 0; u < full; ++u, ++n_s) {
-          bool ok = mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort);
+          ok &= mbar_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort);
           if (any) {
             __syncwarp();
             tc_fence_after();
@@ -963,14 +999,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
           } else {
             mbar_arrive(smem_u32(&hdr->s_read[grp]));
-            ok &= rested();
+            ok &= product_done(C::kPs);
           }
-          mbar_arrive(smem_u32(&hdr->p_ready[grp]));
-          if (!__all_sync(0xffffffffu, ok)) {
-            stop = true;
-            break;
-          }
+          mbar_arrive(smem_u32(&hdr->p_ready[grp][n_s & 1]));
         }
+        stop = !__all_sync(0xffffffffu, ok);
         if (full < steps) break;
       }
       if (stop) break;
@@ -997,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = weigh(s);
           } else {
             mbar_arrive(smem_u32(&hdr->s_read[grp]));
-            ok = rested();
+            ok = product_done(C::kPs);
           }
           if (!__all_sync(0xffffffffu, ok)) {
             stop = true;
@@ -1016,17 +1049,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the rest of its group of 16 slots is read.
             const int j = r % W, slot = start + j;
             const int c0 = r / W * 8 + (g.two ? grp * 4 : 0), c1 = c0 + (g.two ? 4 : 8);
-            const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + (u * W + j) * 128;
+            const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + u * p.step_stride + j * 128;
             if (slot >= g.end) {
               if (j < ((slots + 15) & ~15))
 #pragma unroll 4
                 for (int c = c0; c < c1; ++c)
-                  sts128(row + (c >> 3) * kHalfBytes + (((c ^ j) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+                  sts128(row + (c >> 3) * p.half_stride + (((c ^ j) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
             } else if (slot >= hidden) {
               bool found = false;
 #pragma unroll 1
               for (int c = c0; c < c1; c += 4) {
-                const uint32_t at = row + (c >> 3) * kHalfBytes;
+                const uint32_t at = row + (c >> 3) * p.half_stride;
                 uint4 v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = lds128(at + ((((c + e) ^ j) & 7) << 4));
@@ -1055,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_before();
-          mbar_arrive(smem_u32(&hdr->p_ready[grp]));
+          mbar_arrive(smem_u32(&hdr->p_ready[grp][n_s & 1]));
         }
       }
       if (stop) break;
@@ -1169,11 +1202,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int32_t none = 0;
       mbar_wait(smem_u32(&hdr->drain), 0u, wl, &none);
     }
-    if (warp == 0 && lane == 0) {
+    if ((warp == 0 || warp == 5) && lane == 0) {
       int32_t none = 0;
-      for (uint32_t j = armed > (uint32_t)NS ? armed - NS : 0; j < armed; ++j)
-        if (!(held && j == 0)) mbar_wait(smem_u32(&hdr->full[j % (2 * NS)]), (j / (2 * NS)) & 1, wl, &none);
-      for (uint32_t j = q_armed > 2 ? q_armed - 2 : 0; j < q_armed; ++j)
+      constexpr uint32_t most = (NS + 1) / 2;  // tiles of one loader in the ring
+      for (uint32_t t = armed > most ? armed - most : 0; t < armed; ++t) {
+        const uint32_t at = 2 * t + (warp == 5);
+        if (!(held && at == 0)) mbar_wait(smem_u32(&hdr->full[at % (2 * NS)]), (at / (2 * NS)) & 1, wl, &none);
+      }
+    }
+    if (warp == 7 && lane == 0) {
+      int32_t none = 0;
+      for (uint32_t j = armed > 2 ? armed - 2 : 0; j < armed; ++j)
         mbar_wait(smem_u32(&hdr->q_full[j & 3]), (j >> 2) & 1, wl, &none);
     }
     __syncwarp();
@@ -1190,45 +1229,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinThreads = 256, kJoinBlocks = 8;
 
-// Blocks (w, y), w < workers: the item that starts in worker w and goes on in
+// kJoinBlocks blocks for each worker: the item that starts in it and goes on in
 // the next.  A thread joins four columns of a row (the parts are laid out by
 // columns, so neighbouring rows are neighbours); the parts are added in the
-// order of the workers: the result does not depend on timing.  Blocks past the
-// workers write the status of eight sequences each.
+// order of the workers: the result does not depend on timing.  The blocks
+// after these write the status of a sequence each.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x >= (unsigned)p.workers) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = (blockIdx.x - p.workers) * (kJoinThreads / 32) + warp;
-    if (blockIdx.y != 0 || b >= p.tok.batch) return;
+  if (blockIdx.x >= (unsigned)(p.workers * kJoinBlocks)) {
+    const int b = blockIdx.x - p.workers * kJoinBlocks;
     SeqSpan s;
     bool ok = seq_span(p.tok, p.kv.page_size, b, &s) && s.n <= p.max_tokens;
-    if (ok && s.n > 0)
-      for (int i = lane; i <= (s.ctx + s.n - 1) >> p.kv.page_shift; i += 32)
-        ok &= (uint32_t)__ldg(p.tok.table + (int64_t)b * p.tok.width + i) < (uint32_t)p.kv.pages;
+    const int pages = ok && s.n > 0 ? (s.ctx + s.n - 1) / p.kv.page_size + 1 : 0;
+    const int32_t* row = p.tok.table + (int64_t)b * p.tok.width;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < pages; i += kJoinThreads) ok &= (uint32_t)__ldg(row + i) < (uint32_t)p.kv.pages;
     bool late = false;
-    for (int i = lane; i < p.workers; i += 32) late |= p.errs[i] != 0;
-    ok = __all_sync(0xffffffffu, ok);
-    late = __any_sync(0xffffffffu, late);
-    if (lane == 0) p.status[b] = late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS;
+    for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) late |= __ldcg(p.errs + i) != 0;
+    ok = __syncthreads_and(ok);
+    late = __syncthreads_or(late);
+    if (threadIdx.x == 0) p.status[b] = late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS;
     return;
   }
-  const int w0 = blockIdx.x;
+  const int w0 = blockIdx.x / kJoinBlocks, y = blockIdx.x % kJoinBlocks;
   const Seg g = p.descs[w0];
   if (!g.valid) return;
   const int full = p.tile_tokens * p.group, left = (g.n - g.tok0) * p.group;
   const int v0 = min(left, full), rows = g.two ? min(left, 2 * full) : v0;  // rows of the first M tile, of both
-  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * (D / 4); i += kJoinBlocks * kJoinThreads) {
+  for (int i = y * kJoinThreads + threadIdx.x; i < rows * (D / 4); i += kJoinBlocks * kJoinThreads) {
     const int c = i / rows, k = i % rows;            // columns 4 c .. 4 c + 3 of row k
     const int rr = k < v0 ? k : kTile + k - v0;      // its place in a part
     auto at = [&](int w) { return ((size_t)w * 2 + (w == w0)) * 2 * kTile; };
     float m = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
     for (int w = w0; w <= g.last; ++w) m = fmaxf(m, __ldcg(&p.part_ml[at(w) + rr].x));
     float l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int w = w0; w <= g.last; ++w) {
       const float2 ml = __ldcg(p.part_ml + at(w) + rr);
       const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(w) * D) + (size_t)c * (2 * kTile) + rr);
@@ -1268,7 +1306,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 bool encode(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   return fn && fn(m, dtype == TC_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1319,8 +1357,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorM
   cfg.dynamicSmemBytes = smem_bytes<D>();
   e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D>, p, kv, q);
   if (e != cudaSuccess) return e;
-  constexpr int per = kJoinThreads / 32;
-  cfg.gridDim = dim3((unsigned)(p.workers + (p.tok.batch + per - 1) / per), kJoinBlocks);
+  cfg.gridDim = dim3((unsigned)(p.workers * kJoinBlocks + p.tok.batch));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p);
@@ -1368,12 +1405,16 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
                    "a row");
   KvDevice dev(kv->device);
   if (!dev.ok) return kv_fail(TC_ERR_CUDA, "tc_attend: cannot use the cache's device");
-  // Keys and values of the layer: [page][keys or values, head][slot][element].
+  // Keys and values of the layer: [page][keys or values, head][slot][element],
   const KvView v = kv_view(kv, layer);
   const cuuint64_t d = (cuuint64_t)kv->head_dim, sz = (cuuint64_t)kv->page_size;
-  const cuuint64_t kv_dims[4] = {d, sz, (cuuint64_t)2 * kv->kv_heads, (cuuint64_t)kv->pages};
-  const cuuint64_t kv_strides[3] = {d * 2, sz * d * 2, (cuuint64_t)2 * kv->kv_heads * sz * d * 2};
-  const cuuint32_t kv_box[4] = {64, (cuuint32_t)kv->page_size, 1, 1};
+  // in pieces of 64 columns.  A copy brings a page's slots; where a page holds
+  // whole steps (64 slots at head_dim 128), all its columns at once.
+  const int halves = kv->head_dim / 64;
+  const bool merged = halves == 2 && kv->page_size >= 64;
+  const cuuint64_t kv_dims[5] = {64, sz, (cuuint64_t)halves, (cuuint64_t)2 * kv->kv_heads, (cuuint64_t)kv->pages};
+  const cuuint64_t kv_strides[4] = {d * 2, 128, sz * d * 2, (cuuint64_t)2 * kv->kv_heads * sz * d * 2};
+  const cuuint32_t kv_box[5] = {64, (cuuint32_t)kv->page_size, merged ? 2u : 1u, 1, 1};
   const int group = a->q_heads / kv->kv_heads, tile_tokens = kTile / group;
   // Queries: rows (token, head of the group) of one M tile, at most max_tokens of them.
   const int q_tokens = a->max_tokens < 1 ? 1 : a->max_tokens < tile_tokens ? a->max_tokens : tile_tokens;
@@ -1382,7 +1423,7 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   const cuuint64_t q_strides[2] = {d * 2, (cuuint64_t)(none ? row : a->q_stride) * 2};
   const cuuint32_t q_box[3] = {64, (cuuint32_t)group, (cuuint32_t)q_tokens};
   CUtensorMap map_kv, map_q;
-  if (!encode(&map_kv, kv->dtype, 4, v.base, kv_dims, kv_strides, kv_box) ||
+  if (!encode(&map_kv, kv->dtype, 5, v.base, kv_dims, kv_strides, kv_box) ||
       !encode(&map_q, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, q_box))
     return kv_fail(TC_ERR_UNSUPPORTED, "tc_attend: the sizes or strides do not fit a tensor map");
   AttendParams p{};
@@ -1393,6 +1434,10 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   p.tile_tokens = tile_tokens;
   p.max_tokens = a->max_tokens;
   p.q_rows = group * q_tokens;
+  p.merged = merged;
+  const bool page_is_step = merged && kv->page_size == 64;  // then a step's columns lie together
+  p.half_stride = page_is_step ? kHalfBytes / 2 : kHalfBytes;
+  p.step_stride = page_is_step ? kHalfBytes : kHalfBytes / 2;
   // A scale of zero weighs all slots alike; as a factor so small that every
   // product with a score is nothing, it keeps -inf times the factor -inf.
   p.c = fmaxf(fabsf(a->scale) * 1.4426950408889634f, 1e-30f);
