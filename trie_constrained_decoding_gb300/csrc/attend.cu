@@ -70,7 +70,6 @@ constexpr int kThreads = 512;
 constexpr uint32_t kHalfBytes = kTile * 128; // 128 rows of 64 elements
 constexpr float kRescale = 8.f;             // log2 of the growth that moves the reference maximum
 constexpr int kSegs = 4;                    // segments ahead of the softmax groups
-constexpr int kItemCost = 2;                // an item's beginning and end, in tiles
 constexpr long long kWaitLimit = 1ll << 22; // default polls of one wait before giving up
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -81,6 +80,7 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kStep = D == 128 ? 64 : 128;  // slots of a step
   static constexpr int kSteps = kTile / kStep;       // steps of a tile
+  static constexpr int kItemCost = D == 128 ? 3 : 4; // an item's beginning and end, in tiles (measured)
   // Tensor memory of a group: scores, weights, accumulator.
   static constexpr int kPs = D == 128 ? 2 : 1;  // places of the weights
   static constexpr uint32_t kP = kStep, kO = kP + kPs * (kStep / 2), kCols = 256;
@@ -115,6 +115,7 @@ struct AttendParams {
   int32_t words;
   uint8_t* out;
   int64_t out_stride;
+  int32_t wide_out;                     // 32-byte stores are aligned
   float* lse;
   int32_t* status;
   int32_t workers;
@@ -148,7 +149,7 @@ struct Hdr {
   int32_t abort;
   int64_t off0;                      // the worker's first unit within its sequence
   int32_t seq0, row0, n0, ctx0;      // its sequence
-  uint32_t bad[2][8];                // tokens whose values are not finite, by segment parity
+  uint32_t bad[3][8];                // tokens whose values are not finite, by segment
   Seg seg[kSegs];
   float2 ml[2][kTile];               // (the prologue's sums before the first segment)
 };
@@ -168,9 +169,6 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -322,6 +320,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void stg256(void* a, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -495,19 +498,6 @@ __device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& 
     }
 }
 
-// Writes a warp's 32 finished rows, WORDS 16-byte words of each from word `w0`,
-// from shared memory to byte `at` of the output (< 0: not a row).
-template <int WORDS>
-__device__ __forceinline__ void flush_rows(uint8_t* out, uint32_t stage, int row0, int w0, int64_t at, int lane) {
-#pragma unroll 4
-  for (int i = 0; i < WORDS; ++i) {
-    const int row = (i * 32 + lane) / WORDS, w = w0 + lane % WORDS, rw = row0 + row;
-    const int64_t a = __shfl_sync(0xffffffffu, at, row);
-    const uint4 v = lds128(stage + rw * 128 + (w >> 3) * kHalfBytes + ((w ^ rw) & 7) * 16);
-    if (a >= 0) *reinterpret_cast<uint4*>(out + a + w * 16) = v;
-  }
-}
-
 // ------------------------------------------------------------------- kernel
 
 template <typename T, int D>
@@ -542,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = tid * 8;
     uint32_t n = 1;
     if (at >= offsetof(Hdr, empty) && at < offsetof(Hdr, q_full)) n = 2;      // a commit per group, or two of one
-    if (at >= offsetof(Hdr, q_empty) && at < offsetof(Hdr, s_full)) n = 8;    // softmax warps (or four, twice)
+    if (at >= offsetof(Hdr, q_empty) && at < offsetof(Hdr, s_full)) n = 2;
     if (at >= offsetof(Hdr, s_read) && at < offsetof(Hdr, pv_done)) n = kTile;  // a group's threads
     if (at >= offsetof(Hdr, o_free) && at < offsetof(Hdr, seg_full)) n = 2 * kTile;
     if (at >= offsetof(Hdr, seg_empty) && at < offsetof(Hdr, drain)) n = 7 + 8;  // loaders, issuers, softmax warps
@@ -553,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == kBars) {
     hdr->abort = 0;
     hdr->seq0 = -1;
-    for (int i = 0; i < 16; ++i) hdr->bad[i >> 3][i & 7] = 0u;
+    for (int i = 0; i < 24; ++i) hdr->bad[i >> 3][i & 7] = 0u;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_kv)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
   }
@@ -608,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     all_items += sums[kThreads / 32 + i];
   }
   // With little to do every worker gets tiles first of all.
-  const int extra = all_tiles >= 8 * (int64_t)p.workers ? kItemCost : 0;
+  const int extra = all_tiles >= 8 * (int64_t)p.workers ? C::kItemCost : 0;
   const int64_t total = all_tiles + extra * all_items;
   const int active = (int)min((int64_t)p.workers, total);
   const Cut cut(total, active);
@@ -638,11 +628,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = hdr->tmem_base;
   const bool held = p.withhold != 0 && worker == 0;
   uint32_t armed = 0;  // loaders: tiles armed, for the exit path
-  // Registers: 512 threads launch with 128 each, 65,536 together; a softmax
-  // thread holds a step's row of scores (128 at head_dim 64) and takes 200, the
-  // others keep 56 (56 * 256 + 200 * 256 = 65,536).
+  // Registers: 512 threads launch with 128 each, 65,536 together.  A softmax
+  // thread holds a step's row of scores: 64 (head_dim 128: 200 registers, the
+  // others keep 56) or 128 (head_dim 64: 216 and 40); (56 + 200) * 256 and
+  // (40 + 216) * 256 are 65,536.
   if (warp < 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if constexpr (D == 128)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0 || warp == 5) {
     // ------------------------------------------- loaders of keys and values
     // The warp's t-th tile lies in place 2 t (keys) or 2 t + 1 (values) of the ring.
@@ -755,6 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             release(at, g.two);
           }
+          if (!ok) break;
+          mma_commit(smem_u32(&hdr->q_empty[q & 1]));
+          if (g.two) mma_commit(smem_u32(&hdr->q_empty[q & 1]));
         } else {
           // (the accumulators of the segment before have been read)
           if (k > 0 && !wait(&hdr->o_free, k - 1)) break;
@@ -869,13 +866,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     // ----------------------------------------------------- softmax groups
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if constexpr (D == 128)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int grp = (warp - 8) >> 2;               // which slot
     const int r = tid - 256 - grp * kTile;         // row of the M tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_base + grp * C::kCols;
     const uint32_t t_p = t_s + C::kP, t_o = t_s + C::kO, t_o0 = tmem + lane_base + C::kO;
-    uint32_t n_s = 0, n_meet = 0, it = 0, qi = 0;
+    uint32_t n_s = 0, n_meet = 0, it = 0;
     auto meet = [&]() {
       mbar_arrive(smem_u32(&hdr->meet));
       const bool ok = warp_wait(smem_u32(&hdr->meet), n_meet & 1, wl, abort);
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < p.tile_tokens * p.group && tok < g.n;
       const bool any = __any_sync(0xffffffffu, live);
       const int hidden = first_hidden(p, g);
-      uint32_t* bad = hdr->bad[k & 1];
+      uint32_t* bad = hdr->bad[k % 3];
       float m = -INFINITY, l = 0.f;
       bool stop = false;
       constexpr int W = C::kStep;
@@ -1096,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ end of the segment
       if (!g.two) hdr->ml[grp][r] = make_float2(m, l);
       if (tid == 256)
-        for (int i = 0; i < 8; ++i) hdr->bad[(k & 1) ^ 1][i] = 0u;  // (last read before the groups' last meeting)
+        for (int i = 0; i < 8; ++i) hdr->bad[(k + 1) % 3][i] = 0u;  // (last read before the groups met a segment ago)
       if (!meet()) break;
       const bool used1 = g.two || n > 1;
       if (!warp_wait(smem_u32(&hdr->o_full[0]), k & 1, wl, abort) ||
@@ -1115,15 +1115,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t any_bad = 0;
       for (int i = 0; i < 8; ++i) any_bad |= bad[i];
       const int head = g.head * p.group + r % p.group;
-      const int64_t out_at = ((int64_t)(g.row0 + tok) * p.out_stride + (int64_t)head * D) * 2;  // bytes
+      uint8_t* out = p.out + ((int64_t)(g.row0 + tok) * p.out_stride + (int64_t)head * D) * 2;
       const float norm = g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
       const int rr = (g.two ? grp * kTile : 0) + r;
       const size_t part = ((size_t)worker * 2 + (g.part > 0)) * 2 * kTile;
       // Columns: all of the group's own accumulator, or half of both.
       const int c_lo = g.two ? 0 : grp * (D / 2), c_hi = g.two ? D : c_lo + D / 2;
-      // The item's query tile is done with: finished rows pass through its
-      // place, 16-byte words exclusive-ored with the row as in the swizzle.
-      const uint32_t q_buf = (qi + (g.two ? grp : 0)) & 1, stage = q_s + q_buf * C::kTileBytes;
       if (any) {
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
@@ -1146,14 +1143,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
-          if (g.part < 0) {
+          if (live && g.part < 0) {
+            // (64 bytes of a row: whole sectors, and the row's place in shared
+            // memory is not held up for the next item)
+            uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              sts128(stage + r * 128 + (c >> 6) * kHalfBytes + ((((c >> 3) + j) ^ r) & 7) * 16,
-                     make_uint4(T::pack(v[8 * j] * norm, v[8 * j + 1] * norm),
-                                T::pack(v[8 * j + 2] * norm, v[8 * j + 3] * norm),
-                                T::pack(v[8 * j + 4] * norm, v[8 * j + 5] * norm),
-                                T::pack(v[8 * j + 6] * norm, v[8 * j + 7] * norm)));
+            for (int j = 0; j < 16; ++j) w[j] = T::pack(v[2 * j] * norm, v[2 * j + 1] * norm);
+            if (p.wide_out) {
+              stg256(out + c * 2, w);
+              stg256(out + c * 2 + 32, w + 8);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                reinterpret_cast<uint4*>(out + c * 2)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            }
           } else if (live) {
             // (a warp's rows are neighbours: 512 bytes at a time)
             float4* dst = reinterpret_cast<float4*>(p.part_o + part * D) + (size_t)(c / 4) * (2 * kTile) + rr;
@@ -1166,28 +1169,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The accumulators have been read.
       tc_fence_before();
       mbar_arrive(smem_u32(&hdr->o_free));
-      if (any) {
-        if (live && (g.two || grp == 0)) {
-          if (g.part >= 0)
-            p.part_ml[part + rr] = make_float2(m, l);
-          else if (p.lse)
-            p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
-        }
-        if (g.part < 0) {
-          // The warp's 32 rows, 16 bytes a lane: neighbouring lanes write neighbouring words of a row.
-          __syncwarp();
-          const int64_t mine = live ? out_at : -1;
-          if (g.two)
-            flush_rows<D / 8>(p.out, stage, (warp & 3) * 32, 0, mine, lane);
-          else
-            flush_rows<D / 16>(p.out, stage, (warp & 3) * 32, grp * (D / 16), mine, lane);
-        }
+      if (live && (g.two || grp == 0)) {
+        if (g.part >= 0)
+          p.part_ml[part + rr] = make_float2(m, l);
+        else if (p.lse)
+          p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
       }
-      qi += 1 + g.two;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the loader writes the place next)
-      __syncwarp();
-      if (lane == 0) mbar_arrive_n(smem_u32(&hdr->q_empty[q_buf]), g.two ? 2 : 1);
-      if (!meet()) break;
+      if (!g.two && !meet()) break;  // (ml has been read)
     }
   }
 
@@ -1446,6 +1434,7 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   p.words = a->tree ? a->tree_words : 0;
   p.out = static_cast<uint8_t*>(a->out);
   p.out_stride = a->out_stride;
+  p.wide_out = !kv_misaligned(a->out, 32) && a->out_stride % 16 == 0;
   p.lse = a->lse;
   p.status = status;
   p.workers = sm_count(kv->device);
