@@ -556,7 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The setup above touches only this CTA; everything read or written from
   // here on may belong to the kernel before.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Tiles and items of every sequence: thread i counts a run of them, then a
   // scan over the CTA gives the totals and who holds this worker's first unit.

@@ -90,12 +90,14 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int i, int
 // that both members of every rotated pair, (i, i + D / 2) or (2 i, 2 i + 1), lie
 // in one thread and the only exchange between lanes is the norm's sum.  A warp
 // keeps its token's angles and the weights in registers across the heads and
-// has U heads' loads in flight.  Bound: bytes (each row once in, once out).
-// Four warps more than a plain copy would need per token do not pay, except
-// where there are few tokens: then the split spreads a token's heads over the
-// machine.
+// has U heads' loads in flight.  Bound: bytes (each row once in, once out), and
+// at few tokens the chain of dependent reads that finds a token's place; so a
+// token's heads are spread over more warps only where there are few tokens.
+// Four blocks an SM (64 registers) against three: 74 against 80 us for 15,925
+// tokens of 32 + 2 x 8 heads of 128 (5.3 TB/s); several tokens a warp with the
+// next one's place looked up ahead: 81 us; twice the warps per token: 112 us.
 template <typename T, int D, int U>
-__global__ void __launch_bounds__(kBlock) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kBlock, 4) append_kernel(const AppendParams p) {
   constexpr int L = D / 8;    // lanes per head
   constexpr int HPW = 32 / L; // heads per warp and round
   const int lane = threadIdx.x & 31;
