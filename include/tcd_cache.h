@@ -68,7 +68,8 @@ typedef struct tc_kv_t {
  *  ctx_lens     (device) int32[batch]: tokens of sequence b already cached.
  *               Its new token t lies in slot ctx_lens[b] + t.
  *  page_table   (device) int32[batch][table_width] page ids; entries past a
- *               sequence's last page are not read.
+ *               sequence's last page are not read.  A sequence has at most
+ *               table_width * page_size slots, and fewer than 2^31 - 2^16.
  *
  * A sequence whose rows, lengths, slots or page ids are out of range gets
  * TC_ERR_BOUNDS in the call's status.  Nothing outside the given buffers and

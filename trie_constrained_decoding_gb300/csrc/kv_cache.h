@@ -67,6 +67,9 @@ struct F16 {
   }
 };
 
+// Slots of a sequence (their numbers, rounded up to tiles, fit 31 bits).
+constexpr int64_t kMaxSlots = 0x7fff0000;
+
 // Rows, context and slots of sequence b.  False where they are out of range:
 // rows outside the packed arrays, or more slots than the page table has.
 struct SeqSpan {
@@ -77,8 +80,9 @@ __device__ __forceinline__ bool seq_span(const TokensView& t, int page_size, int
   s->row0 = lo;
   s->n = hi - lo;
   s->ctx = c;
+  const int64_t room = (int64_t)t.width * page_size;
   return lo >= 0 && hi >= lo && hi <= t.n_tokens && c >= 0 &&
-         (int64_t)c + (hi - lo) <= (int64_t)t.width * page_size;
+         (int64_t)c + (hi - lo) <= (room < kMaxSlots ? room : kMaxSlots);
 }
 
 // ------------------------------------------------------------ host helpers
