@@ -566,8 +566,8 @@ def tree_masks(parents, cu_tokens, ctx_lens, masks, positions=None, status=None,
         raise ValueError("masks must be a contiguous int64 tensor [tokens, words]")
     if status is None:
         status = torch.empty(batch, dtype=torch.int32, device=dev)
-    t = _Tokens(batch, n, _int_tensor(cu_tokens, (batch + 1,), dev, "cu_tokens"), _int_tensor(ctx_lens, (batch,), dev, "ctx_lens"),
-                None, 0)
+    t = _Tokens(batch, n, _int_tensor(cu_tokens, (batch + 1,), dev, "cu_tokens"),
+                _int_tensor(ctx_lens, (batch,), dev, "ctx_lens"), None, 0)
     with torch.cuda.device(dev):
         _check(_tree_masks(ctypes.byref(t), _int_tensor(parents, (n,), dev, "parents"), masks.shape[1], masks.data_ptr(),
                            None if positions is None else _int_tensor(positions, (n,), dev, "positions"),

@@ -8,52 +8,75 @@
 // or a prompt fills tiles of 128.
 //
 // Work.  An item is one sequence, one key-value head and up to two M tiles;
-// its units are 128-slot tiles of the cache, and a few more for its beginning
-// and end.  The units of all items form one line that is cut into equal parts,
-// one per CTA (one CTA per SM), whatever the mixture of lengths: a long context
-// is split over many CTAs, many short ones share one.  Every CTA works its part out from the lengths on the
-// device, so the launch depends on none of them and can be captured.  An item
-// that a cut falls into leaves unnormalised partial results, at most two per
-// CTA, which a second kernel joins.
+// its units are 128-slot tiles of the cache, one or two more before them and
+// two after them for what its beginning (first loads, first product) and its
+// end (last product, output) take.  The units of all items form one line that is
+// cut into equal parts, one per CTA (one CTA per SM), whatever the mixture of
+// lengths: a long context is split over many CTAs, many short ones share one, and
+// a cut that falls into an item's beginning or end splits nothing.  (Tiles alone:
+// a prompt of 8192 558 us against 483, 16 short prompts 63 against 53, a decode
+// step of 64 sequences 205 against 185.  All of the cost before the tiles: 486,
+// 55, 184; two before and two after at head_dim 128: 490, 55, 185.)  Every CTA
+// works its part out from the lengths on the device, so the launch depends on
+// none of them and can be captured.  An item that a cut falls into leaves
+// unnormalised partial results in 32 bits, at most two per CTA, which a second
+// kernel joins.
 //
 // One CTA, 16 warps:
 //  - warps 0, 5 and 7 load keys, values and queries by TMA (128-byte swizzle),
 //    keys and values in turn into one ring of 128 x head_dim tiles, a copy per
-//    page (per page and 64 columns where the pages are smaller than a step);
-//    pages past the sequence's end are not loaded.  A copy takes a warp long
-//    enough to issue that one warp for all three would set the pace;
+//    page and 64 columns; pages past the sequence's end are not loaded.  One
+//    warp for all three sets the pace where pages have 16 slots (drafts of 16
+//    sequences: 85 us against 80), and makes no difference for larger ones;
 //  - warps 1 and 3 issue the score products S = Q K^T of one softmax group each
 //    (both operands in shared memory), warps 4 and 6 the output products
 //    O += P V (P in tensor memory), in steps of 64 slots (head_dim 128) or 128
 //    (64).  One thread each, which does nothing but wait for its operands and
-//    issue: an issuer with several things to look at reacts too late;
+//    issue: one that has both products of a group to look at reacts too late
+//    (a prompt of 8192: 696 us against 512 at that time);
 //  - warp 2 hands out the CTA's segments (an item's part) through a small ring;
 //  - warps 8-11 and 12-15 are two softmax groups, one row per thread: a thread
 //    reads its row of S from tensor memory, keeps the row's maximum and sum in
-//    32 bits, and writes the weights P beside it in the cache's type.
+//    32 bits, and writes the weights P beside it in the cache's type, which is
+//    what the tensor cores multiply (the sum is of the weights before that
+//    rounding, whose errors have no common sign).
 // The two groups always alternate with the tensor cores: with two M tiles each
 // takes one and both use every key-value tile; with one M tile they take the
 // even and the odd tiles of the cache and are joined at the end.
 //
 // Tensor memory, 512 columns of 32 bits: each group has its scores S, its
-// weights P and its accumulator O, 64 + 32 + 128 columns (head_dim 128) or
+// weights P and its accumulator O, 64 + 2 x 32 + 128 columns (head_dim 128) or
 // 128 + 64 + 64 (64).  S and P are apart, so that the next step's scores are
-// computed while the group works on this one's weights; with both in one place
-// (steps of 128 slots) a step is one chain of products and softmax.  At
-// head_dim 128 that leaves steps of 64 slots, whose scores read 6 KB of shared
-// memory for 32 cycles of products and take 50; beside the other product,
-// which reads less, a step takes 576 cycles instead of 512 (measured).
+// computed while the group works on this one's weights, and at head_dim 128 P
+// has two places, so that the next weights need not wait for the product of
+// the last.  Steps of 128 slots there would leave room for S and P in one place
+// only, and a step would be one chain of products and softmax.  The scores of a
+// step of 64 read 6 KB of shared memory for 32 cycles of products and take 50;
+// beside the other product, which reads less, a step of 128 slots takes 576
+// cycles instead of 512 (measured).
 //
 // The maximum that the weights refer to is only moved when a row's maximum
 // has grown by more than 2^8 (the sums hold weights up to 2^8 in 32 bits, and
 // the types' relative precision does not depend on the scale): the
 // accumulator in tensor memory is rescaled then and rarely otherwise.
 //
-// A tile that some row does not see entirely (the end of the sequence, the
-// drafted tokens, the diagonal of a prompt) takes the masked path: a 128-bit
-// mask per row; and, as a weight of zero times an infinity would be NaN,
-// infinities and NaN among the values of slots that only some rows see are
-// taken out of the tile and added at the end to the rows that see them.
+// Steps that every row sees entirely run in a loop without masks.  The others
+// (the end of the sequence, the drafted tokens, the diagonal of a prompt) take
+// the masked path: a mask of the step's slots per row; and, as a weight of zero
+// times an infinity would be NaN, infinities and NaN among the values of slots
+// that only some rows see are taken out of the tile and added at the end to the
+// rows that see them.
+//
+// What it measured (bf16, 32 query and 8 key-value heads of 128, pages of 64):
+// a prompt of 8192 tokens in 483 us, 1.14 PFLOP/s, 59 % of what the library's
+// matrix product reaches; 16 prompts of 5 to 261 tokens in 53 us; a decode step of
+// 64 sequences with 97 to 8011 slots in 185 us, 5.9 TB/s, 87 % of a copy's rate;
+// one token over 1500 slots in 17 us.  Bound: long prompts by the chain of waits
+// and exponentials that a softmax group goes through in a step (1900 cycles for
+// two groups' 64 slots, 1024 of them products; without any products it would
+// still take 482 us, without the softmax' arithmetic 453); decode by bytes;
+// small calls by the fetch of instructions that no cache holds yet, about 5000
+// cycles before the first load's barrier and 4000 in the first segment.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -80,7 +103,8 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kStep = D == 128 ? 64 : 128;  // slots of a step
   static constexpr int kSteps = kTile / kStep;       // steps of a tile
-  static constexpr int kItemCost = D == 128 ? 3 : 4; // an item's beginning and end, in tiles (measured)
+    // What an item's beginning and its end take, in tiles.
+  static constexpr int kBegin = D == 128 ? 1 : 2, kEnd = 2;
   // Tensor memory of a group: scores, weights, accumulator.
   static constexpr int kPs = D == 128 ? 2 : 1;  // places of the weights
   static constexpr uint32_t kP = kStep, kO = kP + kPs * (kStep / 2), kCols = 256;
@@ -105,10 +129,6 @@ struct AttendParams {
   int32_t q_heads, group, tile_tokens;  // tile_tokens = 128 / group
   int32_t max_tokens;
   int32_t q_rows;                       // rows of one query load
-  // Places in a key-value tile of a step and of 64 columns: a copy brings all
-  // columns of a page (merged) or 64 of them.
-  int32_t merged;
-  uint32_t step_stride, half_stride;
   float c;                              // |scale| log2(e), the factor of the exponents
   int32_t negate;                       // the scale is negative
   const int64_t* tree;
@@ -124,7 +144,7 @@ struct AttendParams {
   float2* part_ml;   // [workers][2][256] maximum and sum of each row
   float* part_o;     // [workers][2][D / 4][256][4]
   long long wait_limit;
-  int32_t withhold;  // test switch: the first worker's first load is not issued
+  int32_t withhold;  // test switch: the first workers' first loads are not issued
 };
 
 constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile; }
@@ -227,16 +247,16 @@ __device__ __forceinline__ uint64_t desc_k_major(uint32_t a) {
   return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t a, uint32_t half_stride) {
-  return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(half_stride >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t a) {
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | (uint64_t)(kHalfBytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // Instruction descriptor of kind::f16: 32-bit accumulator, M = 128.
 template <typename T>
 __device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major, bool negate_a = false) {
   const uint32_t ty = T::kMma;
-  return (1u << 4) | (ty << 7) | (ty << 10) | (negate_a ? 1u << 13 : 0u) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
-         ((uint32_t)(kTile >> 4) << 24);
+  return (1u << 4) | (ty << 7) | (ty << 10) | (negate_a ? 1u << 13 : 0u) | (b_n_major ? 1u << 16 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
@@ -318,7 +338,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void stg256(void* a, const uint32_t* v) {
@@ -366,7 +389,7 @@ __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
 struct Line {
   int n, ctx, step;  // tokens, cached tokens, tokens of an item
   bool causal;
-  int extra;         // units of an item beside its tiles, counted before them
+  int extra;         // units of an item beside its tiles
   __device__ int items() const { return (n + step - 1) / step; }
   // tiles of item i
   __device__ int tiles(int i) const {
@@ -596,8 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     all_tiles += sums[i];
     all_items += sums[kThreads / 32 + i];
   }
-  // With little to do every worker gets tiles first of all.
-  const int extra = all_tiles >= 8 * (int64_t)p.workers ? C::kItemCost : 0;
+  constexpr int extra = C::kBegin + C::kEnd;
   const int64_t total = all_tiles + extra * all_items;
   const int active = (int)min((int64_t)p.workers, total);
   const Cut cut(total, active);
@@ -625,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const uint32_t tmem = hdr->tmem_base;
-  const bool held = p.withhold != 0 && worker == 0;
+  // (a worker has one unit or more: one of these has the first item's first tile)
+  const bool held = p.withhold != 0 && worker <= C::kBegin;
   uint32_t armed = 0;  // loaders: tiles armed, for the exit path
   // Registers: 512 threads launch with 128 each, 65,536 together.  A softmax
   // thread holds a step's row of scores: 64 (head_dim 128: 200 registers, the
@@ -640,10 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------- loaders of keys and values
     // The warp's t-th tile lies in place 2 t (keys) or 2 t + 1 (values) of the ring.
     const uint32_t is_v = warp == 5;
-    const int box = p.kv.page_size, pieces = kTile / box, copies = p.merged ? 1 : C::kHalves;
-    const int piece = lane / copies, half = lane % copies;
-    const uint32_t dst = kv_s + (p.merged ? piece * box * 128 * C::kHalves : half * kHalfBytes + piece * box * 128);
-    const uint32_t bytes = (uint32_t)(box * 128 * C::kHalves / copies);  // of one copy
+    const int box = p.kv.page_size, pieces = kTile / box;
+    const int piece = lane / C::kHalves, half = lane % C::kHalves;
+    const uint32_t dst = kv_s + half * kHalfBytes + piece * box * 128;
+    const uint32_t bytes = (uint32_t)box * 128;  // of one copy
     bool stop = false;
     for (int k = 0; !stop; ++k) {
       if (!warp_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
@@ -737,12 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < steps; ++u, ++done) {
               // (the scores before have been read)
               if (done > 0 && !wait(&hdr->s_read[slot], done - 1)) break;
-              const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + u * p.step_stride);
+              const uint64_t b = desc_k_major(kv_s + stage * C::kTileBytes + u * C::kStep * 128);
               tc_fence_after();
 #pragma unroll
               for (int e = 0; e < D / 16; ++e) {
                 const uint32_t o = (uint32_t)(e & 3) * 2, h = e >> 2;
-                mma_ss(t_s, q_desc + h * (kHalfBytes >> 4) + o, b + h * (p.half_stride >> 4) + o, id_s, e > 0);
+                mma_ss(t_s, q_desc + h * (kHalfBytes >> 4) + o, b + h * (kHalfBytes >> 4) + o, id_s, e > 0);
               }
               mma_commit(smem_u32(&hdr->s_full[slot]));
             }
@@ -759,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int steps = steps_of<D>(g, g.t0 + i);
             if (!wait(&hdr->full[at % (2 * NS)], at / (2 * NS))) break;
             for (int u = 0; u < steps; ++u, ++done) {
-              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + u * p.step_stride, p.half_stride);
+              const uint64_t b = desc_n_major(kv_s + stage * C::kTileBytes + u * C::kStep * 128);
               // over the 16-slot groups that the step has
               const int groups = (step_slots<D>(g, (g.t0 + i) * kTile + u * C::kStep) + 15) / 16;
               const bool more = i > i0 || u > 0;
@@ -810,8 +833,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (left > 0 && h < p.kv.kv_heads) {
             const int tiles = l.tiles(item);
             const int64_t take = min((int64_t)extra + tiles - r, left);
-            g.t0 = (int)max(r - extra, (int64_t)0);
-            g.t1 = (int)max(r + take - extra, (int64_t)0);
+            g.t0 = (int)min(max(r - C::kBegin, (int64_t)0), (int64_t)tiles);
+            g.t1 = (int)min(max(r + take - C::kBegin, (int64_t)0), (int64_t)tiles);
             if (g.t1 > g.t0) {
               g.valid = 1;
               g.seq = b;
@@ -826,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               g.last = worker;
               if (g.part == 1) {
                 // the item's last unit lies with the worker that this finds
-                const int64_t last_unit = end - left - r + extra + tiles - 1;
+                const int64_t last_unit = end - left - r + C::kBegin + tiles - 1;
                 int w = worker + 1;
                 while (cut.start(w + 1) <= last_unit) ++w;
                 g.last = w;
@@ -1048,17 +1071,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the rest of its group of 16 slots is read.
             const int j = r % W, slot = start + j;
             const int c0 = r / W * 8 + (g.two ? grp * 4 : 0), c1 = c0 + (g.two ? 4 : 8);
-            const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + u * p.step_stride + j * 128;
+            const uint32_t row = kv_s + (vi % NS) * C::kTileBytes + u * C::kStep * 128 + j * 128;
             if (slot >= g.end) {
               if (j < ((slots + 15) & ~15))
 #pragma unroll 4
                 for (int c = c0; c < c1; ++c)
-                  sts128(row + (c >> 3) * p.half_stride + (((c ^ j) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+                  sts128(row + (c >> 3) * kHalfBytes + (((c ^ j) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
             } else if (slot >= hidden) {
               bool found = false;
 #pragma unroll 1
               for (int c = c0; c < c1; c += 4) {
-                const uint32_t at = row + (c >> 3) * p.half_stride;
+                const uint32_t at = row + (c >> 3) * kHalfBytes;
                 uint4 v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = lds128(at + ((((c + e) ^ j) & 7) << 4));
@@ -1143,8 +1166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
           if (live && g.part < 0) {
-            // (64 bytes of a row: whole sectors, and the row's place in shared
-            // memory is not held up for the next item)
+            // (64 bytes of a row: whole sectors, and no shared memory is held up
+            // for the next item.  16 bytes a store: a prompt of 2048 188.6 us
+            // against 186, four of 512 53 against 51.5)
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = T::pack(v[2 * j] * norm, v[2 * j + 1] * norm);
@@ -1154,7 +1178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                reinterpret_cast<uint4*>(out + c * 2)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                reinterpret_cast<uint4*>(out + c * 2)[j] =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
             }
           } else if (live) {
             // (a warp's rows are neighbours: 512 bytes at a time)
@@ -1219,8 +1244,13 @@ constexpr int kJoinThreads = 256, kJoinBlocks = 8;
 // kJoinBlocks blocks for each worker: the item that starts in it and goes on in
 // the next.  A thread joins four columns of a row (the parts are laid out by
 // columns, so neighbouring rows are neighbours); the parts are added in the
-// order of the workers: the result does not depend on timing.  The blocks
-// after these write the status of a sequence each.
+// order of the workers: the result does not depend on timing.  Bound: latency (a
+// few parts of a few rows; up to 20 MB of partial results when every worker has
+// two, 4 us at a copy's rate).  Blocks a worker, 16 short prompts: 4 72 us, 8 64,
+// 16 64.4, 32 65.5.  Letting the blocks start while the first kernel still runs is
+// slower (one token 18.1 us against 17.4).  The blocks after these write the
+// status of a sequence each (one block, as a warp takes 10 us for the pages of
+// 131,000 slots).
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1395,13 +1425,11 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   // Keys and values of the layer: [page][keys or values, head][slot][element],
   const KvView v = kv_view(kv, layer);
   const cuuint64_t d = (cuuint64_t)kv->head_dim, sz = (cuuint64_t)kv->page_size;
-  // in pieces of 64 columns.  A copy brings a page's slots; where a page holds
-  // whole steps (64 slots at head_dim 128), all its columns at once.
+  // in pieces of 64 columns.  A copy brings a page's slots of one piece.
   const int halves = kv->head_dim / 64;
-  const bool merged = halves == 2 && kv->page_size >= 64;
   const cuuint64_t kv_dims[5] = {64, sz, (cuuint64_t)halves, (cuuint64_t)2 * kv->kv_heads, (cuuint64_t)kv->pages};
   const cuuint64_t kv_strides[4] = {d * 2, 128, sz * d * 2, (cuuint64_t)2 * kv->kv_heads * sz * d * 2};
-  const cuuint32_t kv_box[5] = {64, (cuuint32_t)kv->page_size, merged ? 2u : 1u, 1, 1};
+  const cuuint32_t kv_box[5] = {64, (cuuint32_t)kv->page_size, 1, 1, 1};
   const int group = a->q_heads / kv->kv_heads, tile_tokens = kTile / group;
   // Queries: rows (token, head of the group) of one M tile, at most max_tokens of them.
   const int q_tokens = a->max_tokens < 1 ? 1 : a->max_tokens < tile_tokens ? a->max_tokens : tile_tokens;
@@ -1421,10 +1449,6 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   p.tile_tokens = tile_tokens;
   p.max_tokens = a->max_tokens;
   p.q_rows = group * q_tokens;
-  p.merged = merged;
-  const bool page_is_step = merged && kv->page_size == 64;  // then a step's columns lie together
-  p.half_stride = page_is_step ? kHalfBytes / 2 : kHalfBytes;
-  p.step_stride = page_is_step ? kHalfBytes : kHalfBytes / 2;
   // A scale of zero weighs all slots alike; as a factor so small that every
   // product with a score is nothing, it keeps -inf times the factor -inf.
   p.c = fmaxf(fabsf(a->scale) * 1.4426950408889634f, 1e-30f);

@@ -90,7 +90,8 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int i, int
 // that both members of every rotated pair, (i, i + D / 2) or (2 i, 2 i + 1), lie
 // in one thread and the only exchange between lanes is the norm's sum.  A warp
 // keeps its token's angles and the weights in registers across the heads and
-// has U heads' loads in flight.  Bound: bytes (each row once in, once out), and
+// has U heads' loads in flight.  Norm and rotation are in 32 bits, rounded once
+// when they are written; values are copied.  Bound: bytes (each row once in, once out), and
 // at few tokens the chain of dependent reads that finds a token's place; so a
 // token's heads are spread over more warps only where there are few tokens.
 // Four blocks an SM (64 registers) against three: 74 against 80 us for 15,925
@@ -240,8 +241,9 @@ __global__ void __launch_bounds__(kBlock, 4) append_kernel(const AppendParams p)
 // -------------------------------------------------------------- tree masks
 
 // One warp per sequence, one lane per drafted token: a token walks up its
-// ancestors (parents precede their children, so the walk ends).  Small: 2 to
-// 256 tokens a sequence, read and written once.
+// ancestors (parents precede their children, so the walk ends).  Up to 256
+// tokens a sequence, read and written once: bound by the launch and the walk's
+// dependent reads.
 template <int W>
 __global__ void __launch_bounds__(kBlock) tree_mask_kernel(const TokensView t, const int32_t* parents, int64_t* masks,
                                                           int32_t* positions, int32_t* status) {
@@ -283,7 +285,9 @@ __global__ void __launch_bounds__(kBlock) tree_mask_kernel(const TokensView t, c
 constexpr int kCopyUnroll = 8;
 
 // A page of one layer is one run of bytes; a block copies kBlock * kCopyUnroll
-// 16-byte words of it, every load before the first store.  Bound: bytes.
+// 16-byte words of it, every load before the first store.  Bound: bytes: 61
+// pages of 64 slots, 8 heads of 128, in 16 layers take 77 us (6.6 TB/s, 98 % of
+// a plain copy); 4 or 16 words a thread make no difference.
 __global__ void __launch_bounds__(kBlock) copy_pages_kernel(uint8_t* pool, int32_t pages, int64_t page_bytes,
                                                            const int32_t* src, const int32_t* dst, int32_t* status) {
   const int pair = blockIdx.y, layer = blockIdx.z;
@@ -308,7 +312,8 @@ __global__ void __launch_bounds__(kBlock) copy_pages_kernel(uint8_t* pool, int32
 struct CompactParams {
   uint8_t* pool;
   TokensView tok;
-  int32_t layers, pages, kv_heads, page_size, page_shift, row_words;  // row_words: 16-byte words of one slot of one head
+  int32_t layers, pages, kv_heads, page_size, page_shift;
+  int32_t row_words;  // 16-byte words of one slot of one head
   const int32_t* path;
   int32_t path_width;
   const int32_t* n_path;
@@ -316,15 +321,17 @@ struct CompactParams {
   int32_t* status;
 };
 
-constexpr int kMoveUnroll = 8;
+constexpr int kMoveUnroll = 4;
 
 // Grid (columns / kBlock, sequence).  A column is one 16-byte word of one head
 // of one layer's keys or values; its thread moves that word of every slot of
 // the branch, in ascending order.  Indices ascend strictly, so path[i] >= i:
 // the slot that move i writes is the source of no later move, and an earlier
 // move has read it before (same thread, program order).  Reading kMoveUnroll
-// moves before writing them keeps that order.  Bound: latency of two
-// dependent reads (path, then slots) at small sizes, bytes at large ones.
+// moves before writing them keeps that order.  Bound: the chain of path, page
+// table, load and store: 64 branches of up to 12 tokens in 16 layers of 8 heads
+// of 128 take 8.5 us (3.6 TB/s); two moves at a time 10.5, eight 9.4 (more
+// registers, fewer blocks).
 __global__ void __launch_bounds__(kBlock) compact_kernel(const CompactParams p) {
   __shared__ int64_t s_src[TC_PATH_MAX], s_dst[TC_PATH_MAX];  // slot offsets in rows of one head
   const int b = blockIdx.y, tid = threadIdx.x;
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(const CompactParams p) 
     const int32_t* path = p.path + (int64_t)b * p.path_width;
     const int x = __ldg(path + tid), before = tid > 0 ? __ldg(path + tid - 1) : -1;
     const int64_t frm = (int64_t)ctx + x, to = (int64_t)ctx + tid;
-    ok = x > before && frm < (int64_t)p.tok.width * p.page_size;
+    ok = x > before && frm < (int64_t)p.tok.width * p.page_size && frm < kMaxSlots;
     if (ok && x >= tid) {
       const int32_t* row = p.tok.table + (int64_t)b * p.tok.width;
       const int pa = __ldg(row + (frm >> p.page_shift)), pb = __ldg(row + (to >> p.page_shift));
@@ -417,8 +424,10 @@ extern "C" tc_status tc_kv_append(const tc_kv_t* kv, int32_t layer, const tc_tok
   p.q_out_stride = a->q_out_stride;
   p.status = status;
   // Few tokens: their heads are spread over more warps, down to one round of
-  // one load per lane (a whole token in one warp would take its rounds one
-  // after another).
+  // one load per lane (a whole token in one warp takes its rounds one after
+  // another); more than 4096 warps of them cost more than they hide.  1, 512,
+  // 2048 and 4096 tokens: 4.3, 6.5, 14.6 and 24.8 us; always a warp per token
+  // 7.4, 14.6, 18.7, 24.8; always a round per warp 4.3, 10.5, 28.9, 56.7.
   const int hpw = 256 / kv->head_dim;
   const int64_t rounds = (heads + hpw - 1) / hpw;
   int64_t split = 1;
