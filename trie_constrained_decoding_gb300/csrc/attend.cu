@@ -49,7 +49,9 @@
 // 128 + 64 + 64 (64).  S and P are apart, so that the next step's scores are
 // computed while the group works on this one's weights, and at head_dim 128 P
 // has two places, so that the next weights need not wait for the product of
-// the last.  Steps of 128 slots there would leave room for S and P in one place
+// the last (the issuer of the scores waits for the one before that, while its own
+// product runs, and announces both: the group waits once a step, 418 us against
+// 436 for a prompt of 8192).  Steps of 128 slots there would leave room for S and P in one place
 // only, and a step would be one chain of products and softmax.  The scores of a
 // step of 64 read 6 KB of shared memory for 32 cycles of products and take 50;
 // beside the other product, which reads less, a step of 128 slots takes 576
@@ -93,7 +95,7 @@ constexpr int kThreads = 512;
 constexpr uint32_t kHalfBytes = kTile * 128; // 128 rows of 64 elements
 constexpr float kRescale = 8.f;             // log2 of the growth that moves the reference maximum
 constexpr int kSegs = 4;                    // segments ahead of the softmax groups
-constexpr long long kWaitLimit = 1ll << 22; // default polls of one wait before giving up
+constexpr int kWaitLimit = 1 << 22; // default polls of one wait before giving up
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -109,6 +111,7 @@ struct Cfg {
   static constexpr int kPs = D == 128 ? 2 : 1;  // places of the weights
   static constexpr uint32_t kP = kStep, kO = kP + kPs * (kStep / 2), kCols = 256;
   static_assert(kO + D <= kCols, "tensor memory of a group");
+  static_assert(kSteps == kHalves, "the clearing of values shares out a step's rows in these parts");
 };
 
 // A CTA's part of an item.
@@ -143,7 +146,7 @@ struct AttendParams {
   int32_t* errs;     // [workers] a wait ran out
   float2* part_ml;   // [workers][2][256] maximum and sum of each row
   float* part_o;     // [workers][2][D / 4][256][4]
-  long long wait_limit;
+  int32_t wait_limit;
   int32_t withhold;  // test switch: the first workers' first loads are not issued
 };
 
@@ -193,32 +196,33 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Up to 64 polls of a phase (each waits a while in hardware).
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+// One poll of a phase (it waits a while in hardware).
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 64;\n"
-      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
-      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
-      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
   return ok;
 }
-// Waits for a phase, at most `limit` polls; false if it gave up or another
-// wait of the CTA has.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long long limit, volatile int32_t* abort) {
-  if (mbar_poll(bar, parity)) return true;
-  for (long long i = 64; i < limit; i += 64) {
-    if (mbar_poll(bar, parity)) return true;
-    if (*abort) return false;
-  }
+// Waits for a phase, at most `limit` polls; false if it gave up or another wait
+// of the CTA has.  (One poll by itself in front, as most waits of the softmax groups
+// are over when they begin: with a counted loop in front a prompt of 8192 took
+// 475 us where this took 436.)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int limit, volatile int32_t* abort) {
+  if (mbar_try(bar, parity)) return true;
+  int i = 1;
+#pragma unroll 1
+  do {
+    if (mbar_try(bar, parity)) return true;
+    ++i;
+  } while (i < limit && !*abort);
   *abort = 1;
   return false;
 }
 // The same for a whole warp, with one answer for all of it.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit, volatile int32_t* abort) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int limit, volatile int32_t* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
 __device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap* map, int slot, int half, int head, int page,
@@ -355,34 +359,40 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 
 // ------------------------------------------------------------ the work's line
 
-// Division of non-negative 64-bit numbers that mostly fit 32 bits.
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
+// (Divisions here are of 32 bits: the code of a 64-bit one is long, and a small
+// call is bound by the fetch of its instructions.)
 
-// sum over i < n of floor((a i + b) / m), in O(log m) steps (Euclid's scheme).
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum over i < n of floor((a i + b) / m), in O(log m) steps (Euclid's scheme);
+// a n + b fits 32 bits.
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t ans = 0;
   while (n > 0) {
-    if (a >= m) {
-      const int64_t q = div64(a, m);
-      ans += n * (n - 1) / 2 * q;
-      a -= q * m;
-    }
-    if (b >= m) {
-      const int64_t q = div64(b, m);
-      ans += n * q;
-      b -= q * m;
-    }
-    const int64_t y = a * n + b;
-    if (y < m) break;
-    n = div64(y, m);
+    const uint32_t qa = a / m, qb = b / m;
+    ans += (int64_t)n * (n - 1) / 2 * qa + (int64_t)n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const uint32_t y = a * n + b;
+    n = y / m;
     b = y - n * m;
-    const int64_t t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
+    if (n == 0) break;  // (m may be 0 now)
   }
   return ans;
+}
+
+// a / n for n < 2^16, in pieces of 16 bits.
+__device__ __forceinline__ int64_t div_small(int64_t a, uint32_t n) {
+  uint32_t rest = 0;
+  int64_t q = 0;
+#pragma unroll 1
+  for (int i = (uint64_t)a >> 32 ? 48 : 16; i >= 0; i -= 16) {
+    const uint32_t t = rest << 16 | ((uint32_t)(a >> i) & 0xffffu), d = t / n;
+    rest = t - d * n;
+    q = q << 16 | d;
+  }
+  return q;
 }
 
 // Items and units of one sequence's key-value head.
@@ -397,23 +407,36 @@ struct Line {
     return (int)((ctx + end + kTile - 1) / kTile);
   }
   // units of the items before item i
-  __device__ int64_t before(int i) const {
-    if (!causal || i == 0) return (int64_t)i * (tiles(0) + extra);
-    return floor_sum(i, kTile, step, (int64_t)ctx + step + kTile - 1) + (int64_t)i * extra;
+  __device__ __forceinline__ int64_t before(int i) const {
+    if (!causal) return (int64_t)i * (tiles(0) + extra);
+    return floor_sum(i, kTile, step, (uint32_t)ctx + step + kTile - 1) + (int64_t)i * extra;
   }
-  __device__ int64_t units() const {
+  __device__ __forceinline__ int64_t units() const {
     if (n <= step) return n > 0 ? tiles(0) + extra : 0;  // (one item)
     return before(items() - 1) + tiles(items() - 1) + extra;
   }
-  // the item that unit u is in
-  __device__ int item_of(int64_t u) const {
+  // The item that unit u is in; u becomes its number within the item.
+  __device__ __forceinline__ int item_of(int64_t& u) const {
     if (n <= step) return 0;
-    if (!causal) return (int)div64(u, tiles(0) + extra);
+    if (!causal) {  // (at most 256 tokens: the units of a head fit 32 bits)
+      const uint32_t per = tiles(0) + extra, i = (uint32_t)u / per;
+      u -= (int64_t)i * per;
+      return (int)i;
+    }
     int lo = 0, hi = items();
+    int64_t at = 0;
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (before(mid) <= u) lo = mid; else hi = mid;
+      const int64_t x = before(mid);
+      if (x <= u) {
+        lo = mid;
+        at = x;
+      } else {
+        hi = mid;
+      }
     }
+    u -= at;
     return lo;
   }
 };
@@ -433,7 +456,7 @@ __device__ __forceinline__ bool line_of(const AttendParams& p, int b, int extra,
 struct Cut {
   int64_t q;
   uint32_t r, active;
-  __device__ Cut(int64_t total, int n) : q(n ? div64(total, n) : 0), r((uint32_t)(total - q * n)), active(n) {}
+  __device__ Cut(int64_t total, int n) : q(n ? div_small(total, n) : 0), r((uint32_t)(total - q * n)), active(n) {}
   __device__ int64_t start(int w) const { return q * w + r * (uint32_t)w / active; }
 };
 
@@ -535,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int worker = blockIdx.x;
   volatile int32_t* abort = &hdr->abort;
-  const long long wl = p.wait_limit;
+  const int wl = p.wait_limit;
 
   // The swizzle wants tiles on 1024-byte boundaries; dynamic shared memory
   // starts on one where a kernel has no other.
@@ -767,6 +790,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t o = (uint32_t)(e & 3) * 2, h = e >> 2;
                 mma_ss(t_s, q_desc + h * (kHalfBytes >> 4) + o, b + h * (kHalfBytes >> 4) + o, id_s, e > 0);
               }
+              // The product two steps ago is done as well when the scores are
+              // announced: the softmax group need not wait for the weights' place.
+              if (C::kPs > 1 && done > 1 && !wait(&hdr->pv_done[slot][done & 1], (done - 2) >> 1)) break;
               mma_commit(smem_u32(&hdr->s_full[slot]));
             }
             release(at, g.two);
@@ -824,12 +850,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (b < p.tok.batch && !(line_of(p, b, extra, &s, &l) && (per = l.units()) > 0)) ++b;
             if (b >= p.tok.batch) break;  // (cannot be: the units add up)
           }
-          const int head = (int)div64(off, per);
-          int64_t r = off - head * per;
+          // (kv_heads < 2^16)
+          int h = 0;
+          int64_t r = off;
+#pragma unroll 1
+          for (int i = 15; i >= 0; --i)
+            if (r >= per << i) {
+              r -= per << i;
+              h |= 1 << i;
+            }
           int item = l.item_of(r);
-          r -= l.before(item);
           // the rest of this sequence, segment by segment
-          int h = head;
           while (left > 0 && h < p.kv.kv_heads) {
             const int tiles = l.tiles(item);
             const int64_t take = min((int64_t)extra + tiles - r, left);
@@ -933,10 +964,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&hdr->s_read[grp]));
       };
-      // The output product `back` steps ago is done.  kPs steps ago: its weights'
-      // place is free.  (Warps without rows wait as well: a warp must not
-      // announce a step's weights before the group's others have announced those
-      // that were in the same place.)  One step ago: the accumulator is at rest.
+      // The output product `back` steps ago is done.  One step ago: the
+      // accumulator is at rest, and with one place for the weights it is free.
+      // (With two, the scores' announcement says that the place is free.  In
+      // either case warps without rows wait as well: a warp must not announce a
+      // step's weights before the group's others have announced those that were in
+      // the same place.)
       auto product_done = [&](uint32_t back) {
         const uint32_t j = n_s - back;
         return n_s < back || mbar_wait(smem_u32(&hdr->pv_done[grp][j & 1]), (j >> 1) & 1, wl, abort);
@@ -950,8 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 4; j < W; j += 2)
           mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        bool ok = product_done(C::kPs);
-        tc_fence_after();
+        bool ok = true;
+        if (C::kPs == 1) {
+          ok = product_done(1);
+          tc_fence_after();
+        }
         // Move the reference maximum only for a large growth (the first finite
         // score's among them); the accumulator exists from the second step on.
         const bool grow = (top - m) * p.c > kRescale;
@@ -1021,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
           } else {
             mbar_arrive(smem_u32(&hdr->s_read[grp]));
-            ok &= product_done(C::kPs);
+            if (C::kPs == 1) ok &= product_done(1);
           }
           mbar_arrive(smem_u32(&hdr->p_ready[grp][n_s & 1]));
         }
@@ -1052,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = weigh(s);
           } else {
             mbar_arrive(smem_u32(&hdr->s_read[grp]));
-            ok = product_done(C::kPs);
+            ok = C::kPs > 1 || product_done(1);
           }
           if (!__all_sync(0xffffffffu, ok)) {
             stop = true;
@@ -1152,17 +1188,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           tmem_arrived(o);
           float v[32];
-          if (g.two) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]);
-          } else {
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;  // (two M tiles: f0 is 1)
+          if (!g.two && used1) {
+            tmem_arrived(o1);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f0;
-            if (used1) {
-              tmem_arrived(o1);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o1[j]), f1, v[j]);
-            }
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o1[j]), f1, v[j]);
           }
           if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
           if (live && g.part < 0) {
@@ -1469,7 +1500,7 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   p.descs = reinterpret_cast<Seg*>(ws);
   ws += (size_t)p.workers * sizeof(Seg);
   p.errs = reinterpret_cast<int32_t*>(ws);
-  p.wait_limit = a->wait_polls > 0 ? a->wait_polls : kWaitLimit;
+  p.wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
   p.withhold = a->withhold;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
