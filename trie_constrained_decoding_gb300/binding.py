@@ -401,6 +401,16 @@ def _rows(t, dtype, device, what: str, heads: int, head_dim: int):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * head_dim
 
 
+def _empty(n: int, dtype, device, stream: int):
+    """A buffer that belongs to the stream its kernels run on: memory of another stream may still be in use there."""
+    import torch
+    if stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(n, dtype=dtype, device=device)
+    own = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(own):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 class KvCache:
     """A paged key-value cache over a torch CUDA tensor
     [layers, pages, 2 (keys, values), kv_heads, page_size, head_dim], bf16 or f16.
@@ -409,7 +419,8 @@ class KvCache:
     and the lengths.  ``status`` arguments are int32 tensors, one code per
     sequence (per pair for copy_pages); left out, they go to a buffer of the
     object that raise_on_error() reads.  Calls on one object use its buffers
-    (that status, and a workspace per stream) and belong to one host thread.
+    (that status and a workspace, a pair of them per stream) and belong to one
+    host thread.
     """
 
     def __init__(self, pool):
@@ -424,7 +435,7 @@ class KvCache:
         self._kv = _Kv(pool.data_ptr(), pool.device.index, types[pool.dtype], self.layers, self.pages, self.kv_heads,
                        self.page_size, self.head_dim)
         self._kvp = ctypes.byref(self._kv)
-        self._i32, self._i64, self._f32 = torch.int32, torch.int64, torch.float32
+        self._i32, self._i64, self._f32, self._u8 = torch.int32, torch.int64, torch.float32, torch.uint8
         # (a decode step's calls are a few microseconds long: asking for the stream object would be a good part)
         index, raw = pool.device.index, getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(index).cuda_stream)
@@ -432,8 +443,8 @@ class KvCache:
         _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
         self._ws_bytes, self._ws = need.value, {}
         self._wait_test = (0, 0)
-        self._status = torch.zeros(64, dtype=torch.int32, device=pool.device)
-        self._n_status = 0
+        self._status, self._last = {}, None  # per stream; the last one used and how much of it
+        self._kept = []                      # outgrown ones: a captured graph may still write to them
 
     def _stream(self, stream):
         if stream is None:
@@ -445,14 +456,16 @@ class KvCache:
             raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {self.device}")
         return t.data_ptr()
 
-    def _codes(self, status, n: int):
+    def _codes(self, status, n: int, stream: int):
         if status is not None:
             return self._ints(status, (n,), "status")
-        if n > self._status.numel():
-            import torch
-            self._status = torch.zeros(2 * n, dtype=torch.int32, device=self.device)
-        self._n_status = n
-        return self._status.data_ptr()
+        own = self._status.get(stream)
+        if own is None or n > own.shape[0]:
+            if own is not None:
+                self._kept.append(own)
+            own = self._status[stream] = _empty(max(64, 2 * n), self._i32, self.device, stream)
+        self._last = (own, n)
+        return own.data_ptr()
 
     def _tokens(self, n, cu, ctx_lens, page_table):
         batch, width = page_table.shape
@@ -487,8 +500,8 @@ class KvCache:
                     None if positions is None else self._ints(positions, (n,), "positions"), bool(interleaved),
                     *_rows(q_out, dtype, device, "q_out", hq, d))
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
-        _check(_kv_append(self._kvp, layer, t, a, self._codes(status, t.batch), self._stream(stream)),
-               "tc_kv_append")
+        s = self._stream(stream)
+        _check(_kv_append(self._kvp, layer, t, a, self._codes(status, t.batch, s), s), "tc_kv_append")
 
     def attend(self, layer: int, q, cu_tokens, ctx_lens, page_table, out, max_tokens: int, scale=None, tree=None,
                lse=None, status=None, stream=None):
@@ -518,9 +531,8 @@ class KvCache:
         s = self._stream(stream)
         ws = self._ws.get(s)
         if ws is None:
-            import torch
-            ws = self._ws[s] = torch.empty(self._ws_bytes, dtype=torch.uint8, device=device)
-        _check(_attend(self._kvp, layer, t, a, ws.data_ptr(), self._ws_bytes, self._codes(status, t.batch), s),
+            ws = self._ws[s] = _empty(self._ws_bytes, self._u8, device, s)
+        _check(_attend(self._kvp, layer, t, a, ws.data_ptr(), self._ws_bytes, self._codes(status, t.batch, s), s),
                "tc_attend")
 
     def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
@@ -530,22 +542,26 @@ class KvCache:
 
     def copy_pages(self, src, dst, status=None, stream=None):
         """tc_kv_copy_pages: page dst[i] becomes page src[i] in every layer."""
-        n = src.shape[0]
+        n, s = src.shape[0], self._stream(stream)
         _check(_kv_copy_pages(self._kvp, self._ints(src, (n,), "src"), self._ints(dst, (n,), "dst"), n,
-                              self._codes(status, n), self._stream(stream)), "tc_kv_copy_pages")
+                              self._codes(status, n, s), s), "tc_kv_copy_pages")
 
     def compact(self, page_table, ctx_lens, path, n_path, lens_out, status=None, stream=None):
         """tc_kv_compact: slot ctx_lens[b] + i takes what slot ctx_lens[b] + path[b, i] holds, i < n_path[b];
         lens_out = ctx_lens + n_path."""
         t = self._tokens(0, None, ctx_lens, page_table)
-        b, wide = t.batch, path.shape[-1]
+        b, wide, s = t.batch, path.shape[-1], self._stream(stream)
         _check(_kv_compact(self._kvp, t, self._ints(path, (b, wide), "path"), wide,
                            self._ints(n_path, (b,), "n_path"), self._ints(lens_out, (b,), "lens_out"),
-                           self._codes(status, b), self._stream(stream)), "tc_kv_compact")
+                           self._codes(status, b, s), s), "tc_kv_compact")
 
     def raise_on_error(self):
         """Wait for the device and raise the first error of the last call made without `status`."""
-        for b, code in enumerate(self._status[:self._n_status].tolist()):
+        import torch
+        if self._last is None:
+            return
+        torch.cuda.synchronize(self.device)
+        for b, code in enumerate(self._last[0][:self._last[1]].tolist()):
             if code != TC_OK:
                 raise TcError(code, f"sequence {b}")
 
@@ -564,14 +580,16 @@ def tree_masks(parents, cu_tokens, ctx_lens, masks, positions=None, status=None,
     if masks.dtype is not torch.int64 or masks.device != dev or masks.dim() != 2 or masks.shape[0] != n or \
             not masks.is_contiguous():
         raise ValueError("masks must be a contiguous int64 tensor [tokens, words]")
-    if status is None:
-        status = torch.empty(batch, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        s = _stream_ptr(stream)
+        if status is None:
+            status = _empty(batch, torch.int32, dev, s)
     t = _Tokens(batch, n, _int_tensor(cu_tokens, (batch + 1,), dev, "cu_tokens"),
                 _int_tensor(ctx_lens, (batch,), dev, "ctx_lens"), None, 0)
     with torch.cuda.device(dev):
         _check(_tree_masks(ctypes.byref(t), _int_tensor(parents, (n,), dev, "parents"), masks.shape[1], masks.data_ptr(),
                            None if positions is None else _int_tensor(positions, (n,), dev, "positions"),
-                           _int_tensor(status, (batch,), dev, "status"), _stream_ptr(stream)), "tc_tree_masks")
+                           _int_tensor(status, (batch,), dev, "status"), s), "tc_tree_masks")
     return status
 
 
