@@ -13,12 +13,12 @@
 // end (last product, output) take.  The units of all items form one line that is
 // cut into equal parts, one per CTA (one CTA per SM), whatever the mixture of
 // lengths: a long context is split over many CTAs, many short ones share one, and
-// a cut that falls into an item's beginning or end splits nothing.  (Tiles alone:
-// a prompt of 8192 558 us against 483, 16 short prompts 63 against 53, a decode
-// step of 64 sequences 205 against 185.  All of the cost before the tiles: 486,
-// 55, 184; two before and two after at head_dim 128: 490, 55, 185.)  Every CTA
-// works its part out from the lengths on the device, so the launch depends on
-// none of them and can be captured.  An item that a cut falls into leaves
+// a cut that falls into an item's beginning or end splits nothing.  (Against
+// tiles alone: a prompt of 8192 416 us, was 488; 16 short prompts 45.5, was 53; a
+// decode step of 64 sequences 180, was 192.  With three units before and none
+// after a prompt of 2048 takes 156 us instead of 148, with two and two 151.)
+// Every CTA works its part out from the lengths on the device, so the launch
+// depends on none of them and can be captured.  An item that a cut falls into leaves
 // unnormalised partial results in 32 bits, at most two per CTA, which a second
 // kernel joins.
 //
@@ -33,7 +33,7 @@
 //    O += P V (P in tensor memory), in steps of 64 slots (head_dim 128) or 128
 //    (64).  One thread each, which does nothing but wait for its operands and
 //    issue: one that has both products of a group to look at reacts too late
-//    (a prompt of 8192: 696 us against 512 at that time);
+//    (a prompt of 8192 took 696 us so when it took 512 with two);
 //  - warp 2 hands out the CTA's segments (an item's part) through a small ring;
 //  - warps 8-11 and 12-15 are two softmax groups, one row per thread: a thread
 //    reads its row of S from tensor memory, keeps the row's maximum and sum in
@@ -51,9 +51,9 @@
 // has two places, so that the next weights need not wait for the product of
 // the last (the issuer of the scores waits for the one before that, while its own
 // product runs, and announces both: the group waits once a step, 418 us against
-// 436 for a prompt of 8192).  Steps of 128 slots there would leave room for S and P in one place
-// only, and a step would be one chain of products and softmax.  The scores of a
-// step of 64 read 6 KB of shared memory for 32 cycles of products and take 50;
+// 436 for a prompt of 8192).  Steps of 128 slots there would leave room for S and
+// P in one place only, and a step would be one chain of products and softmax.  The
+// scores of a step of 64 read 6 KB of shared memory for 32 cycles of products and take 50;
 // beside the other product, which reads less, a step of 128 slots takes 576
 // cycles instead of 512 (measured).
 //
@@ -70,15 +70,15 @@
 // rows that see them.
 //
 // What it measured (bf16, 32 query and 8 key-value heads of 128, pages of 64):
-// a prompt of 8192 tokens in 483 us, 1.14 PFLOP/s, 59 % of what the library's
-// matrix product reaches; 16 prompts of 5 to 261 tokens in 53 us; a decode step of
-// 64 sequences with 97 to 8011 slots in 185 us, 5.9 TB/s, 87 % of a copy's rate;
-// one token over 1500 slots in 17 us.  Bound: long prompts by the chain of waits
-// and exponentials that a softmax group goes through in a step (1900 cycles for
-// two groups' 64 slots, 1024 of them products; without any products it would
-// still take 482 us, without the softmax' arithmetic 453); decode by bytes;
-// small calls by the fetch of instructions that no cache holds yet, about 5000
-// cycles before the first load's barrier and 4000 in the first segment.
+// a prompt of 8192 tokens in 436 us back to back, 1.26 PFLOP/s, 65 % of what the
+// library's matrix product reaches (417 us in short runs, 68 %); 16 prompts of 5 to
+// 261 tokens in 45 us; a decode step of 64 sequences with 97 to 8011 slots in 179 us,
+// 6.1 TB/s, 90 % of a copy's rate; one token over 1500 slots in 16.5 us.  Bound: long
+// prompts by the chain of waits and exponentials that a softmax group goes through
+// in a step (0.96 us for both groups' 64 slots, of which the products take 0.53);
+// decode by bytes; small calls and many short items by latencies one after another
+// and the fetch of instructions, as each part of the code runs once an item (6 us
+// for an item of one tile).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1198,8 +1198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
           if (live && g.part < 0) {
             // (64 bytes of a row: whole sectors, and no shared memory is held up
-            // for the next item.  16 bytes a store: a prompt of 2048 188.6 us
-            // against 186, four of 512 53 against 51.5)
+            // for the next item.  16 bytes a store: a prompt of 2048 152 us against
+            // 148, 16 short ones 47 against 45.5)
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = T::pack(v[2 * j] * norm, v[2 * j + 1] * norm);
@@ -1276,12 +1276,12 @@ constexpr int kJoinThreads = 256, kJoinBlocks = 8;
 // the next.  A thread joins four columns of a row (the parts are laid out by
 // columns, so neighbouring rows are neighbours); the parts are added in the
 // order of the workers: the result does not depend on timing.  Bound: latency (a
-// few parts of a few rows; up to 20 MB of partial results when every worker has
-// two, 4 us at a copy's rate).  Blocks a worker, 16 short prompts: 4 72 us, 8 64,
-// 16 64.4, 32 65.5.  Letting the blocks start while the first kernel still runs is
-// slower (one token 18.1 us against 17.4).  The blocks after these write the
-// status of a sequence each (one block, as a warp takes 10 us for the pages of
-// 131,000 slots).
+// few parts of a few rows; up to 40 MB of partial results when every worker has
+// two full ones, 6 us at a copy's rate).  Blocks a worker, 16 short prompts and
+// drafts of 16 sequences: 4 50 and 74.6 us, 8 45.5 and 73.6, 16 43.6 and 75.2.
+// Letting the blocks start while the first kernel still runs is slower (one token
+// 18.1 us against 17.4).  The blocks after these write the status of a sequence
+// each (one block, as a warp takes 10 us for the pages of 131,000 slots).
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
