@@ -38,8 +38,9 @@
 //  - warps 8-11 and 12-15 are two softmax groups, one row per thread: a thread
 //    reads its row of S from tensor memory, keeps the row's maximum and sum in
 //    32 bits, and writes the weights P beside it in the cache's type, which is
-//    what the tensor cores multiply (the sum is of the weights before that
-//    rounding, whose errors have no common sign).
+//    what the tensor cores multiply.  The sum is of the weights before that
+//    rounding: the rounding's errors have a common sign only where weights
+//    coincide, and are then at most half a unit of the type.
 // The two groups always alternate with the tensor cores: with two M tiles each
 // takes one and both use every key-value tile; with one M tile they take the
 // even and the odd tiles of the cache and are joined at the end.
@@ -58,9 +59,16 @@
 // cycles instead of 512 (measured).
 //
 // The maximum that the weights refer to is only moved when a row's maximum
-// has grown by more than 2^8 (the sums hold weights up to 2^8 in 32 bits, and
-// the types' relative precision does not depend on the scale): the
-// accumulator in tensor memory is rescaled then and rarely otherwise.
+// has grown by more than 2^8: the accumulator in tensor memory is rescaled then
+// and rarely otherwise.  bf16 and the sums in 32 bits hold such weights as well as
+// smaller ones.  f16 has few exponents: below 2^-14 a weight would lose bits, below
+// 2^-25 it would vanish from the products but not from the sum, always to one side
+// (131,072 slots of 2^-25 of the largest weight hold 0.4 % of a row).  So its weights,
+// and with them sum and accumulator, carry a factor of 2^7, the most that stays
+// under f16's largest number with the 2^8: what a slot may lose is 2^-32 of the
+// largest weight, below the output's rounding up to 2^20 slots.  (Moving the maximum
+// sooner leaves room for a larger factor but costs time: 2^6 and 2^9 357 us for
+// prompt chunks of head_dim 64, 2^4 and 2^11 375, these 353, as without a factor.)
 //
 // Steps that every row sees entirely run in a loop without masks.  The others
 // (the end of the sequence, the drafted tokens, the diagonal of a prompt) take
@@ -105,7 +113,7 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kStep = D == 128 ? 64 : 128;  // slots of a step
   static constexpr int kSteps = kTile / kStep;       // steps of a tile
-    // What an item's beginning and its end take, in tiles.
+  // What an item's beginning and its end take, in tiles.
   static constexpr int kBegin = D == 128 ? 1 : 2, kEnd = 2;
   // Tensor memory of a group: scores, weights, accumulator.
   static constexpr int kPs = D == 128 ? 2 : 1;  // places of the weights
@@ -515,6 +523,12 @@ template <typename T>
 __device__ __forceinline__ float2 non_finite(uint32_t v) {
   const float2 f = T::unpack(v);
   return make_float2((v & T::kExp) == T::kExp ? f.x : 0.f, (v & (T::kExp << 16)) == (T::kExp << 16) ? f.y : 0.f);
+}
+
+// Logarithm of a row's sum of exponentials.
+template <typename T>
+__device__ __forceinline__ float log_sum(float m, float l, float c) {
+  return l == 0.f ? -INFINITY : (m * c + (log2f(l) - T::kShift)) * kLn2;
 }
 
 // Adds to 32 columns of a row the infinities and NaN that were taken out of the
@@ -952,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int W = C::kStep;
       const int hop = g.two ? 1 : 2;
       const uint64_t c2 = f2(p.c, p.c);
-      float off = 0.f;     // -m c, or 0 while m is -inf
+      float off = 0.f;     // T::kShift - m c, or 0 while m is -inf
       bool first = true;   // no step of this segment yet
       // The scores of a step, read and handed back.
       auto load = [&](uint32_t(&s)[W]) {
@@ -1014,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (grow) {
             m = top;
-            off = -m * p.c;
+            off = T::kShift - m * p.c;
           }
         }
         first = false;
@@ -1228,7 +1242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g.part >= 0)
           p.part_ml[part + rr] = make_float2(m, l);
         else if (p.lse)
-          p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
+          p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = log_sum<T>(m, l, p.c);
       }
       if (!g.two && !meet()) break;  // (ml has been read)
     }
@@ -1331,7 +1345,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
     *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + (int64_t)head * D + 4 * c) * 2) =
         make_uint2(T::pack(v.x * norm, v.y * norm), T::pack(v.z * norm, v.w * norm));
     if (p.lse && c == 0)
-      p.lse[row * p.q_heads + head] = l == 0.f ? -INFINITY : (m * p.c + log2f(l)) * kLn2;
+      p.lse[row * p.q_heads + head] = log_sum<T>(m, l, p.c);
   }
 }
 

@@ -30,7 +30,8 @@ struct TokensView {
   int32_t batch, n_tokens, width;
 };
 
-// 16-bit element types: pairs to and from 32-bit floats.
+// 16-bit element types: pairs to and from 32-bit floats.  kShift is log2 of a
+// factor that the attention's weights carry (attend.cu says why).
 struct Bf16 {
   // acc + 0 * v for each half: zero as long as every v is finite, else NaN.
   static __device__ __forceinline__ uint32_t trace(uint32_t v, uint32_t acc) {
@@ -40,6 +41,7 @@ struct Bf16 {
   }
   static constexpr uint32_t kMma = 1;       // operand type of a tensor-core instruction
   static constexpr uint32_t kExp = 0x7f80;  // exponent bits
+  static constexpr float kShift = 0.f;
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
@@ -57,6 +59,7 @@ struct F16 {
   }
   static constexpr uint32_t kMma = 0;
   static constexpr uint32_t kExp = 0x7c00;
+  static constexpr float kShift = 7.f;
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
   }
