@@ -145,9 +145,10 @@ def decode(tcd, draft: int, batch: int = 4, prompt_len: int = 37, k: int = 3):
         flat = torch.tensor([t for d in drafts for t in d[0]], device="cuda")
         masks = torch.zeros((len(flat), 1), dtype=torch.int64, device="cuda")
         positions = ints([0] * len(flat))
-        tcd.tree_masks(ints([p for d in drafts for p in d[1]]), cu, lens_dev, masks, positions)
+        bad = tcd.tree_masks(ints([p for d in drafts for p in d[1]]), cu, lens_dev, masks, positions)
         hidden = model.forward(flat, cu, lens_dev, rows, max(count), masks, positions)
-        model.cache.raise_on_error()
+        model.cache.raise_on_error()    # (of every call since the last look: all layers, page copies, the prompt)
+        assert not bool(bad.any())
         # constrained steps along the drafts, while every sequence's next token is one of them
         first = np.concatenate(([0], np.cumsum(count)))
         at, paths = [0] * batch, [[] if d else [0] for d in done]

@@ -42,6 +42,10 @@ enum {
  *  dtype      TC_DT_BF16 or TC_DT_F16.
  *  page_size  16, 32, 64 or 128 tokens.      head_dim  64 or 128.
  *  device     the CUDA device the pool lies on; calls run there.
+ *  keep_status  0: a call writes its whole status array.  1: it writes the
+ *             code of a sequence (or pair) only if that is an error and the
+ *             array has TC_OK there, so that one array, which the caller has
+ *             set to TC_OK, gathers the first errors of many calls.
  *
  * Token i of a sequence lies in slot i % page_size of the page that entry
  * i / page_size of the sequence's page table names, in every layer.
@@ -55,6 +59,7 @@ typedef struct tc_kv_t {
   int32_t kv_heads;
   int32_t page_size;
   int32_t head_dim;
+  int32_t keep_status;
 } tc_kv_t;
 
 /*

@@ -340,13 +340,13 @@ def loop_floor(device: int, batch: int, iterations: int, stream=None):
 # ------------------------------------------------- paged cache (include/tcd_cache.h)
 
 DT_BF16, DT_F16 = 0, 1
-TREE_MAX_WORDS, PATH_MAX = 4, 256
+TREE_MAX_WORDS, PATH_MAX, KV_MAX_BATCH = 4, 256, 65536
 
 
 class _Kv(ctypes.Structure):
     _fields_ = [("pool", _vp), ("device", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layers", ctypes.c_int32),
                 ("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32)]
+                ("head_dim", ctypes.c_int32), ("keep_status", ctypes.c_int32)]
 
 
 class _Tokens(ctypes.Structure):
@@ -411,16 +411,34 @@ def _empty(n: int, dtype, device, stream: int):
         return torch.empty(n, dtype=dtype, device=device)
 
 
+def _zeros(n: int, dtype, device, stream: int):
+    import torch
+    t = _empty(n, dtype, device, stream)
+    own = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(own):
+        return t.zero_()
+
+
+class _Own:
+    """What the calls on one stream use where the caller gives nothing: error codes (of sequences, then of pairs of
+    pages) and a workspace."""
+
+    def __init__(self, codes):
+        self.codes, self.at, self.workspace = codes, codes.data_ptr(), None
+        self.used = [0, 0]  # entries that a call may have written
+
+
 class KvCache:
     """A paged key-value cache over a torch CUDA tensor
     [layers, pages, 2 (keys, values), kv_heads, page_size, head_dim], bf16 or f16.
 
     The object holds no cache state: the caller owns the pool, the page tables
     and the lengths.  ``status`` arguments are int32 tensors, one code per
-    sequence (per pair for copy_pages); left out, they go to a buffer of the
-    object that raise_on_error() reads.  Calls on one object use its buffers
-    (that status and a workspace, a pair of them per stream) and belong to one
-    host thread.
+    sequence (per pair for copy_pages), written whole by the call; left out,
+    errors are gathered in a buffer of the object, the first of each sequence
+    (or pair), until raise_on_error() raises and clears them.  Calls on one
+    object use its buffers (those codes and a workspace, a pair of them per
+    stream) and belong to one host thread.
     """
 
     def __init__(self, pool):
@@ -435,16 +453,18 @@ class KvCache:
         self._kv = _Kv(pool.data_ptr(), pool.device.index, types[pool.dtype], self.layers, self.pages, self.kv_heads,
                        self.page_size, self.head_dim)
         self._kvp = ctypes.byref(self._kv)
+        self._kv_keep = _Kv.from_buffer_copy(self._kv)   # for calls whose errors are gathered
+        self._kv_keep.keep_status = 1
+        self._kvp_keep = ctypes.byref(self._kv_keep)
         self._i32, self._i64, self._f32, self._u8 = torch.int32, torch.int64, torch.float32, torch.uint8
         # (a decode step's calls are a few microseconds long: asking for the stream object would be a good part)
         index, raw = pool.device.index, getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(index).cuda_stream)
         need = ctypes.c_int64()
         _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
-        self._ws_bytes, self._ws = need.value, {}
+        self._ws_bytes = need.value
         self._wait_test = (0, 0)
-        self._status, self._last = {}, None  # per stream; the last one used and how much of it
-        self._kept = []                      # outgrown ones: a captured graph may still write to them
+        self._own = {}                       # _Own per stream
 
     def _stream(self, stream):
         if stream is None:
@@ -456,16 +476,19 @@ class KvCache:
             raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {self.device}")
         return t.data_ptr()
 
-    def _codes(self, status, n: int, stream: int):
+    def _buffers(self, stream: int):
+        own = self._own.get(stream)
+        if own is None:
+            own = self._own[stream] = _Own(_zeros(2 * KV_MAX_BATCH, self._i32, self.device, stream))
+        return own
+
+    def _codes(self, status, n: int, stream: int, pairs: int = 0):
+        """Where a call's codes go, behind the description of the cache that says how."""
         if status is not None:
-            return self._ints(status, (n,), "status")
-        own = self._status.get(stream)
-        if own is None or n > own.shape[0]:
-            if own is not None:
-                self._kept.append(own)
-            own = self._status[stream] = _empty(max(64, 2 * n), self._i32, self.device, stream)
-        self._last = (own, n)
-        return own.data_ptr()
+            return self._kvp, self._ints(status, (n,), "status")
+        own = self._buffers(stream)
+        own.used[pairs] = max(own.used[pairs], min(n, KV_MAX_BATCH))
+        return self._kvp_keep, own.at + 4 * KV_MAX_BATCH * pairs
 
     def _tokens(self, n, cu, ctx_lens, page_table):
         batch, width = page_table.shape
@@ -501,7 +524,8 @@ class KvCache:
                     *_rows(q_out, dtype, device, "q_out", hq, d))
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
         s = self._stream(stream)
-        _check(_kv_append(self._kvp, layer, t, a, self._codes(status, t.batch, s), s), "tc_kv_append")
+        kv, codes = self._codes(status, t.batch, s)
+        _check(_kv_append(kv, layer, t, a, codes, s), "tc_kv_append")
 
     def attend(self, layer: int, q, cu_tokens, ctx_lens, page_table, out, max_tokens: int, scale=None, tree=None,
                lse=None, status=None, stream=None):
@@ -529,11 +553,11 @@ class KvCache:
                     words, *_rows(out, dtype, device, "out", hq, d), sums, *self._wait_test)
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
         s = self._stream(stream)
-        ws = self._ws.get(s)
-        if ws is None:
-            ws = self._ws[s] = _empty(self._ws_bytes, self._u8, device, s)
-        _check(_attend(self._kvp, layer, t, a, ws.data_ptr(), self._ws_bytes, self._codes(status, t.batch, s), s),
-               "tc_attend")
+        own = self._buffers(s)
+        if own.workspace is None:
+            own.workspace = _empty(self._ws_bytes, self._u8, device, s)
+        kv, codes = self._codes(status, t.batch, s)
+        _check(_attend(kv, layer, t, a, own.workspace.data_ptr(), self._ws_bytes, codes, s), "tc_attend")
 
     def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
         """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)
@@ -543,27 +567,38 @@ class KvCache:
     def copy_pages(self, src, dst, status=None, stream=None):
         """tc_kv_copy_pages: page dst[i] becomes page src[i] in every layer."""
         n, s = src.shape[0], self._stream(stream)
-        _check(_kv_copy_pages(self._kvp, self._ints(src, (n,), "src"), self._ints(dst, (n,), "dst"), n,
-                              self._codes(status, n, s), s), "tc_kv_copy_pages")
+        kv, codes = self._codes(status, n, s, pairs=1)
+        _check(_kv_copy_pages(kv, self._ints(src, (n,), "src"), self._ints(dst, (n,), "dst"), n, codes, s),
+               "tc_kv_copy_pages")
 
     def compact(self, page_table, ctx_lens, path, n_path, lens_out, status=None, stream=None):
         """tc_kv_compact: slot ctx_lens[b] + i takes what slot ctx_lens[b] + path[b, i] holds, i < n_path[b];
         lens_out = ctx_lens + n_path."""
         t = self._tokens(0, None, ctx_lens, page_table)
         b, wide, s = t.batch, path.shape[-1], self._stream(stream)
-        _check(_kv_compact(self._kvp, t, self._ints(path, (b, wide), "path"), wide,
-                           self._ints(n_path, (b,), "n_path"), self._ints(lens_out, (b,), "lens_out"),
-                           self._codes(status, b, s), s), "tc_kv_compact")
+        kv, codes = self._codes(status, b, s)
+        _check(_kv_compact(kv, t, self._ints(path, (b, wide), "path"), wide, self._ints(n_path, (b,), "n_path"),
+                           self._ints(lens_out, (b,), "lens_out"), codes, s), "tc_kv_compact")
 
     def raise_on_error(self):
-        """Wait for the device and raise the first error of the last call made without `status`."""
+        """Wait for the device, and if a call made without `status` since the last error raised has failed, clear
+        all codes and raise one of the first errors."""
         import torch
-        if self._last is None:
+        if not self._own:
             return
         torch.cuda.synchronize(self.device)
-        for b, code in enumerate(self._last[0][:self._last[1]].tolist()):
-            if code != TC_OK:
-                raise TcError(code, f"sequence {b}")
+        found = None
+        for own in self._own.values():
+            for pairs, what in enumerate(("sequence", "page copy")):
+                codes = own.codes[KV_MAX_BATCH * pairs:][:own.used[pairs]]
+                for i, code in enumerate(codes.tolist()):
+                    if code != TC_OK:
+                        found = found or (code, f"{what} {i}")
+                        codes.zero_()
+                        break
+        if found:
+            torch.cuda.synchronize(self.device)
+            raise TcError(*found)
 
 
 def _int_tensor(t, shape, device, what: str):

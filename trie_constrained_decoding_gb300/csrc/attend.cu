@@ -1311,7 +1311,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
     for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) late |= __ldcg(p.errs + i) != 0;
     ok = __syncthreads_and(ok);
     late = __syncthreads_or(late);
-    if (threadIdx.x == 0) p.status[b] = late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS;
+    if (threadIdx.x == 0)
+      set_status(p.status, b, late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS, p.kv.keep);
     return;
   }
   const int w0 = blockIdx.x / kJoinBlocks, y = blockIdx.x % kJoinBlocks;

@@ -39,6 +39,7 @@ KvView kv_view(const tc_kv_t* kv, int32_t layer) {
   v.kv_heads = kv->kv_heads;
   v.page_size = kv->page_size;
   v.page_shift = __builtin_ctz((unsigned)kv->page_size);
+  v.keep = kv->keep_status != 0;
   return v;
 }
 
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kBlock, 4) append_kernel(const AppendParams p)
         }
     }
     ok = __all_sync(0xffffffffu, ok);
-    if (lane == 0) p.status[b] = ok ? TC_OK : TC_ERR_BOUNDS;
+    if (lane == 0) set_status(p.status, b, ok ? TC_OK : TC_ERR_BOUNDS, p.kv.keep);
     return;
   }
   const int i = (int)(w / p.split), part = (int)(w % p.split);
@@ -289,11 +290,12 @@ constexpr int kCopyUnroll = 8;
 // pages of 64 slots, 8 heads of 128, in 16 layers take 77 us (6.6 TB/s, 98 % of
 // a plain copy); 4 or 16 words a thread make no difference.
 __global__ void __launch_bounds__(kBlock) copy_pages_kernel(uint8_t* pool, int32_t pages, int64_t page_bytes,
-                                                           const int32_t* src, const int32_t* dst, int32_t* status) {
+                                                           const int32_t* src, const int32_t* dst, int32_t* status,
+                                                           int32_t keep) {
   const int pair = blockIdx.y, layer = blockIdx.z;
   const int a = __ldg(src + pair), b = __ldg(dst + pair);
   const bool ok = (uint32_t)a < (uint32_t)pages && (uint32_t)b < (uint32_t)pages;
-  if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) status[pair] = ok ? TC_OK : TC_ERR_BOUNDS;
+  if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) set_status(status, pair, ok ? TC_OK : TC_ERR_BOUNDS, keep);
   if (!ok) return;
   const uint4* from = reinterpret_cast<const uint4*>(pool + ((int64_t)layer * pages + a) * page_bytes);
   uint4* to = reinterpret_cast<uint4*>(pool + ((int64_t)layer * pages + b) * page_bytes);
@@ -319,6 +321,7 @@ struct CompactParams {
   const int32_t* n_path;
   int32_t* lens_out;
   int32_t* status;
+  int32_t keep;
 };
 
 constexpr int kMoveUnroll = 4;
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(const CompactParams p) 
   ok = __syncthreads_and(ok);
   if (blockIdx.x == 0 && tid == 0) {
     p.lens_out[b] = ok ? ctx + n : ctx;
-    p.status[b] = ok ? TC_OK : TC_ERR_BOUNDS;
+    set_status(p.status, b, ok ? TC_OK : TC_ERR_BOUNDS, p.keep);
   }
   if (!ok) return;
   const int64_t col = (int64_t)blockIdx.x * kBlock + tid;
@@ -475,7 +478,8 @@ extern "C" tc_status tc_kv_copy_pages(const tc_kv_t* kv, const int32_t* src, con
   const int64_t per_block = (int64_t)kBlock * kCopyUnroll * 16;
   const dim3 grid((unsigned)((page_bytes + per_block - 1) / per_block), (unsigned)n, (unsigned)kv->layers);
   copy_pages_kernel<<<grid, kBlock, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint8_t*>(kv->pool), kv->pages,
-                                                                           page_bytes, src, dst, status);
+                                                                           page_bytes, src, dst, status,
+                                                                           kv->keep_status != 0);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_copy_pages");
 }
@@ -510,6 +514,7 @@ extern "C" tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens,
   p.n_path = n_path;
   p.lens_out = lens_out;
   p.status = status;
+  p.keep = v.keep;
   const int64_t cols = (int64_t)kv->layers * 2 * kv->kv_heads * p.row_words;
   const dim3 grid((unsigned)((cols + kBlock - 1) / kBlock), (unsigned)tokens->batch);
   compact_kernel<<<grid, kBlock, 0, static_cast<cudaStream_t>(stream)>>>(p);

@@ -20,7 +20,12 @@ struct KvView {
   int32_t kv_heads;
   int32_t page_size;  // a power of two
   int32_t page_shift; // its logarithm
+  int32_t keep;       // only errors are written to the status, and only over TC_OK
 };
+
+__device__ __forceinline__ void set_status(int32_t* status, int64_t i, int32_t code, int32_t keep) {
+  if (!keep || (code != TC_OK && status[i] == TC_OK)) status[i] = code;
+}
 
 // The tokens of a call (tc_tokens_t by value).
 struct TokensView {
