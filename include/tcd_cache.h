@@ -17,7 +17,10 @@
  * and launch nothing, errors found on the device are recorded per sequence.
  * Calls are stateless (no handle holds anything between calls) and may be
  * made from several threads and streams as long as they write different
- * memory; a workspace belongs to one call at a time.
+ * memory; a workspace belongs to one call at a time.  A captured call keeps the
+ * addresses it was given: graphs that may run at the same time, or beside calls
+ * on a stream, need workspaces of their own, for as long as they exist
+ * (tc_capture_id and tc_capture_watch tell a caller when).
  */
 #ifndef TCD_CACHE_H
 #define TCD_CACHE_H
@@ -291,6 +294,32 @@ tc_status tc_pages_row(const tc_pages* p, int32_t seq, int32_t* row, int32_t wid
 
 /* Pages that nobody holds. */
 tc_status tc_pages_free_count(const tc_pages* p, int32_t* n);
+
+/*
+ * For callers that manage the buffers of captured calls.
+ *
+ * tc_capture_id - *id receives a number that names the capture a stream is part
+ * of (another for each capture of the process), 0 if it is being captured into no
+ * graph.
+ *
+ * tc_capture_watch - *gone receives a host word that is 0 and becomes 1 when the
+ * graph that `stream` is being captured into, all graphs made from it and their
+ * last launch have ended: buffers given to its calls may be freed then.
+ * TC_ERR_INVALID_ARG if the stream is not being captured.
+ *
+ * tc_capture_unwatch - frees such a word, once it is 1.
+ *
+ * tc_capture_mode - swaps the calling thread's capture mode with *mode (0 global,
+ * 1 thread, 2 relaxed: memory for the buffers may be allocated during a capture).
+ *
+ * tc_clear_now - sets device memory to zero by way of `stream`, which must not be
+ * part of a capture, and waits for it; allowed while other streams are captured.
+ */
+tc_status tc_capture_id(void* stream, uint64_t* id);
+tc_status tc_capture_watch(void* stream, int32_t** gone);
+void tc_capture_unwatch(int32_t* gone);
+tc_status tc_capture_mode(int32_t* mode);
+tc_status tc_clear_now(void* ptr, int64_t bytes, void* stream);
 
 #ifdef __cplusplus
 }

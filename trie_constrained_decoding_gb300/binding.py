@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional, Sequence
 
 import numpy as np
@@ -385,6 +386,11 @@ _pages_fork = _decl("tc_pages_fork", ctypes.c_int, [_vp, ctypes.c_int32, ctypes.
 _pages_trim = _decl("tc_pages_trim", ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int64])
 _pages_row = _decl("tc_pages_row", ctypes.c_int, [_vp, ctypes.c_int32, _i32p, ctypes.c_int32, _i32p])
 _pages_free_count = _decl("tc_pages_free_count", ctypes.c_int, [_vp, _i32p])
+_capture_id = _decl("tc_capture_id", ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint64)])
+_capture_watch = _decl("tc_capture_watch", ctypes.c_int, [_vp, ctypes.POINTER(_i32p)])
+_capture_unwatch = _decl("tc_capture_unwatch", None, [_i32p])
+_capture_mode = _decl("tc_capture_mode", ctypes.c_int, [_i32p])
+_clear_now = _decl("tc_clear_now", ctypes.c_int, [_vp, ctypes.c_int64, _vp])
 
 
 def _rows(t, dtype, device, what: str, heads: int, head_dim: int):
@@ -419,13 +425,65 @@ def _zeros(n: int, dtype, device, stream: int):
         return t.zero_()
 
 
-class _Own:
-    """What the calls on one stream use where the caller gives nothing: error codes (of sequences, then of pairs of
-    pages) and a workspace."""
+class _Codes:
+    """Gathered error codes: of sequences, then of pairs of pages."""
 
     def __init__(self, codes):
-        self.codes, self.at, self.workspace = codes, codes.data_ptr(), None
+        self.codes, self.at = codes, codes.data_ptr()
         self.used = [0, 0]  # entries that a call may have written
+
+
+class _Own:
+    """What calls use where the caller gives nothing: of one stream, or of one graph that it is captured into."""
+
+    def __init__(self, codes: _Codes, stream: int, gone=None):
+        self.codes, self.workspace, self.place, self.stream = codes, None, None, stream  # (whose memory it is)
+        self.gone = gone                     # (captured) a word: 1 when the graph is gone
+
+    def idle(self) -> bool:
+        return bool(self.gone) and self.gone[0] != 0
+
+    def __del__(self):
+        try:
+            if self.idle():
+                _capture_unwatch(self.gone)
+        except Exception:
+            pass
+
+
+_held = []  # of captured calls: they stay while their graph does, whatever becomes of the KvCache
+_held_lock = threading.Lock()
+
+
+def _hold(own: _Own):
+    with _held_lock:
+        _held[:] = [o for o in _held if not o.idle()]
+        _held.append(own)
+
+
+def _stream_aside(device) -> int:
+    """A stream that is not part of a capture."""
+    import torch
+    n = ctypes.c_uint64()
+    for _ in range(64):
+        s = torch.cuda.Stream(device).cuda_stream
+        _check(_capture_id(s, ctypes.byref(n)), "tc_capture_id")
+        if not n.value:
+            return s
+    raise RuntimeError("every stream is being captured")
+
+
+def _empty_aside(n: int, dtype, device, stream: int, clear: bool):
+    """A buffer for captured calls, out of the memory of a stream aside.  What that memory was used for before is
+    over when it is returned (and it is cleared): a graph waits for nothing on that stream."""
+    mode = ctypes.c_int32(2)                 # (the allocator may have to ask the driver for memory)
+    _check(_capture_mode(ctypes.byref(mode)), "tc_capture_mode")
+    try:
+        t = _empty(n, dtype, device, stream)
+    finally:
+        _check(_capture_mode(ctypes.byref(mode)), "tc_capture_mode")
+    _check(_clear_now(t.data_ptr(), n * t.element_size() if clear else 0, stream), "tc_clear_now")
+    return t
 
 
 class KvCache:
@@ -436,9 +494,12 @@ class KvCache:
     and the lengths.  ``status`` arguments are int32 tensors, one code per
     sequence (per pair for copy_pages), written whole by the call; left out,
     errors are gathered in a buffer of the object, the first of each sequence
-    (or pair), until raise_on_error() raises and clears them.  Calls on one
-    object use its buffers (those codes and a workspace, a pair of them per
-    stream) and belong to one host thread.
+    (or pair), until raise_on_error() raises and clears them.  attend's
+    ``workspace`` is a tensor of at least ``workspace_bytes`` bytes that belongs
+    to one call at a time; left out, it is a buffer of the object as well, one
+    per stream, and one per stream of every capture: a captured graph shares
+    none with other graphs or with calls on a stream, and its buffers stay while
+    it exists.  Calls on one object belong to one host thread.
     """
 
     def __init__(self, pool):
@@ -462,9 +523,12 @@ class KvCache:
         self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(index).cuda_stream)
         need = ctypes.c_int64()
         _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
-        self._ws_bytes = need.value
+        self.workspace_bytes = need.value
         self._wait_test = (0, 0)
         self._own = {}                       # _Own per stream
+        self._captured, self._graph_codes = {}, None   # _Own per capture and stream; their common codes
+        self._capture = ctypes.c_uint64()
+        self._capture_ref = ctypes.byref(self._capture)
 
     def _stream(self, stream):
         if stream is None:
@@ -477,18 +541,52 @@ class KvCache:
         return t.data_ptr()
 
     def _buffers(self, stream: int):
+        if stream:                           # (the default stream cannot be captured)
+            _check(_capture_id(stream, self._capture_ref), "tc_capture_id")
+            if self._capture.value:
+                return self._captured.get((self._capture.value, stream)) or \
+                    self._capture_buffers(self._capture.value, stream)
         own = self._own.get(stream)
         if own is None:
-            own = self._own[stream] = _Own(_zeros(2 * KV_MAX_BATCH, self._i32, self.device, stream))
+            own = self._own[stream] = _Own(_Codes(_zeros(2 * KV_MAX_BATCH, self._i32, self.device, stream)), stream)
+        return own
+
+    def _capture_buffers(self, capture: int, stream: int):
+        """Their memory is no graph's own and the codes are cleared outside of the capture: a launch must not clear
+        what the one before has left.  (Only errors are written: all graphs of the object share the codes.)"""
+        for key in [k for k, o in self._captured.items() if o.idle()]:
+            del self._captured[key]
+        aside = _stream_aside(self.device)
+        if self._graph_codes is None:
+            self._graph_codes = _Codes(_empty_aside(2 * KV_MAX_BATCH, self._i32, self.device, aside, clear=True))
+        gone = _i32p()
+        if _capture_watch(stream, ctypes.byref(gone)) != TC_OK:
+            gone = None                      # (never known to be gone: kept)
+        own = self._captured[capture, stream] = _Own(self._graph_codes, aside, gone)
+        _hold(own)
         return own
 
     def _codes(self, status, n: int, stream: int, pairs: int = 0):
         """Where a call's codes go, behind the description of the cache that says how."""
         if status is not None:
             return self._kvp, self._ints(status, (n,), "status")
-        own = self._buffers(stream)
+        own = self._buffers(stream).codes
         own.used[pairs] = max(own.used[pairs], min(n, KV_MAX_BATCH))
         return self._kvp_keep, own.at + 4 * KV_MAX_BATCH * pairs
+
+    def _workspace(self, workspace, stream: int):
+        if workspace is None:
+            own = self._buffers(stream)
+            if own.place is None:
+                if own.stream == stream:
+                    own.workspace = _empty(self.workspace_bytes, self._u8, self.device, stream)
+                else:
+                    own.workspace = _empty_aside(self.workspace_bytes, self._u8, self.device, own.stream, clear=False)
+                own.place = own.workspace.data_ptr(), self.workspace_bytes
+            return own.place
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def _tokens(self, n, cu, ctx_lens, page_table):
         batch, width = page_table.shape
@@ -528,7 +626,7 @@ class KvCache:
         _check(_kv_append(kv, layer, t, a, codes, s), "tc_kv_append")
 
     def attend(self, layer: int, q, cu_tokens, ctx_lens, page_table, out, max_tokens: int, scale=None, tree=None,
-               lse=None, status=None, stream=None):
+               lse=None, status=None, stream=None, workspace=None):
         """tc_attend: q and out [n, q_heads, head_dim]; tree int64 [n, words] (tree_masks) or None for the causal
         mask; scale defaults to head_dim ** -0.5; lse float32 [n, q_heads] or None."""
         d, shape = self.head_dim, q.shape
@@ -553,11 +651,8 @@ class KvCache:
                     words, *_rows(out, dtype, device, "out", hq, d), sums, *self._wait_test)
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
         s = self._stream(stream)
-        own = self._buffers(s)
-        if own.workspace is None:
-            own.workspace = _empty(self._ws_bytes, self._u8, device, s)
         kv, codes = self._codes(status, t.batch, s)
-        _check(_attend(kv, layer, t, a, own.workspace.data_ptr(), self._ws_bytes, codes, s), "tc_attend")
+        _check(_attend(kv, layer, t, a, *self._workspace(workspace, s), codes, s), "tc_attend")
 
     def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
         """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)
@@ -584,11 +679,14 @@ class KvCache:
         """Wait for the device, and if a call made without `status` since the last error raised has failed, clear
         all codes and raise one of the first errors."""
         import torch
-        if not self._own:
+        gathered = [o.codes for o in self._own.values()]
+        if self._graph_codes:
+            gathered.append(self._graph_codes)
+        if not gathered:
             return
         torch.cuda.synchronize(self.device)
         found = None
-        for own in self._own.values():
+        for own in gathered:
             for pairs, what in enumerate(("sequence", "page copy")):
                 codes = own.codes[KV_MAX_BATCH * pairs:][:own.used[pairs]]
                 for i, code in enumerate(codes.tolist()):
