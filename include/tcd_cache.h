@@ -218,9 +218,9 @@ tc_status tc_tree_masks(const tc_tokens_t* tokens, const int32_t* parents, int32
 
 /*
  * tc_kv_copy_pages - copy whole pages, in every layer: page dst[i] becomes
- * page src[i].  src and dst (device) int32[n]; no page may be written twice,
- * nor be both read and written by one call.  status (device) int32[n]:
- * TC_ERR_BOUNDS for a pair with a page id out of range (not copied).
+ * page src[i].  src and dst (device) int32[n], n <= TC_KV_MAX_BATCH; no page may
+ * be written twice, nor be both read and written by one call.  status (device)
+ * int32[n]: TC_ERR_BOUNDS for a pair with a page id out of range (not copied).
  */
 tc_status tc_kv_copy_pages(const tc_kv_t* kv, const int32_t* src, const int32_t* dst, int32_t n, int32_t* status,
                            void* stream);

@@ -286,20 +286,21 @@ __global__ void __launch_bounds__(kBlock) tree_mask_kernel(const TokensView t, c
 constexpr int kCopyUnroll = 8;
 
 // A page of one layer is one run of bytes; a block copies kBlock * kCopyUnroll
-// 16-byte words of it, every load before the first store.  Bound: bytes: 61
+// 16-byte words of it, every load before the first store.  Grid (blocks of a page
+// x pairs, layers): the second and third axes end at 65,535.  Bound: bytes: 61
 // pages of 64 slots, 8 heads of 128, in 16 layers take 77 us (6.6 TB/s, 98 % of
 // a plain copy); 4 or 16 words a thread make no difference.
 __global__ void __launch_bounds__(kBlock) copy_pages_kernel(uint8_t* pool, int32_t pages, int64_t page_bytes,
                                                            const int32_t* src, const int32_t* dst, int32_t* status,
-                                                           int32_t keep) {
-  const int pair = blockIdx.y, layer = blockIdx.z;
+                                                           int32_t keep, unsigned blocks) {
+  const int pair = blockIdx.x / blocks, part = blockIdx.x % blocks, layer = blockIdx.y;
   const int a = __ldg(src + pair), b = __ldg(dst + pair);
   const bool ok = (uint32_t)a < (uint32_t)pages && (uint32_t)b < (uint32_t)pages;
-  if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) set_status(status, pair, ok ? TC_OK : TC_ERR_BOUNDS, keep);
+  if (part == 0 && layer == 0 && threadIdx.x == 0) set_status(status, pair, ok ? TC_OK : TC_ERR_BOUNDS, keep);
   if (!ok) return;
   const uint4* from = reinterpret_cast<const uint4*>(pool + ((int64_t)layer * pages + a) * page_bytes);
   uint4* to = reinterpret_cast<uint4*>(pool + ((int64_t)layer * pages + b) * page_bytes);
-  const int n = (int)(page_bytes / 16), at = blockIdx.x * kBlock * kCopyUnroll + threadIdx.x;
+  const int n = (int)(page_bytes / 16), at = part * kBlock * kCopyUnroll + threadIdx.x;
   uint4 v[kCopyUnroll];
 #pragma unroll
   for (int u = 0; u < kCopyUnroll; ++u)
@@ -322,11 +323,12 @@ struct CompactParams {
   int32_t* lens_out;
   int32_t* status;
   int32_t keep;
+  uint32_t blocks;    // of a sequence
 };
 
 constexpr int kMoveUnroll = 4;
 
-// Grid (columns / kBlock, sequence).  A column is one 16-byte word of one head
+// Grid: for each sequence, blocks of kBlock columns.  A column is one 16-byte word of one head
 // of one layer's keys or values; its thread moves that word of every slot of
 // the branch, in ascending order.  Indices ascend strictly, so path[i] >= i:
 // the slot that move i writes is the source of no later move, and an earlier
@@ -337,7 +339,7 @@ constexpr int kMoveUnroll = 4;
 // registers, fewer blocks).
 __global__ void __launch_bounds__(kBlock) compact_kernel(const CompactParams p) {
   __shared__ int64_t s_src[TC_PATH_MAX], s_dst[TC_PATH_MAX];  // slot offsets in rows of one head
-  const int b = blockIdx.y, tid = threadIdx.x;
+  const int b = blockIdx.x / p.blocks, part = blockIdx.x % p.blocks, tid = threadIdx.x;
   const int ctx = __ldg(p.tok.ctx + b), n = __ldg(p.n_path + b);
   bool ok = ctx >= 0 && n >= 0 && n <= p.path_width;
   if (ok && tid < n) {
@@ -354,12 +356,12 @@ __global__ void __launch_bounds__(kBlock) compact_kernel(const CompactParams p) 
     }
   }
   ok = __syncthreads_and(ok);
-  if (blockIdx.x == 0 && tid == 0) {
+  if (part == 0 && tid == 0) {
     p.lens_out[b] = ok ? ctx + n : ctx;
     set_status(p.status, b, ok ? TC_OK : TC_ERR_BOUNDS, p.keep);
   }
   if (!ok) return;
-  const int64_t col = (int64_t)blockIdx.x * kBlock + tid;
+  const int64_t col = (int64_t)part * kBlock + tid;
   const int word = (int)(col % p.row_words);
   const int64_t head = col / p.row_words;  // layer * 2 * kv_heads + (keys or values) * kv_heads + head
   if (head >= (int64_t)p.layers * 2 * p.kv_heads) return;
@@ -469,17 +471,19 @@ extern "C" tc_status tc_kv_copy_pages(const tc_kv_t* kv, const int32_t* src, con
   if (rc != TC_OK) return rc;
   if (n < 0 || (n > 0 && (!src || !dst || !status)))
     return kv_fail(TC_ERR_INVALID_ARG, "tc_kv_copy_pages: invalid arguments");
-  if (n > 65535 || kv->layers > 65535)
-    return kv_fail(TC_ERR_CAPACITY, "tc_kv_copy_pages: more than 65535 pairs or layers");
+  if (n > TC_KV_MAX_BATCH || kv->layers > 65535)
+    return kv_fail(TC_ERR_CAPACITY, "tc_kv_copy_pages: more than 65536 pairs or 65535 layers");
   if (n == 0) return TC_OK;
-  KvDevice dev(kv->device);
-  if (!dev.ok) return kv_fail(TC_ERR_CUDA, "tc_kv_copy_pages: cannot use the cache's device");
   const int64_t page_bytes = (int64_t)4 * kv->kv_heads * kv->page_size * kv->head_dim;
   const int64_t per_block = (int64_t)kBlock * kCopyUnroll * 16;
-  const dim3 grid((unsigned)((page_bytes + per_block - 1) / per_block), (unsigned)n, (unsigned)kv->layers);
+  const int64_t blocks = (page_bytes + per_block - 1) / per_block;
+  if (blocks * n > INT_MAX) return kv_fail(TC_ERR_CAPACITY, "tc_kv_copy_pages: pairs x page size is too large");
+  KvDevice dev(kv->device);
+  if (!dev.ok) return kv_fail(TC_ERR_CUDA, "tc_kv_copy_pages: cannot use the cache's device");
+  const dim3 grid((unsigned)(blocks * n), (unsigned)kv->layers);
   copy_pages_kernel<<<grid, kBlock, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint8_t*>(kv->pool), kv->pages,
                                                                            page_bytes, src, dst, status,
-                                                                           kv->keep_status != 0);
+                                                                           kv->keep_status != 0, (unsigned)blocks);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_copy_pages");
 }
@@ -496,7 +500,10 @@ extern "C" tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens,
     return kv_fail(TC_ERR_CAPACITY, "tc_kv_compact: path_width is more than " + std::to_string(TC_PATH_MAX));
   if (lens_out < tokens->ctx_lens + tokens->batch && tokens->ctx_lens < lens_out + tokens->batch)
     return kv_fail(TC_ERR_INVALID_ARG, "tc_kv_compact: lens_out overlaps ctx_lens");
-  if (tokens->batch > 65535) return kv_fail(TC_ERR_CAPACITY, "tc_kv_compact: more than 65535 sequences");
+  const int64_t cols = (int64_t)kv->layers * 2 * kv->kv_heads * (kv->head_dim / 8);
+  const int64_t blocks = (cols + kBlock - 1) / kBlock;
+  if (blocks * tokens->batch > INT_MAX)
+    return kv_fail(TC_ERR_CAPACITY, "tc_kv_compact: sequences x layers x kv_heads is too large");
   KvDevice dev(kv->device);
   if (!dev.ok) return kv_fail(TC_ERR_CUDA, "tc_kv_compact: cannot use the cache's device");
   CompactParams p;
@@ -515,9 +522,8 @@ extern "C" tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens,
   p.lens_out = lens_out;
   p.status = status;
   p.keep = v.keep;
-  const int64_t cols = (int64_t)kv->layers * 2 * kv->kv_heads * p.row_words;
-  const dim3 grid((unsigned)((cols + kBlock - 1) / kBlock), (unsigned)tokens->batch);
-  compact_kernel<<<grid, kBlock, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  p.blocks = (uint32_t)blocks;
+  compact_kernel<<<(unsigned)(blocks * tokens->batch), kBlock, 0, static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_compact");
 }
