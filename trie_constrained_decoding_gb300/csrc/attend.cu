@@ -1523,5 +1523,5 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
     e = kv->head_dim == 128 ? launch<Bf16, 128>(p, map_kv, map_q, s) : launch<Bf16, 64>(p, map_kv, map_q, s);
   else
     e = kv->head_dim == 128 ? launch<F16, 128>(p, map_kv, map_q, s) : launch<F16, 64>(p, map_kv, map_q, s);
-  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_attend");
+  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_attend: ");
 }

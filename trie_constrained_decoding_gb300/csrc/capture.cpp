@@ -11,13 +11,10 @@
 
 namespace {
 
+// (`what` ends in ": ")
 tc_status fail(const char* what, cudaError_t e) {
   cudaGetLastError();
-  try {
-    tcd::set_error_message(std::string(what) + ": " + cudaGetErrorString(e));
-  } catch (...) {
-  }
-  return TC_ERR_CUDA;
+  return tcd::fail_with(TC_ERR_CUDA, what, cudaGetErrorString(e));
 }
 
 // Called by the graph's destruction, on any thread; no CUDA call is allowed.
@@ -43,7 +40,7 @@ extern "C" tc_status tc_capture_id(void* stream, uint64_t* id) {
     cudaGetLastError();
     return TC_OK;
   }
-  if (e != cudaSuccess) return fail("tc_capture_id", e);
+  if (e != cudaSuccess) return fail("tc_capture_id: ", e);
   if (st != cudaStreamCaptureStatusNone) *id = n;
   return TC_OK;
 }
@@ -55,7 +52,7 @@ extern "C" tc_status tc_capture_watch(void* stream, int32_t** gone) {
   unsigned long long n = 0;
   cudaGraph_t graph = nullptr;
   cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &st, &n, &graph);
-  if (e != cudaSuccess) return fail("tc_capture_watch", e);
+  if (e != cudaSuccess) return fail("tc_capture_watch: ", e);
   if (st != cudaStreamCaptureStatusActive || !graph) return TC_ERR_INVALID_ARG;
   auto* word = new (std::nothrow) std::atomic<int32_t>(0);
   if (!word) return TC_ERR_OOM;
@@ -63,12 +60,12 @@ extern "C" tc_status tc_capture_watch(void* stream, int32_t** gone) {
   e = cudaUserObjectCreate(&obj, word, mark, 1, cudaUserObjectNoDestructorSync);
   if (e != cudaSuccess) {
     delete word;
-    return fail("tc_capture_watch", e);
+    return fail("tc_capture_watch: ", e);
   }
   e = cudaGraphRetainUserObject(graph, obj, 1, cudaGraphUserObjectMove);
   if (e != cudaSuccess) {  // (the word is marked when the release is done, and stays)
     cudaUserObjectRelease(obj, 1);
-    return fail("tc_capture_watch", e);
+    return fail("tc_capture_watch: ", e);
   }
   *gone = reinterpret_cast<int32_t*>(word);
   return TC_OK;
@@ -82,7 +79,7 @@ extern "C" tc_status tc_capture_mode(int32_t* mode) {
                                                  cudaStreamCaptureModeRelaxed};
   cudaStreamCaptureMode m = modes[*mode];
   const cudaError_t e = cudaThreadExchangeStreamCaptureMode(&m);
-  if (e != cudaSuccess) return fail("tc_capture_mode", e);
+  if (e != cudaSuccess) return fail("tc_capture_mode: ", e);
   *mode = m == modes[0] ? 0 : m == modes[1] ? 1 : 2;
   return TC_OK;
 }
@@ -92,5 +89,5 @@ extern "C" tc_status tc_clear_now(void* ptr, int64_t bytes, void* stream) {
   Relaxed relaxed;
   cudaError_t e = cudaMemsetAsync(ptr, 0, (size_t)bytes, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? TC_OK : fail("tc_clear_now", e);
+  return e == cudaSuccess ? TC_OK : fail("tc_clear_now: ", e);
 }

@@ -8,26 +8,26 @@
 
 namespace tcd {
 
+static_assert(TC_KV_MAX_BATCH == 65536 && TC_PATH_MAX == 256, "the messages name these");
+
 tc_status kv_check(const char* who, const tc_kv_t* kv) {
-  const std::string w(who);
-  if (!kv) return kv_fail(TC_ERR_INVALID_ARG, w + ": the cache is NULL");
+  if (!kv) return kv_fail(TC_ERR_INVALID_ARG, who, ": the cache is NULL");
   if (!kv->pool || kv_misaligned(kv->pool, 16) || kv->layers < 1 || kv->pages < 1 || kv->kv_heads < 1 ||
       kv->device < 0)
-    return kv_fail(TC_ERR_INVALID_ARG, w + ": the cache wants a 16-byte aligned pool and sizes >= 1");
+    return kv_fail(TC_ERR_INVALID_ARG, who, ": the cache wants a 16-byte aligned pool and sizes >= 1");
   if ((kv->dtype != TC_DT_BF16 && kv->dtype != TC_DT_F16) || (kv->head_dim != 64 && kv->head_dim != 128) ||
       (kv->page_size != 16 && kv->page_size != 32 && kv->page_size != 64 && kv->page_size != 128))
     return kv_fail(TC_ERR_UNSUPPORTED,
-                   w + ": the cache wants bf16 or f16, head_dim 64 or 128, page_size 16, 32, 64 or 128");
-  if (kv->kv_heads > 65535) return kv_fail(TC_ERR_CAPACITY, w + ": more than 65535 kv_heads");
+                   who, ": the cache wants bf16 or f16, head_dim 64 or 128, page_size 16, 32, 64 or 128");
+  if (kv->kv_heads > 65535) return kv_fail(TC_ERR_CAPACITY, who, ": more than 65535 kv_heads");
   return TC_OK;
 }
 
 tc_status kv_check_tokens(const char* who, const tc_tokens_t* t, bool rows) {
-  const std::string w(who);
   if (!t || t->batch < 1 || t->n_tokens < 0 || !t->ctx_lens || (rows && !t->cu_tokens))
-    return kv_fail(TC_ERR_INVALID_ARG, w + ": the tokens want batch >= 1, cu_tokens and ctx_lens");
+    return kv_fail(TC_ERR_INVALID_ARG, who, ": the tokens want batch >= 1, cu_tokens and ctx_lens");
   if (t->batch > TC_KV_MAX_BATCH)
-    return kv_fail(TC_ERR_CAPACITY, w + ": more than " + std::to_string(TC_KV_MAX_BATCH) + " sequences");
+    return kv_fail(TC_ERR_CAPACITY, who, ": more than 65536 sequences");
   return TC_OK;
 }
 
@@ -445,7 +445,7 @@ extern "C" tc_status tc_kv_append(const tc_kv_t* kv, int32_t layer, const tc_tok
     e = kv->head_dim == 128 ? launch_append<Bf16, 128>(p, warps, s) : launch_append<Bf16, 64>(p, warps, s);
   else
     e = kv->head_dim == 128 ? launch_append<F16, 128>(p, warps, s) : launch_append<F16, 64>(p, warps, s);
-  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_append");
+  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_append: ");
 }
 
 extern "C" tc_status tc_tree_masks(const tc_tokens_t* tokens, const int32_t* parents, int32_t words, int64_t* masks,
@@ -462,7 +462,7 @@ extern "C" tc_status tc_tree_masks(const tc_tokens_t* tokens, const int32_t* par
   if (words == 3) tree_mask_kernel<3><<<grid, kBlock, 0, s>>>(t, parents, masks, positions, status);
   if (words == 4) tree_mask_kernel<4><<<grid, kBlock, 0, s>>>(t, parents, masks, positions, status);
   const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_tree_masks");
+  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_tree_masks: ");
 }
 
 extern "C" tc_status tc_kv_copy_pages(const tc_kv_t* kv, const int32_t* src, const int32_t* dst, int32_t n,
@@ -485,7 +485,7 @@ extern "C" tc_status tc_kv_copy_pages(const tc_kv_t* kv, const int32_t* src, con
                                                                            page_bytes, src, dst, status,
                                                                            kv->keep_status != 0, (unsigned)blocks);
   const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_copy_pages");
+  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_copy_pages: ");
 }
 
 extern "C" tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens, const int32_t* path,
@@ -497,7 +497,7 @@ extern "C" tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens,
   if (!path || !n_path || !lens_out || !status || !tokens->page_table || tokens->table_width < 1 || path_width < 1)
     return kv_fail(TC_ERR_INVALID_ARG, "tc_kv_compact: invalid arguments");
   if (path_width > TC_PATH_MAX)
-    return kv_fail(TC_ERR_CAPACITY, "tc_kv_compact: path_width is more than " + std::to_string(TC_PATH_MAX));
+    return kv_fail(TC_ERR_CAPACITY, "tc_kv_compact: path_width is more than 256");
   if (lens_out < tokens->ctx_lens + tokens->batch && tokens->ctx_lens < lens_out + tokens->batch)
     return kv_fail(TC_ERR_INVALID_ARG, "tc_kv_compact: lens_out overlaps ctx_lens");
   const int64_t cols = (int64_t)kv->layers * 2 * kv->kv_heads * (kv->head_dim / 8);
@@ -525,5 +525,5 @@ extern "C" tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens,
   p.blocks = (uint32_t)blocks;
   compact_kernel<<<(unsigned)(blocks * tokens->batch), kBlock, 0, static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_compact");
+  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_kv_compact: ");
 }

@@ -95,15 +95,14 @@ __device__ __forceinline__ bool seq_span(const TokensView& t, int page_size, int
 
 // ------------------------------------------------------------ host helpers
 
-inline tc_status kv_fail(tc_status code, const std::string& msg) {
-  set_error_message(msg);
-  return code;
+inline tc_status kv_fail(tc_status code, const char* who, const char* what = "") noexcept {
+  return fail_with(code, who, what);
 }
 
-inline tc_status kv_cuda_fail(cudaError_t e, const char* what) {
-  set_error_message(std::string(what) + ": " + cudaGetErrorString(e));
+// (`what` ends in ": ")
+inline tc_status kv_cuda_fail(cudaError_t e, const char* what) noexcept {
   cudaGetLastError();
-  return e == cudaErrorMemoryAllocation ? TC_ERR_OOM : TC_ERR_CUDA;
+  return fail_with(e == cudaErrorMemoryAllocation ? TC_ERR_OOM : TC_ERR_CUDA, what, cudaGetErrorString(e));
 }
 
 inline bool kv_misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }

@@ -58,10 +58,7 @@ struct tc_pages {
 
 namespace {
 
-tc_status fail(tc_status code, const char* msg) {
-  tcd::set_error_message(msg);
-  return code;
-}
+tc_status fail(tc_status code, const char* msg) { return tcd::fail_with(code, msg); }
 
 // Runs `f` with every C++ exception turned into a status.
 template <typename F>

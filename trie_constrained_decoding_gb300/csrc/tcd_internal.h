@@ -53,4 +53,15 @@ std::vector<int32_t> build_walk_image(const tc_trie& t, const WalkLayout& L);
 
 void set_error_message(const std::string& msg);
 
+// The message of a failed call, and its code: also where the memory for the
+// message cannot be had (it is empty then), as no exception may leave a C entry.
+inline tc_status fail_with(tc_status code, const char* who, const char* what = "") noexcept {
+  try {
+    set_error_message(std::string(who) + what);
+  } catch (...) {
+    set_error_message(std::string());  // (no memory is needed for this)
+  }
+  return code;
+}
+
 }  // namespace tcd
