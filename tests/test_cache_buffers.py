@@ -21,7 +21,7 @@ def world(tcd, monkeypatch):
         ref._obj.contents = word
         return 0
 
-    def empty(n, dtype, device, stream):
+    def empty(n, dtype, device, stream, zero=False):
         assert not captures.get(stream), "memory of a stream that is being captured would be the graph's own"
         made.append(stream)
         return torch.zeros(n, dtype=dtype)
@@ -32,7 +32,6 @@ def world(tcd, monkeypatch):
     monkeypatch.setattr(tcd, "_clear_now", lambda p, n, s: 0)
     monkeypatch.setattr(tcd, "_capture_mode", lambda ref: 0)
     monkeypatch.setattr(tcd, "_empty", empty)
-    monkeypatch.setattr(tcd, "_zeros", empty)
     monkeypatch.setattr(tcd, "_stream_aside", lambda device: 900)
     monkeypatch.setattr(tcd, "_held", [])
 

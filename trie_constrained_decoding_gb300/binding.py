@@ -407,22 +407,15 @@ def _rows(t, dtype, device, what: str, heads: int, head_dim: int):
     return t.data_ptr(), stride[0] if shape[0] > 1 else heads * head_dim
 
 
-def _empty(n: int, dtype, device, stream: int):
+def _empty(n: int, dtype, device, stream: int, zero: bool = False):
     """A buffer that belongs to the stream its kernels run on: memory of another stream may still be in use there."""
     import torch
+    make = torch.zeros if zero else torch.empty
     if stream == torch.cuda.current_stream(device).cuda_stream:
-        return torch.empty(n, dtype=dtype, device=device)
+        return make(n, dtype=dtype, device=device)
     own = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     with torch.cuda.stream(own):
-        return torch.empty(n, dtype=dtype, device=device)
-
-
-def _zeros(n: int, dtype, device, stream: int):
-    import torch
-    t = _empty(n, dtype, device, stream)
-    own = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    with torch.cuda.stream(own):
-        return t.zero_()
+        return make(n, dtype=dtype, device=device)
 
 
 class _Codes:
@@ -548,7 +541,8 @@ class KvCache:
                     self._capture_buffers(self._capture.value, stream)
         own = self._own.get(stream)
         if own is None:
-            own = self._own[stream] = _Own(_Codes(_zeros(2 * KV_MAX_BATCH, self._i32, self.device, stream)), stream)
+            codes = _empty(2 * KV_MAX_BATCH, self._i32, self.device, stream, zero=True)
+            own = self._own[stream] = _Own(_Codes(codes), stream)
         return own
 
     def _capture_buffers(self, capture: int, stream: int):
@@ -566,17 +560,18 @@ class KvCache:
         _hold(own)
         return own
 
-    def _codes(self, status, n: int, stream: int, pairs: int = 0):
+    def _codes(self, status, n: int, stream: int, pairs: int = 0, own=None):
         """Where a call's codes go, behind the description of the cache that says how."""
         if status is not None:
             return self._kvp, self._ints(status, (n,), "status")
-        own = self._buffers(stream).codes
-        own.used[pairs] = max(own.used[pairs], min(n, KV_MAX_BATCH))
-        return self._kvp_keep, own.at + 4 * KV_MAX_BATCH * pairs
+        codes = (own or self._buffers(stream)).codes
+        if n > codes.used[pairs]:
+            codes.used[pairs] = min(n, KV_MAX_BATCH)
+        return self._kvp_keep, codes.at + 4 * KV_MAX_BATCH * pairs
 
-    def _workspace(self, workspace, stream: int):
+    def _workspace(self, workspace, stream: int, own=None):
         if workspace is None:
-            own = self._buffers(stream)
+            own = own or self._buffers(stream)
             if own.place is None:
                 if own.stream == stream:
                     own.workspace = _empty(self.workspace_bytes, self._u8, self.device, stream)
@@ -651,8 +646,9 @@ class KvCache:
                     words, *_rows(out, dtype, device, "out", hq, d), sums, *self._wait_test)
         t = self._tokens(n, cu_tokens, ctx_lens, page_table)
         s = self._stream(stream)
-        kv, codes = self._codes(status, t.batch, s)
-        _check(_attend(kv, layer, t, a, *self._workspace(workspace, s), codes, s), "tc_attend")
+        own = None if workspace is not None else self._buffers(s)
+        kv, codes = self._codes(status, t.batch, s, own=own)
+        _check(_attend(kv, layer, t, a, *self._workspace(workspace, s, own), codes, s), "tc_attend")
 
     def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
         """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)
