@@ -71,8 +71,10 @@ typedef struct tc_kv_t {
  *
  *  batch        sequences (1 .. TC_KV_MAX_BATCH).
  *  n_tokens     rows of the packed token arrays (>= 0; 0 only does the status).
- *  cu_tokens    (device) int32[batch + 1]: sequence b's tokens are rows
- *               [cu_tokens[b], cu_tokens[b + 1]); none is allowed.
+ *  cu_tokens    (device) int32[batch + 1], ascending: sequence b's tokens are
+ *               rows [cu_tokens[b], cu_tokens[b + 1]); none is allowed.  (Where
+ *               it descends, that sequence gets TC_ERR_BOUNDS; a row that other
+ *               sequences then have in common belongs to any one of them.)
  *  ctx_lens     (device) int32[batch]: tokens of sequence b already cached.
  *               Its new token t lies in slot ctx_lens[b] + t.
  *  page_table   (device) int32[batch][table_width] page ids; entries past a
@@ -156,7 +158,9 @@ tc_status tc_kv_append(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* toke
  * A slot that a token does not see contributes nothing, whatever it holds
  * (infinities and NaN included).  A token that sees nothing gets zeros.
  * Scores, maxima, sums and outputs are held in 32 bits; the weights of one
- * tile are rounded to the cache's type for the tensor cores.
+ * tile are rounded to the cache's type for the tensor cores (f16:
+ * as far as 2^-21 of the row's largest weight, smaller ones to multiples of 2^-31
+ * of it).
  *
  *  q           (device) [n_tokens][q_heads][head_dim] of the cache's type,
  *              rows q_stride elements apart (a multiple of 8), 16-byte aligned.
@@ -168,8 +172,9 @@ tc_status tc_kv_append(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* toke
  *  out         (device) like q, rows out_stride elements apart.
  *  lse         (device) float[n_tokens][q_heads] or NULL: the logarithm of the
  *              sum of exp(scale * q . k) over the slots seen (-inf for none).
- *  workspace   (device) tc_attend_workspace bytes, 16-byte aligned; its content
- *              before and after the call means nothing.
+ *  workspace   (device) tc_attend_workspace bytes (about 40 MB: two partial
+ *              results per SM), 16-byte aligned; its content before and after the
+ *              call means nothing.
  *  status      (device) int32[batch]: TC_OK, TC_ERR_BOUNDS, or
  *              TC_ERR_DEVICE_TIMEOUT for every sequence if a bounded wait of
  *              the kernel gave up (the outputs are then invalid).
@@ -255,8 +260,11 @@ tc_status tc_kv_compact(const tc_kv_t* kv, const tc_tokens_t* tokens, const int3
  *
  * Calls that need pages fail with TC_ERR_CAPACITY when there are not enough
  * and then change nothing.  Copies that a call asks for are appended to
- * src / dst (host, room for `cap` pairs; a call never asks for more than one);
- * run them with tc_kv_copy_pages before the next write to those sequences.
+ * src / dst (host; a call never asks for more than one pair).  Run them with
+ * tc_kv_copy_pages before anything is written to any sequence (another holder of
+ * the source page may be its only one by now, and write to it without a copy) and
+ * before a sequence is closed or trimmed (a source page may become free, and be
+ * handed out again as another copy's target).
  * One host thread at a time per object.
  */
 typedef struct tc_pages tc_pages;
@@ -274,7 +282,8 @@ tc_status tc_pages_close(tc_pages* p, int32_t seq);
  * Make room to write slots [from, upto) of a sequence: pages are added, and if
  * the page of slot `from` is shared and holds earlier slots, it is replaced by
  * a copy (one pair, *n_copies = 1, else 0); shared pages further on are
- * replaced by fresh ones without a copy.
+ * replaced by fresh ones without a copy: slots from `from` on count as given up,
+ * what a shared page held there, behind `upto` as well, is the sequence's no more.
  */
 tc_status tc_pages_reserve(tc_pages* p, int32_t seq, int64_t from, int64_t upto, int32_t* src, int32_t* dst,
                            int32_t* n_copies);

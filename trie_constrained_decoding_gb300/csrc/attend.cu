@@ -16,7 +16,7 @@
 // a cut that falls into an item's beginning or end splits nothing.  (Against
 // tiles alone: a prompt of 8192 416 us, was 488; 16 short prompts 45.5, was 53; a
 // decode step of 64 sequences 180, was 192.  With three units before and none
-// after a prompt of 2048 takes 156 us instead of 148, with two and two 151.)
+// after four prompts of 2048 take 156 us instead of 148, with two and two 151.)
 // Every CTA works its part out from the lengths on the device, so the launch
 // depends on none of them and can be captured.  An item that a cut falls into leaves
 // unnormalised partial results in 32 bits, at most two per CTA, which a second
@@ -78,10 +78,11 @@
 // rows that see them.
 //
 // What it measured (bf16, 32 query and 8 key-value heads of 128, pages of 64):
-// a prompt of 8192 tokens in 436 us back to back, 1.26 PFLOP/s, 65 % of what the
+// a prompt of 8192 tokens in 439 us back to back, 1.25 PFLOP/s, 65 % of what the
 // library's matrix product reaches (417 us in short runs, 68 %); 16 prompts of 5 to
 // 261 tokens in 45 us; a decode step of 64 sequences with 97 to 8011 slots in 179 us,
-// 6.1 TB/s, 90 % of a copy's rate; one token over 1500 slots in 16.5 us.  Bound: long
+// 6.1 TB/s, 90 % of a copy's rate; one token over 1500 slots in 16.3 us; one token of
+// 253 sequences with 20 to 81 slots and 16 heads of their own in 166 us.  Bound: long
 // prompts by the chain of waits and exponentials that a softmax group goes through
 // in a step (0.96 us for both groups' 64 slots, of which the products take 0.53);
 // decode by bytes; small calls and many short items by latencies one after another
@@ -370,8 +371,9 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 // (Divisions here are of 32 bits: the code of a 64-bit one is long, and a small
 // call is bound by the fetch of its instructions.)
 
-// sum over i < n of floor((a i + b) / m), in O(log m) steps (Euclid's scheme);
-// a n + b fits 32 bits.
+// sum over i < n of floor((a i + b) / m), in O(log m) steps like Euclid's algorithm
+// (Graham, Knuth and Patashnik, "Concrete Mathematics", section 3.5); a n + b fits
+// 32 bits.
 __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t ans = 0;
   while (n > 0) {
@@ -1212,8 +1214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
           if (live && g.part < 0) {
             // (64 bytes of a row: whole sectors, and no shared memory is held up
-            // for the next item.  16 bytes a store: a prompt of 2048 152 us against
-            // 148, 16 short ones 47 against 45.5)
+            // for the next item.  16 bytes a store: four prompts of 2048
+            // 152 us against 148, 16 short ones 47 against 45.5)
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = T::pack(v[2 * j] * norm, v[2 * j + 1] * norm);
