@@ -1,0 +1,64 @@
+"""tc_linear's checks of its arguments (CPU: a refused call touches no device)."""
+import ctypes
+
+import pytest
+
+INVALID, CAPACITY, UNSUPPORTED = 1, 10, 11
+AT = 1 << 20   # (an address that is never read)
+
+
+def layer(tcd, **kw):
+    v = dict(device=0, dtype=0, in_features=64, out_features=32, weight=AT, weight_stride=64, gate=None, gate_stride=0,
+             bias=None, gate_bias=None, act=0)
+    v.update(kw)
+    return tcd._LinearWeights(*[v[n] for n, _ in tcd._LinearWeights._fields_])
+
+
+def call(tcd, **kw):
+    v = dict(n_tokens=4, x=AT, x_stride=64, residual=None, residual_stride=0, out=AT, out_stride=32, wait_polls=0,
+             withhold=0)
+    v.update(kw)
+    return tcd._LinearCall(*[v[n] for n, _ in tcd._LinearCall._fields_])
+
+
+WEIGHTS = [
+    (dict(device=-1), INVALID), (dict(device=64), INVALID), (dict(in_features=0), INVALID),
+    (dict(out_features=0), INVALID), (dict(act=5), INVALID), (dict(act=-1), INVALID), (dict(dtype=2), UNSUPPORTED),
+    (dict(in_features=(1 << 20) + 1, weight_stride=1 << 21), CAPACITY), (dict(out_features=(1 << 20) + 1), CAPACITY),
+    (dict(weight=None), INVALID), (dict(weight=AT + 8), INVALID), (dict(weight_stride=63), INVALID),
+    (dict(weight_stride=56), INVALID), (dict(gate=AT + 2, gate_stride=64), INVALID), (dict(gate=AT), INVALID),
+    (dict(gate=AT, gate_stride=68), INVALID), (dict(gate_bias=AT), INVALID), (dict(bias=AT + 1), INVALID),
+    (dict(gate=AT, gate_stride=64, gate_bias=AT + 1), INVALID),
+]
+CALLS = [
+    (dict(n_tokens=-1), INVALID), (dict(n_tokens=(1 << 24) + 1), CAPACITY), (dict(x=None), INVALID),
+    (dict(x=AT + 2), INVALID), (dict(x_stride=60), INVALID), (dict(x_stride=56), INVALID), (dict(out=None), INVALID),
+    (dict(out=AT + 1), INVALID), (dict(out_stride=31), INVALID), (dict(residual=AT, residual_stride=31), INVALID),
+    (dict(residual=AT + 1, residual_stride=32), INVALID),
+]
+
+
+@pytest.mark.parametrize("change,code", WEIGHTS, ids=str)
+def test_weights(tcd, change, code):
+    assert tcd._linear(layer(tcd, **change), call(tcd), AT, None) == code
+
+
+@pytest.mark.parametrize("change,code", CALLS, ids=str)
+def test_call(tcd, change, code):
+    assert tcd._linear(layer(tcd), call(tcd, **change), AT, None) == code
+
+
+def test_missing(tcd):
+    assert tcd._linear(None, call(tcd), AT, None) == INVALID
+    assert tcd._linear(layer(tcd), None, AT, None) == INVALID
+    assert tcd._linear(layer(tcd), call(tcd), None, None) == INVALID
+
+
+def test_no_tokens_is_no_launch(tcd):
+    """(x and out may be NULL then.)"""
+    assert tcd._linear(layer(tcd), call(tcd, n_tokens=0, x=None, out=None), AT, None) == 0
+
+
+def test_structures_match_the_header(tcd):
+    """Sizes of the C structures on a 64-bit host."""
+    assert ctypes.sizeof(tcd._LinearWeights) == 72 and ctypes.sizeof(tcd._LinearCall) == 72

@@ -1,4 +1,4 @@
-"""Thin ctypes binding over ``libtcd.so`` (the C ABI of ``include/tcd.h``).
+"""Thin ctypes binding over ``libtcd.so`` (the C ABI of ``include/tcd*.h``).
 
 Argument marshalling only: every step of the decode path runs in the CUDA
 kernels behind the C ABI.  Device buffers are passed as torch CUDA tensors
@@ -720,6 +720,136 @@ def tree_masks(parents, cu_tokens, ctx_lens, masks, positions=None, status=None,
                            None if positions is None else _int_tensor(positions, (n,), dev, "positions"),
                            _int_tensor(status, (batch,), dev, "status"), s), "tc_tree_masks")
     return status
+
+
+# ------------------------------------------------- projections (include/tcd_linear.h)
+
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+
+
+class _LinearWeights(ctypes.Structure):
+    _fields_ = [("device", ctypes.c_int32), ("dtype", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32), ("weight", _vp), ("weight_stride", ctypes.c_int64), ("gate", _vp),
+                ("gate_stride", ctypes.c_int64), ("bias", _vp), ("gate_bias", _vp), ("act", ctypes.c_int32)]
+
+
+class _LinearCall(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("x", _vp), ("x_stride", ctypes.c_int64), ("residual", _vp),
+                ("residual_stride", ctypes.c_int64), ("out", _vp), ("out_stride", ctypes.c_int64),
+                ("wait_polls", ctypes.c_int64), ("withhold", ctypes.c_int32)]
+
+
+_linear = _decl("tc_linear", ctypes.c_int, [ctypes.POINTER(_LinearWeights), ctypes.POINTER(_LinearCall), _vp, _vp])
+
+_words = {}    # per device: error words that are never freed (a captured call keeps its own), and how many are taken
+_words_lock = threading.Lock()
+_WORDS = 4096
+
+
+def _error_word(device):
+    """An int32 of device memory, 0, for one object's errors."""
+    import torch
+    with _words_lock:
+        words, taken = _words.get(device, (None, _WORDS))
+        if taken == _WORDS:
+            words, taken = _empty_aside(_WORDS, torch.int32, device, _stream_aside(device), clear=True), 0
+        _words[device] = words, taken + 1
+    return words[taken:taken + 1]
+
+
+class Linear:
+    """A projection y = act(x W^T + bias) + residual, or with a gate
+    y = act(x G^T + gate_bias) * (x W^T + bias) + residual (the first half of a
+    gated feed-forward block), over torch CUDA tensors, bf16 or f16.
+
+    weight and gate [out_features, in_features], rows contiguous and a multiple
+    of 8 elements apart; bias and gate_bias [out_features].  The object holds no
+    state but the weights.  Errors found on the device are gathered in a word of
+    the object until raise_on_error(), or written to a call's ``status`` (one
+    int32, set to TC_OK by the caller, written only on an error).  Calls need no
+    workspace and may run at the same time, captured or not.
+    """
+
+    def __init__(self, weight, bias=None, gate=None, gate_bias=None, act: int = ACT_NONE):
+        import torch
+        types = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+        if not (weight.is_cuda and weight.dtype in types and weight.dim() == 2 and weight.numel() > 0):
+            raise ValueError("weight must be a bfloat16 or float16 CUDA tensor [out_features, in_features]")
+        self.dtype, self.device = weight.dtype, weight.device
+        self.out_features, self.in_features = weight.shape
+        if gate is None and gate_bias is not None:
+            raise ValueError("gate_bias without a gate")
+        self._keep = (weight, bias, gate, gate_bias)
+        wide = (self.in_features + 7) // 8 * 8   # (of a single row: torch keeps whatever stride it was)
+        self._x_stride = wide
+
+        def rows(t, what):
+            if t.shape != weight.shape or t.dtype is not self.dtype or t.device != self.device or \
+                    (self.in_features > 1 and t.stride(1) != 1):
+                raise ValueError(f"{what} must hold {self.out_features} rows of {self.in_features} contiguous "
+                                 f"{self.dtype} elements on {self.device}")
+            return t.data_ptr(), t.stride(0) if self.out_features > 1 else wide
+
+        def line(t, what):
+            if t is None:
+                return None
+            if t.shape != (self.out_features,) or t.dtype is not self.dtype or t.device != self.device or \
+                    not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous {self.dtype} tensor of {self.out_features} elements")
+            return t.data_ptr()
+
+        self._layer = _LinearWeights(self.device.index, types[self.dtype], self.in_features, self.out_features,
+                                     *rows(weight, "weight"), *((None, 0) if gate is None else rows(gate, "gate")),
+                                     line(bias, "bias"), line(gate_bias, "gate_bias"), act)
+        self._layer_ref = ctypes.byref(self._layer)
+        self._i32 = torch.int32
+        self._word = _error_word(self.device)
+        self._word_at = self._word.data_ptr()
+        index, raw = self.device.index, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(index).cuda_stream)
+        self._wait_test = (0, 0)
+
+    def _rows(self, t, n: int, features: int, what: str):
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != n or shape[1] != features or t.dtype is not self.dtype or \
+                t.device != self.device:
+            raise ValueError(f"{what} must hold {n} rows of {features} {self.dtype} elements on {self.device}")
+        stride, step = t.stride()
+        if step != 1 and features > 1:
+            raise ValueError(f"{what} must have contiguous rows")
+        return t.data_ptr(), stride if n > 1 else features
+
+    def apply(self, x, out, residual=None, status=None, stream=None):
+        """tc_linear: x [n, in_features], out and residual [n, out_features] (rows may be slices of wider ones;
+        residual may be out itself)."""
+        n = x.shape[0]
+        at, stride = self._rows(x, n, self.in_features, "x")
+        call = _LinearCall(n, at, stride if n > 1 else self._x_stride,
+                           *((None, 0) if residual is None else self._rows(residual, n, self.out_features, "residual")),
+                           *self._rows(out, n, self.out_features, "out"), *self._wait_test)
+        if status is None:
+            word = self._word_at
+        else:
+            if status.dtype is not self._i32 or status.numel() != 1 or status.device != self.device:
+                raise ValueError(f"status must be an int32 tensor of one element on {self.device}")
+            word = status.data_ptr()
+        s = self._current() if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+        _check(_linear(self._layer_ref, call, word, s), "tc_linear")
+
+    def wait_test(self, withhold: bool, wait_polls: int = 0):
+        """Make the kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0) restores."""
+        self._wait_test = (int(wait_polls), int(bool(withhold)))
+
+    def raise_on_error(self):
+        """Wait for the device, and if a call made without `status` since the last error raised has failed, clear
+        the error and raise it."""
+        import torch
+        torch.cuda.synchronize(self.device)
+        code = int(self._word.item())
+        if code != TC_OK:
+            self._word.zero_()
+            torch.cuda.synchronize(self.device)
+            raise TcError(code, "projection")
 
 
 class PagePool:
