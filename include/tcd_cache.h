@@ -203,6 +203,41 @@ tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens,
 tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes);
 
 /*
+ * tc_attend_shared - tc_attend for sequences that share the beginning of their
+ * contexts (tc_pages_fork): a shared prefix is read once for all tokens of its
+ * sequences, and the result of each token is joined with that over the slots its
+ * sequence has for itself.  The outputs are tc_attend's (their sums are split at
+ * the end of the prefix, so that last bits may differ).
+ *
+ *  groups       1 .. batch: runs of neighbouring sequences.
+ *  cu_seqs      (device) int32[groups + 1], ascending within [0, batch]: group g
+ *               is sequences [cu_seqs[g], cu_seqs[g + 1]).  Where they do not
+ *               ascend, every sequence gets TC_ERR_BOUNDS.  A sequence that no
+ *               group holds, or that is alone in one, shares nothing.
+ *  shared_lens  (device) int32[groups]: the first shared_lens[g] slots of a
+ *               group's sequences are the same; sharing is in whole pages, so
+ *               the length is rounded down to them.  Those pages have the same
+ *               ids in every sequence's page table.  A sequence where they
+ *               differ from the group's first one's, or with fewer slots cached
+ *               than its group shares, gets TC_ERR_BOUNDS, and so does a whole
+ *               group whose length is out of range.
+ *  workspace    (device) tc_attend_shared_workspace bytes for this number of
+ *               tokens and heads (those of tc_attend, and two results of
+ *               head_dim + 2 floats for each token and query head).
+ */
+typedef struct tc_shared_t {
+  int32_t groups;
+  const int32_t* cu_seqs;
+  const int32_t* shared_lens;
+} tc_shared_t;
+
+tc_status tc_attend_shared(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* args,
+                           const tc_shared_t* shared, void* workspace, int64_t workspace_bytes, int32_t* status,
+                           void* stream);
+
+tc_status tc_attend_shared_workspace(const tc_kv_t* kv, int32_t n_tokens, int32_t q_heads, int64_t* bytes);
+
+/*
  * tc_tree_masks - the masks and positions of drafted trees from their parents.
  *
  *  parents    (device) int32[n_tokens]: a drafted token's parent as its index

@@ -368,11 +368,19 @@ class _Attend(ctypes.Structure):
                 ("withhold", ctypes.c_int32)]
 
 
+class _Shared(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("cu_seqs", _vp), ("shared_lens", _vp)]
+
+
 _kvp, _tokp = ctypes.POINTER(_Kv), ctypes.POINTER(_Tokens)
 _kv_append = _decl("tc_kv_append", ctypes.c_int, [_kvp, ctypes.c_int32, _tokp, ctypes.POINTER(_Append), _vp, _vp])
 _attend = _decl("tc_attend", ctypes.c_int, [_kvp, ctypes.c_int32, _tokp, ctypes.POINTER(_Attend), _vp, ctypes.c_int64,
                                             _vp, _vp])
 _attend_workspace = _decl("tc_attend_workspace", ctypes.c_int, [_kvp, _i64p])
+_attend_shared = _decl("tc_attend_shared", ctypes.c_int, [_kvp, ctypes.c_int32, _tokp, ctypes.POINTER(_Attend),
+                                                          ctypes.POINTER(_Shared), _vp, ctypes.c_int64, _vp, _vp])
+_attend_shared_workspace = _decl("tc_attend_shared_workspace", ctypes.c_int, [_kvp, ctypes.c_int32, ctypes.c_int32,
+                                                                             _i64p])
 _tree_masks = _decl("tc_tree_masks", ctypes.c_int, [_tokp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp])
 _kv_copy_pages = _decl("tc_kv_copy_pages", ctypes.c_int, [_kvp, _vp, _vp, ctypes.c_int32, _vp, _vp])
 _kv_compact = _decl("tc_kv_compact", ctypes.c_int, [_kvp, _tokp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp])
@@ -431,6 +439,7 @@ class _Own:
 
     def __init__(self, codes: _Codes, stream: int, gone=None):
         self.codes, self.workspace, self.place, self.stream = codes, None, None, stream  # (whose memory it is)
+        self.outgrown = []                   # (captured) smaller workspaces that earlier calls of the graph use
         self.gone = gone                     # (captured) a word: 1 when the graph is gone
 
     def idle(self) -> bool:
@@ -569,15 +578,18 @@ class KvCache:
             codes.used[pairs] = min(n, KV_MAX_BATCH)
         return self._kvp_keep, codes.at + 4 * KV_MAX_BATCH * pairs
 
-    def _workspace(self, workspace, stream: int, own=None):
+    def _workspace(self, workspace, stream: int, own=None, need: int = 0):
         if workspace is None:
             own = own or self._buffers(stream)
-            if own.place is None:
-                if own.stream == stream:
-                    own.workspace = _empty(self.workspace_bytes, self._u8, self.device, stream)
+            if own.place is None or own.place[1] < need:
+                need = max(need, self.workspace_bytes)
+                if own.stream == stream:     # (an outgrown one goes back to its stream's memory)
+                    own.workspace = _empty(need, self._u8, self.device, stream)
                 else:
-                    own.workspace = _empty_aside(self.workspace_bytes, self._u8, self.device, own.stream, clear=False)
-                own.place = own.workspace.data_ptr(), self.workspace_bytes
+                    if own.workspace is not None:
+                        own.outgrown.append(own.workspace)
+                    own.workspace = _empty_aside(need, self._u8, self.device, own.stream, clear=False)
+                own.place = own.workspace.data_ptr(), need
             return own.place
         if workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
@@ -624,6 +636,36 @@ class KvCache:
                lse=None, status=None, stream=None, workspace=None):
         """tc_attend: q and out [n, q_heads, head_dim]; tree int64 [n, words] (tree_masks) or None for the causal
         mask; scale defaults to head_dim ** -0.5; lse float32 [n, q_heads] or None."""
+        a, t = self._attend_args(q, cu_tokens, ctx_lens, page_table, out, max_tokens, scale, tree, lse)
+        s = self._stream(stream)
+        own = None if workspace is not None else self._buffers(s)
+        kv, codes = self._codes(status, t.batch, s, own=own)
+        _check(_attend(kv, layer, t, a, *self._workspace(workspace, s, own), codes, s), "tc_attend")
+
+    def attend_shared(self, layer: int, q, cu_tokens, ctx_lens, page_table, out, max_tokens: int, cu_seqs, shared_lens,
+                      scale=None, tree=None, lse=None, status=None, stream=None, workspace=None):
+        """tc_attend_shared: attend for sequences that share the beginning of their contexts, which is read once for
+        all of them.  cu_seqs int32 [groups + 1]: the first sequence of each group, and the last one's end;
+        shared_lens int32 [groups]: slots that a group shares (rounded down to whole pages).  A workspace given to the
+        call has shared_workspace_bytes(n, q_heads) bytes or more."""
+        a, t = self._attend_args(q, cu_tokens, ctx_lens, page_table, out, max_tokens, scale, tree, lse)
+        groups = shared_lens.shape[0]
+        g = _Shared(groups, self._ints(cu_seqs, (groups + 1,), "cu_seqs"),
+                    self._ints(shared_lens, (groups,), "shared_lens"))
+        s = self._stream(stream)
+        own = None if workspace is not None else self._buffers(s)
+        kv, codes = self._codes(status, t.batch, s, own=own)
+        need = self.shared_workspace_bytes(t.n_tokens, a.q_heads)
+        _check(_attend_shared(kv, layer, t, a, g, *self._workspace(workspace, s, own, need), codes, s),
+               "tc_attend_shared")
+
+    def shared_workspace_bytes(self, n: int, q_heads: int) -> int:
+        """Bytes of workspace that attend_shared needs for n tokens."""
+        need = ctypes.c_int64()
+        _check(_attend_shared_workspace(self._kvp, n, q_heads, ctypes.byref(need)), "tc_attend_shared_workspace")
+        return need.value
+
+    def _attend_args(self, q, cu_tokens, ctx_lens, page_table, out, max_tokens, scale, tree, lse):
         d, shape = self.head_dim, q.shape
         n = shape[0]
         if out.shape[0] != n:
@@ -644,11 +686,7 @@ class KvCache:
             sums = lse.data_ptr()
         a = _Attend(*_rows(q, dtype, device, "q", hq, d), hq, max_tokens, d ** -0.5 if scale is None else scale, masks,
                     words, *_rows(out, dtype, device, "out", hq, d), sums, *self._wait_test)
-        t = self._tokens(n, cu_tokens, ctx_lens, page_table)
-        s = self._stream(stream)
-        own = None if workspace is not None else self._buffers(s)
-        kv, codes = self._codes(status, t.batch, s, own=own)
-        _check(_attend(kv, layer, t, a, *self._workspace(workspace, s, own), codes, s), "tc_attend")
+        return a, self._tokens(n, cu_tokens, ctx_lens, page_table)
 
     def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
         """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)

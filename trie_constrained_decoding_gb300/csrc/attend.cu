@@ -93,6 +93,7 @@
 
 #include <climits>
 #include <cstddef>
+#include <type_traits>
 
 #include "kv_cache.h"
 
@@ -135,6 +136,16 @@ struct Seg {
   int32_t last;      // (slot 1) the last worker that has a part of the item
 };
 
+// What an item of a call with common prefixes (SH) is: a sequence that shares nothing,
+// a group's prefix, the rest of one of its sequences.
+enum { kWhole = 0, kPrefix = 1, kRest = 2 };
+struct SharedSeg : Seg {
+  int32_t kind;
+  int64_t pages;     // where the item's page ids begin in the table
+};
+template <bool SH>
+using SegOf = std::conditional_t<SH, SharedSeg, Seg>;
+
 struct AttendParams {
   KvView kv;
   TokensView tok;
@@ -151,13 +162,22 @@ struct AttendParams {
   float* lse;
   int32_t* status;
   int32_t workers;
-  Seg* descs;        // [workers] item that starts in a worker and goes on in the next (valid = 0: none)
+  SharedSeg* descs;  // [workers] item that starts in a worker and goes on in the next (valid = 0: none)
   int32_t* errs;     // [workers] a wait ran out
   float2* part_ml;   // [workers][2][256] maximum and sum of each row
   float* part_o;     // [workers][2][D / 4][256][4]
   int32_t wait_limit;
   int32_t withhold;  // test switch: the first workers' first loads are not issued
+  // Groups with a common prefix:
+  const int32_t* cu_seqs;
+  const int32_t* shared_lens;
+  int32_t groups;
+  int32_t prefix_q_rows;  // rows of one query load of a prefix
+  float* row_o;      // [prefix or rest][token, head][D] results before they are joined,
+  float2* row_ml;    // [prefix or rest][token, head] and their maxima and sums
 };
+
+constexpr int kMisfit = 2;  // in errs: the groups do not ascend
 
 constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile; }
 
@@ -181,10 +201,24 @@ struct Hdr {
   int32_t abort;
   int64_t off0;                      // the worker's first unit within its sequence
   int32_t seq0, row0, n0, ctx0;      // its sequence
+  int32_t kind0;
+  int64_t pages0;
   uint32_t bad[3][8];                // tokens whose values are not finite, by segment
   Seg seg[kSegs];
+  int32_t seg_kind[kSegs];           // (beside them, for calls with common prefixes)
+  int64_t seg_pages[kSegs];
   float2 ml[2][kTile];               // (the prologue's sums before the first segment)
 };
+template <bool SH>
+__device__ __forceinline__ SegOf<SH> read_seg(const Hdr* hdr, int i) {
+  SegOf<SH> g;
+  static_cast<Seg&>(g) = hdr->seg[i];
+  if constexpr (SH) {
+    g.kind = hdr->seg_kind[i];
+    g.pages = hdr->seg_pages[i];
+  }
+  return g;
+}
 template <int D>
 constexpr size_t smem_bytes() {
   return (2 + Cfg<D>::kStages) * (size_t)Cfg<D>::kTileBytes + sizeof(Hdr);
@@ -410,10 +444,11 @@ struct Line {
   int n, ctx, step;  // tokens, cached tokens, tokens of an item
   bool causal;
   int extra;         // units of an item beside its tiles
+  bool prefix = false;  // the tokens have no slots of their own among these
   __device__ int items() const { return (n + step - 1) / step; }
   // tiles of item i
   __device__ int tiles(int i) const {
-    const int64_t end = causal ? min((int64_t)n, (int64_t)(i + 1) * step) : n;
+    const int64_t end = prefix ? 0 : causal ? min((int64_t)n, (int64_t)(i + 1) * step) : n;
     return (int)((ctx + end + kTile - 1) / kTile);
   }
   // units of the items before item i
@@ -428,6 +463,11 @@ struct Line {
   // The item that unit u is in; u becomes its number within the item.
   __device__ __forceinline__ int item_of(int64_t& u) const {
     if (n <= step) return 0;
+    if (prefix) {  // (any number of tokens)
+      const int64_t per = tiles(0) + extra, i = u / per;
+      u -= i * per;
+      return (int)i;
+    }
     if (!causal) {  // (at most 256 tokens: the units of a head fit 32 bits)
       const uint32_t per = tiles(0) + extra, i = (uint32_t)u / per;
       u -= (int64_t)i * per;
@@ -451,7 +491,76 @@ struct Line {
   }
 };
 
-__device__ __forceinline__ bool line_of(const AttendParams& p, int b, int extra, SeqSpan* s, Line* l) {
+// The group of sequence b among ascending ones, or -1.
+__device__ __forceinline__ int group_of(const AttendParams& p, int b) {
+  int lo = -1, hi = p.groups;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(p.cu_seqs + mid) <= b)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo >= 0 && __ldg(p.cu_seqs + lo + 1) > b ? lo : -1;
+}
+// Slots of group g's prefix: whole pages; 0 where fewer than two sequences share it; -1: out of range.
+__device__ __forceinline__ int prefix_of(const AttendParams& p, int g) {
+  const int len = __ldg(p.shared_lens + g);
+  const int64_t room = (int64_t)p.tok.width * p.kv.page_size;
+  if (len < 0 || len > (room < kMaxSlots ? room : kMaxSlots)) return -1;
+  return __ldg(p.cu_seqs + g + 1) - __ldg(p.cu_seqs + g) < 2 ? 0 : len & -p.kv.page_size;
+}
+
+// A line of the work: a sequence, or (SH: there are groups with a common prefix) first
+// each group's prefix, then what each sequence has for itself.
+struct Span : SeqSpan {
+  int32_t kind = kWhole;
+  int64_t pages = 0;
+};
+template <bool SH>
+__device__ __forceinline__ int lines(const AttendParams& p) {
+  return SH ? p.groups + p.tok.batch : p.tok.batch;
+}
+template <bool SH>
+__device__ __forceinline__ void set_line(const AttendParams& p, const Span& s, int extra, Line* l) {
+  l->n = s.n;
+  l->ctx = s.ctx;
+  l->step = 2 * p.tile_tokens;
+  l->causal = p.tree == nullptr && !(SH && s.kind == kPrefix);
+  l->extra = extra;
+  l->prefix = SH && s.kind == kPrefix;
+}
+template <bool SH>
+__device__ __forceinline__ bool line_of(const AttendParams& p, int v, int extra, Span* s, Line* l) {
+  if constexpr (SH) {
+    bool ok;
+    if (v < p.groups) {
+      const int lo = __ldg(p.cu_seqs + v), hi = __ldg(p.cu_seqs + v + 1), len = prefix_of(p, v);
+      s->kind = kPrefix;
+      ok = len > 0;
+      if (ok) {
+        s->row0 = __ldg(p.tok.cu + lo);
+        const int end = __ldg(p.tok.cu + hi);
+        s->n = end - s->row0;
+        s->ctx = len;
+        s->pages = (int64_t)lo * p.tok.width;
+        ok = s->row0 >= 0 && end >= s->row0 && end <= p.tok.n_tokens;
+      }
+    } else {
+      const int b = v - p.groups;
+      ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
+      const int g = group_of(p, b), len = g < 0 ? 0 : prefix_of(p, g);
+      ok = ok && len >= 0 && len <= s->ctx;
+      s->kind = len > 0 ? kRest : kWhole;
+      s->pages = (int64_t)b * p.tok.width + (len >> p.kv.page_shift);
+      s->ctx -= len;
+    }
+    if (!ok) s->n = s->ctx = 0;
+    set_line<SH>(p, *s, extra, l);
+    return ok;
+  }
+  const int b = v;
   const bool ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
   l->n = ok ? s->n : 0;
   l->ctx = ok ? s->ctx : 0;
@@ -471,9 +580,20 @@ struct Cut {
 };
 
 // Which of the 32 NW slots from `start` a row sees.
-template <int NW>
-__device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, int tok, int start, uint32_t (&m)[NW]) {
+template <bool SH, int NW>
+__device__ __forceinline__ void row_mask(const AttendParams& p, const SegOf<SH>& g, int tok, int start,
+                                         uint32_t (&m)[NW]) {
   int left = g.end - start;  // slots from `start` that any row sees
+  if constexpr (SH) {
+    if (g.kind == kPrefix) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const int k = left - 32 * w;
+        m[w] = k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
+      }
+      return;
+    }
+  }
   if (!p.tree) left = g.ctx + tok + 1 - start;
   uint32_t v[NW + 1];
   // The first slot as a drafted token's number, and the row's words from the
@@ -498,7 +618,11 @@ __device__ __forceinline__ void row_mask(const AttendParams& p, const Seg& g, in
 }
 
 // The first slot of an item that some row of it does not see.
-__device__ __forceinline__ int first_hidden(const AttendParams& p, const Seg& g) {
+template <bool SH>
+__device__ __forceinline__ int first_hidden(const AttendParams& p, const SegOf<SH>& g) {
+  if constexpr (SH) {
+    if (g.kind == kPrefix) return g.end;
+  }
   return p.tree ? g.ctx : g.ctx + g.tok0 + 1;
 }
 
@@ -533,10 +657,19 @@ __device__ __forceinline__ float log_sum(float m, float l, float c) {
   return l == 0.f ? -INFINITY : (m * c + (log2f(l) - T::kShift)) * kLn2;
 }
 
+// The page ids of an item.
+template <bool SH>
+__device__ __forceinline__ const int32_t* page_row(const AttendParams& p, const SegOf<SH>& g) {
+  if constexpr (SH)
+    return p.tok.table + g.pages;
+  else
+    return p.tok.table + (int64_t)g.seq * p.tok.width;
+}
+
 // Adds to 32 columns of a row the infinities and NaN that were taken out of the
 // values of slots it sees (from the cache itself; rare).
-template <typename T, int D>
-__device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& g, const uint32_t* bad, int hidden,
+template <typename T, int D, bool SH>
+__device__ __forceinline__ void add_taken_out(const AttendParams& p, const SegOf<SH>& g, const uint32_t* bad, int hidden,
                                            int tok, int c, float (&v)[32]) {
 #pragma unroll 1
   for (int i = 0; i < 8; ++i)
@@ -544,9 +677,9 @@ __device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& 
     for (uint32_t w = bad[i]; w; w &= w - 1) {
       const int slot = hidden + i * 32 + __ffs(w) - 1;
       uint32_t mask[1];
-      row_mask<1>(p, g, tok, slot, mask);
+      row_mask<SH, 1>(p, g, tok, slot, mask);
       if (!(mask[0] & 1u)) continue;
-      const int page = __ldg(p.tok.table + (int64_t)g.seq * p.tok.width + (slot >> p.kv.page_shift));
+      const int page = __ldg(page_row<SH>(p, g) + (slot >> p.kv.page_shift));
       if ((uint32_t)page >= (uint32_t)p.kv.pages) continue;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           p.kv.base + ((((int64_t)page * 2 + 1) * p.kv.kv_heads + g.head) * p.kv.page_size +
@@ -562,10 +695,10 @@ __device__ __forceinline__ void add_taken_out(const AttendParams& p, const Seg& 
 
 // ------------------------------------------------------------------- kernel
 
-template <typename T, int D>
+template <typename T, int D, bool SH>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap map_kv,
-                  const __grid_constant__ CUtensorMap map_q) {
+                  const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pq) {
   using C = Cfg<D>;
   constexpr int NS = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -621,14 +754,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Tiles and items of every sequence: thread i counts a run of them, then a
   // scan over the CTA gives the totals and who holds this worker's first unit.
-  const int run = (p.tok.batch + kThreads - 1) / kThreads;
+  const int n_lines = lines<SH>(p), run = (n_lines + kThreads - 1) / kThreads;
+  bool fits = true;
+  if constexpr (SH) {
+    // Groups that do not ascend: no work, and an error of every sequence.
+    for (int g = tid; g < p.groups; g += kThreads) {
+      const int lo = __ldg(p.cu_seqs + g), hi = __ldg(p.cu_seqs + g + 1);
+      fits &= lo >= 0 && hi >= lo && hi <= p.tok.batch;
+    }
+    fits = __syncthreads_and(fits);
+  }
   int64_t* sums = reinterpret_cast<int64_t*>(hdr->ml);
   int64_t tiles = 0, items = 0;
   for (int i = 0; i < run; ++i) {
     const int b = tid * run + i;
-    SeqSpan s;
+    Span s;
     Line l;
-    if (b < p.tok.batch && line_of(p, b, 0, &s, &l) && s.n > 0) {
+    if (b < n_lines && fits && line_of<SH>(p, b, 0, &s, &l) && s.n > 0) {
       tiles += l.units() * p.kv.kv_heads;
       items += (int64_t)l.items() * p.kv.kv_heads;
     }
@@ -669,9 +811,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t at = excl;
     for (int i = 0; i < run; ++i) {
       const int b = tid * run + i;
-      SeqSpan s;
+      Span s;
       Line l;
-      if (b >= p.tok.batch || !line_of(p, b, extra, &s, &l)) continue;
+      if (b >= n_lines || !line_of<SH>(p, b, extra, &s, &l)) continue;
       const int64_t u = l.units() * p.kv.kv_heads;
       if (begin < at + u) {
         hdr->seq0 = b;
@@ -679,6 +821,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         hdr->n0 = s.n;
         hdr->ctx0 = s.ctx;
         hdr->off0 = begin - at;
+        if (SH) {
+          hdr->kind0 = s.kind;
+          hdr->pages0 = s.pages;
+        }
         break;
       }
       at += u;
@@ -709,11 +855,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = false;
     for (int k = 0; !stop; ++k) {
       if (!warp_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
-      const Seg g = hdr->seg[k % kSegs];
+      const SegOf<SH> g = read_seg<SH>(hdr, k % kSegs);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
       if (!g.valid) break;
-      const int32_t* row = p.tok.table + (int64_t)g.seq * p.tok.width;
+      const int32_t* row = page_row<SH>(p, g);
       const int head = (is_v ? p.kv.kv_heads : 0) + g.head;
       int slot = g.t0 * kTile + piece * box;
       bool load = piece < pieces && slot < g.end;
@@ -745,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool stop = false;
       for (int k = 0; !stop; ++k) {
         if (!mbar_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
-        const Seg g = hdr->seg[k % kSegs];
+        const SegOf<SH> g = read_seg<SH>(hdr, k % kSegs);
         mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
         if (!g.valid) break;
         for (int m = 0; m <= g.two; ++m, ++armed) {
@@ -754,9 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t bar = smem_u32(&hdr->q_full[armed & 3]);
-          mbar_expect_tx(bar, (uint32_t)p.q_rows * 128u * C::kHalves);
+          bool of_prefix = false;
+          if constexpr (SH) of_prefix = g.kind == kPrefix;
+          mbar_expect_tx(bar, (uint32_t)(of_prefix ? p.prefix_q_rows : p.q_rows) * 128u * C::kHalves);
           for (int h = 0; h < C::kHalves; ++h)
-            tma_q(q_s + (armed & 1) * C::kTileBytes + h * kHalfBytes, &map_q, h * 64, g.head * p.group,
+            tma_q(q_s + (armed & 1) * C::kTileBytes + h * kHalfBytes, of_prefix ? &map_pq : &map_q, h * 64,
+                  g.head * p.group,
                   g.row0 + g.tok0 + m * p.tile_tokens, bar);
         }
       }
@@ -784,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int k = 0; ok; ++k) {
         if (!wait(&hdr->seg_full[k % kSegs], k / kSegs)) break;
-        const Seg g = hdr->seg[k % kSegs];
+        const SegOf<SH> g = read_seg<SH>(hdr, k % kSegs);
         mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
         if (!g.valid) break;
         const int n = g.t1 - g.t0, hop = g.two ? 1 : 2, i0 = g.two ? 0 : slot;
@@ -852,19 +1001,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       int b = hdr->seq0, k = 0;
       bool open_end = false, ok = true;
       if (b < 0) left = 0;
-      Seg d{};
+      SegOf<SH> d{};
       while (ok) {
-        Seg g{};
+        SegOf<SH> g{};
         if (left > 0) {
-          SeqSpan s{hdr->row0, hdr->n0, hdr->ctx0};
-          Line l{s.n, s.ctx, 2 * p.tile_tokens, p.tree == nullptr, extra};
+          Span s;
+          s.row0 = hdr->row0;
+          s.n = hdr->n0;
+          s.ctx = hdr->ctx0;
+          if (SH) {
+            s.kind = hdr->kind0;
+            s.pages = hdr->pages0;
+          }
+          Line l;
+          set_line<SH>(p, s, extra, &l);
           int64_t per = 0;
           if (b == hdr->seq0) {
             per = l.units();
           } else {
             // (sequences without units are passed over)
-            while (b < p.tok.batch && !(line_of(p, b, extra, &s, &l) && (per = l.units()) > 0)) ++b;
-            if (b >= p.tok.batch) break;  // (cannot be: the units add up)
+            while (b < n_lines && !(line_of<SH>(p, b, extra, &s, &l) && (per = l.units()) > 0)) ++b;
+            if (b >= n_lines) break;  // (cannot be: the units add up)
           }
           // (kv_heads < 2^16)
           int h = 0;
@@ -891,7 +1048,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               g.head = h;
               g.tok0 = item * l.step;
               g.two = s.n - g.tok0 > p.tile_tokens;
-              g.end = s.ctx + (p.tree ? s.n : min(s.n, g.tok0 + l.step));
+              g.end = s.ctx + (l.prefix ? 0 : p.tree ? s.n : min(s.n, g.tok0 + l.step));
+              if constexpr (SH) {
+                g.kind = s.kind;
+                g.pages = s.pages;
+              }
               g.part = g.t1 - g.t0 == tiles ? -1 : g.t0 > 0 ? 0 : 1;
               g.last = worker;
               if (g.part == 1) {
@@ -908,6 +1069,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
               }
               hdr->seg[k % kSegs] = g;
+              if constexpr (SH) {
+                hdr->seg_kind[k % kSegs] = g.kind;
+                hdr->seg_pages[k % kSegs] = g.pages;
+              }
               mbar_arrive(smem_u32(&hdr->seg_full[k % kSegs]));
               ++k;
             }
@@ -929,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       d.valid = open_end;
-      p.descs[worker] = d;
+      static_cast<SegOf<SH>&>(p.descs[worker]) = d;
     }
     __syncwarp();
   }
@@ -953,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int k = 0;; ++k) {
       if (!warp_wait(smem_u32(&hdr->seg_full[k % kSegs]), (k / kSegs) & 1, wl, abort)) break;
-      const Seg g = hdr->seg[k % kSegs];
+      const SegOf<SH> g = read_seg<SH>(hdr, k % kSegs);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&hdr->seg_empty[k % kSegs]));
       if (!g.valid) break;
@@ -961,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = g.tok0 + (g.two ? grp * p.tile_tokens : 0) + r / p.group;
       const bool live = r < p.tile_tokens * p.group && tok < g.n;
       const bool any = __any_sync(0xffffffffu, live);
-      const int hidden = first_hidden(p, g);
+      const int hidden = first_hidden<SH>(p, g);
       uint32_t* bad = hdr->bad[k % 3];
       float m = -INFINITY, l = 0.f;
       bool stop = false;
@@ -1089,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t mask[W / 32];
 #pragma unroll
           for (int c = 0; c < W / 32; ++c) mask[c] = 0u;
-          if (live) row_mask<W / 32>(p, g, tok, start, mask);
+          if (live) row_mask<SH, W / 32>(p, g, tok, start, mask);
           if (!warp_wait(smem_u32(&hdr->s_full[grp]), n_s & 1, wl, abort)) {
             stop = true;
             break;
@@ -1190,7 +1355,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i) any_bad |= bad[i];
       const int head = g.head * p.group + r % p.group;
       uint8_t* out = p.out + ((int64_t)(g.row0 + tok) * p.out_stride + (int64_t)head * D) * 2;
-      const float norm = g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
+      bool joined = false;  // (a result to be joined with another's)
+      size_t row_at = 0;
+      if constexpr (SH) {
+        joined = g.kind != kWhole;
+        row_at = ((size_t)(g.kind == kRest) * p.tok.n_tokens + g.row0 + tok) * p.q_heads + head;
+      }
+      const float norm = g.part >= 0 || joined ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
       const int rr = (g.two ? grp * kTile : 0) + r;
       const size_t part = ((size_t)worker * 2 + (g.part > 0)) * 2 * kTile;
       // Columns: all of the group's own accumulator, or half of both.
@@ -1211,8 +1382,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o1[j]), f1, v[j]);
           }
-          if (live && any_bad) add_taken_out<T, D>(p, g, bad, hidden, tok, c, v);
-          if (live && g.part < 0) {
+          if (live && any_bad) add_taken_out<T, D, SH>(p, g, bad, hidden, tok, c, v);
+          if (joined && live && g.part < 0) {
+            float* dst = p.row_o + row_at * D + c;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) stg256(dst + j, reinterpret_cast<const uint32_t*>(v) + j);
+          } else if (live && g.part < 0) {
             // (64 bytes of a row: whole sectors, and no shared memory is held up
             // for the next item.  16 bytes a store: four prompts of 2048
             // 152 us against 148, 16 short ones 47 against 45.5)
@@ -1243,6 +1418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live && (g.two || grp == 0)) {
         if (g.part >= 0)
           p.part_ml[part + rr] = make_float2(m, l);
+        else if (joined)
+          p.row_ml[row_at] = make_float2(m, l);
         else if (p.lse)
           p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = log_sum<T>(m, l, p.c);
       }
@@ -1276,7 +1453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
-  if (tid == 0) p.errs[worker] = hdr->abort;
+  if (tid == 0) p.errs[worker] = hdr->abort ? 1 : fits ? 0 : kMisfit;
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
@@ -1298,7 +1475,7 @@ constexpr int kJoinThreads = 256, kJoinBlocks = 8;
 // Letting the blocks start while the first kernel still runs is slower (one token
 // 18.1 us against 17.4).  The blocks after these write the status of a sequence
 // each (one block, as a warp takes 10 us for the pages of 131,000 slots).
-template <typename T, int D>
+template <typename T, int D, bool SH>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x >= (unsigned)(p.workers * kJoinBlocks)) {
@@ -1310,7 +1487,25 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
 #pragma unroll 4
     for (int i = threadIdx.x; i < pages; i += kJoinThreads) ok &= (uint32_t)__ldg(row + i) < (uint32_t)p.kv.pages;
     bool late = false;
-    for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) late |= __ldcg(p.errs + i) != 0;
+    if constexpr (SH) {
+      bool fits = true;
+      for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) {
+        const int e = __ldcg(p.errs + i);
+        late |= e == 1;
+        fits &= e != kMisfit;
+      }
+      fits = __syncthreads_and(fits);
+      const int g = fits ? group_of(p, b) : -1, len = g < 0 ? 0 : prefix_of(p, g);
+      ok &= fits && len >= 0 && (!ok || s.n == 0 || len <= s.ctx);
+      // the prefix lies in the same pages as the group's first sequence's
+      if (ok && len > 0) {
+        const int32_t* first = p.tok.table + (int64_t)__ldg(p.cu_seqs + g) * p.tok.width;
+        for (int i = threadIdx.x; i < len >> p.kv.page_shift && s.n > 0; i += kJoinThreads)
+          ok &= __ldg(row + i) == __ldg(first + i);
+      }
+    } else {
+      for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) late |= __ldcg(p.errs + i) != 0;
+    }
     ok = __syncthreads_and(ok);
     late = __syncthreads_or(late);
     if (threadIdx.x == 0)
@@ -1318,7 +1513,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
     return;
   }
   const int w0 = blockIdx.x / kJoinBlocks, y = blockIdx.x % kJoinBlocks;
-  const Seg g = p.descs[w0];
+  const SegOf<SH> g = p.descs[w0];
   if (!g.valid) return;
   const int full = p.tile_tokens * p.group, left = (g.n - g.tok0) * p.group;
   const int v0 = min(left, full), rows = g.two ? min(left, 2 * full) : v0;  // rows of the first M tile, of both
@@ -1345,10 +1540,53 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
     const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
     const int tok = g.tok0 + k / p.group, head = g.head * p.group + k % p.group;
     const int64_t row = g.row0 + tok;
+    if constexpr (SH) {
+      if (g.kind != kWhole) {
+        const size_t to = ((size_t)(g.kind == kRest) * p.tok.n_tokens + row) * p.q_heads + head;
+        *reinterpret_cast<float4*>(p.row_o + to * D + 4 * c) = v;
+        if (c == 0) p.row_ml[to] = make_float2(m, l);
+        continue;
+      }
+    }
     *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + (int64_t)head * D + 4 * c) * 2) =
         make_uint2(T::pack(v.x * norm, v.y * norm), T::pack(v.z * norm, v.w * norm));
     if (p.lse && c == 0)
       p.lse[row * p.q_heads + head] = log_sum<T>(m, l, p.c);
+  }
+}
+
+// The prefix's part and the own part of each row: out = sum of the parts, each
+// times exp(its maximum - the larger one), over the sum of theirs.  A block takes
+// every blocks-th group of rows of its sequence, a row's 4 columns a thread.
+constexpr int kPairThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPairThreads) attend_pair_kernel(const AttendParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x;
+  SeqSpan s;
+  if (__ldcg(p.errs) == kMisfit || !seq_span(p.tok, p.kv.page_size, b, &s) || s.n > p.max_tokens) return;
+  const int g = group_of(p, b), len = g < 0 ? 0 : prefix_of(p, g);
+  if (len <= 0 || len > s.ctx) return;
+  constexpr int kRow = D / 4;  // threads of a row
+  const size_t first = (size_t)s.row0 * p.q_heads, rest = (size_t)p.tok.n_tokens * p.q_heads;
+  const int64_t rows = (int64_t)s.n * p.q_heads;
+  for (int64_t r = blockIdx.y * (kPairThreads / kRow) + threadIdx.x / kRow; r < rows;
+       r += gridDim.y * (kPairThreads / kRow)) {
+    const size_t at = first + r;
+    const int c = threadIdx.x % kRow * 4;
+    const float2 x = __ldcg(p.row_ml + at), y = __ldcg(p.row_ml + rest + at);
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(p.row_o + at * D + c));
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.row_o + (rest + at) * D + c));
+    const float m = fmaxf(x.x, y.x);
+    const float e = m == -INFINITY ? 0.f : ex2((x.x - m) * p.c), f = m == -INFINITY ? 0.f : ex2((y.x - m) * p.c);
+    const float l = fmaf(x.y, e, y.y * f);
+    const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
+    const int64_t row = s.row0 + r / p.q_heads, head = r % p.q_heads;
+    *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + head * D + c) * 2) =
+        make_uint2(T::pack(fmaf(u.x, e, v.x * f) * norm, fmaf(u.y, e, v.y * f) * norm),
+                   T::pack(fmaf(u.z, e, v.z * f) * norm, fmaf(u.w, e, v.w * f) * norm));
+    if (p.lse && c == 0) p.lse[at] = log_sum<T>(m, l, p.c);
   }
 }
 
@@ -1396,17 +1634,24 @@ int sm_count(int device) {
 }
 
 size_t workspace_bytes(int workers, int head_dim) {
-  return (size_t)workers * (sizeof(Seg) + 16) + part_rows(workers) * (sizeof(float2) + sizeof(float) * head_dim) + 64;
+  return (size_t)workers * (sizeof(SharedSeg) + 16) + part_rows(workers) * (sizeof(float2) + sizeof(float) * head_dim) + 64;
 }
 
-template <typename T, int D>
-cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q, cudaStream_t s) {
+// What joining two results of every row takes beside that.
+size_t shared_bytes(int64_t rows, int head_dim) {
+  return 2 * (size_t)rows * (sizeof(float2) + sizeof(float) * head_dim) + 256;
+}
+
+template <typename T, int D, bool SH>
+cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q, const CUtensorMap& pq,
+                   cudaStream_t s) {
   static bool ready[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+    e = cudaFuncSetAttribute(attend_kernel<T, D, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_bytes<D>());
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
@@ -1420,56 +1665,56 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorM
   cfg.gridDim = dim3((unsigned)p.workers);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes<D>();
-  e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D>, p, kv, q);
+  e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D, SH>, p, kv, q, pq);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(p.workers * kJoinBlocks + p.tok.batch));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p);
+  e = cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, SH>, p);
+  if (!SH || e != cudaSuccess) return e;
+  const int64_t most = (int64_t)(p.max_tokens < p.tok.n_tokens ? p.max_tokens : p.tok.n_tokens) * p.q_heads;
+  const int64_t blocks = (most + 2 * (kPairThreads / (D / 4)) - 1) / (2 * (kPairThreads / (D / 4)));
+  cfg.gridDim = dim3((unsigned)p.tok.batch, (unsigned)(blocks < 1 ? 1 : blocks < 256 ? blocks : 256));
+  cfg.blockDim = dim3(kPairThreads);
+  return cudaLaunchKernelEx(&cfg, attend_pair_kernel<T, D>, p);
 }
 
-}  // namespace
-}  // namespace tcd
-
-using namespace tcd;
-
-extern "C" tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes) {
-  const tc_status rc = kv_check("tc_attend_workspace", kv);
-  if (rc != TC_OK) return rc;
-  if (!bytes) return kv_fail(TC_ERR_INVALID_ARG, "tc_attend_workspace: bytes is NULL");
-  const int sms = sm_count(kv->device);
-  if (sms < 1) return kv_fail(TC_ERR_CUDA, "tc_attend_workspace: no such device");
-  *bytes = (int64_t)workspace_bytes(sms, kv->head_dim);
-  return TC_OK;
+template <bool SH>
+cudaError_t launch(int dtype, int head_dim, const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q,
+                   const CUtensorMap& pq, cudaStream_t s) {
+  if (dtype == TC_DT_BF16)
+    return head_dim == 128 ? launch<Bf16, 128, SH>(p, kv, q, pq, s) : launch<Bf16, 64, SH>(p, kv, q, pq, s);
+  return head_dim == 128 ? launch<F16, 128, SH>(p, kv, q, pq, s) : launch<F16, 64, SH>(p, kv, q, pq, s);
 }
 
-extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* a,
-                               void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
-  tc_status rc = kv_check("tc_attend", kv);
-  if (rc == TC_OK) rc = kv_check_tokens("tc_attend", tokens, true);
+tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* a,
+                 const tc_shared_t* sh, void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
+  tc_status rc = kv_check(who, kv);
+  if (rc == TC_OK) rc = kv_check_tokens(who, tokens, true);
   if (rc != TC_OK) return rc;
   if (!a || !status || layer < 0 || layer >= kv->layers || a->q_heads < 1 || a->max_tokens < 0 ||
       !tokens->page_table || tokens->table_width < 1 || !(a->scale == a->scale))
-    return kv_fail(TC_ERR_INVALID_ARG, "tc_attend: invalid arguments");
+    return kv_fail(TC_ERR_INVALID_ARG, who, ": invalid arguments");
   if (a->q_heads % kv->kv_heads != 0 || a->q_heads / kv->kv_heads > 128)
-    return kv_fail(TC_ERR_UNSUPPORTED,
-                   "tc_attend: q_heads must be a multiple of kv_heads, with at most 128 of them for each");
+    return kv_fail(TC_ERR_UNSUPPORTED, who,
+                   ": q_heads must be a multiple of kv_heads, with at most 128 of them for each");
   if (a->tree && (a->tree_words < 1 || a->tree_words > TC_TREE_MAX_WORDS || a->max_tokens > 64 * a->tree_words))
-    return kv_fail(TC_ERR_CAPACITY, "tc_attend: a tree wants 1 to 4 words and at most 64 tokens a word");
+    return kv_fail(TC_ERR_CAPACITY, who, ": a tree wants 1 to 4 words and at most 64 tokens a word");
+  if (sh && (sh->groups < 1 || sh->groups > tokens->batch || !sh->cu_seqs || !sh->shared_lens))
+    return kv_fail(TC_ERR_INVALID_ARG, who, ": there must be 1 to batch groups, with cu_seqs and shared_lens");
   int64_t need = 0;
-  rc = tc_attend_workspace(kv, &need);
+  rc = sh ? tc_attend_shared_workspace(kv, tokens->n_tokens, a->q_heads, &need) : tc_attend_workspace(kv, &need);
   if (rc != TC_OK) return rc;
   if (!workspace || kv_misaligned(workspace, 16) || workspace_bytes < need)
-    return kv_fail(TC_ERR_CAPACITY, "tc_attend: the workspace is too small or not 16-byte aligned");
+    return kv_fail(TC_ERR_CAPACITY, who, ": the workspace is too small or not 16-byte aligned");
   const int64_t row = (int64_t)a->q_heads * kv->head_dim;
   if (tokens->n_tokens > 0 &&
       (!a->q || !a->out || kv_misaligned(a->q, 16) || kv_misaligned(a->out, 16) || a->q_stride % 8 != 0 ||
        a->out_stride % 8 != 0 || a->q_stride < row || a->out_stride < row))
-    return kv_fail(TC_ERR_INVALID_ARG,
-                   "tc_attend: q and out must be 16-byte aligned, with row strides that are multiples of 8 and hold "
-                   "a row");
+    return kv_fail(TC_ERR_INVALID_ARG, who,
+                   ": q and out must be 16-byte aligned, with row strides that are multiples of 8 and hold a row");
   KvDevice dev(kv->device);
-  if (!dev.ok) return kv_fail(TC_ERR_CUDA, "tc_attend: cannot use the cache's device");
+  if (!dev.ok) return kv_fail(TC_ERR_CUDA, who, ": cannot use the cache's device");
   // Keys and values of the layer: [page][keys or values, head][slot][element],
   const KvView v = kv_view(kv, layer);
   const cuuint64_t d = (cuuint64_t)kv->head_dim, sz = (cuuint64_t)kv->page_size;
@@ -1479,16 +1724,21 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   const cuuint64_t kv_strides[4] = {d * 2, 128, sz * d * 2, (cuuint64_t)2 * kv->kv_heads * sz * d * 2};
   const cuuint32_t kv_box[5] = {64, (cuuint32_t)kv->page_size, 1, 1, 1};
   const int group = a->q_heads / kv->kv_heads, tile_tokens = kTile / group;
-  // Queries: rows (token, head of the group) of one M tile, at most max_tokens of them.
-  const int q_tokens = a->max_tokens < 1 ? 1 : a->max_tokens < tile_tokens ? a->max_tokens : tile_tokens;
+  // Queries: rows (token, head of the group) of one M tile, at most max_tokens of them
+  // (of a prefix: of all sequences that share it).
+  const auto tokens_of = [&](int most) { return most < 1 ? 1 : most < tile_tokens ? most : tile_tokens; };
+  const int q_tokens = tokens_of(a->max_tokens), pq_tokens = tokens_of(tokens->n_tokens);
   const bool none = tokens->n_tokens == 0;  // (no queries: the map is not used, any valid one does)
   const cuuint64_t q_dims[3] = {d, (cuuint64_t)(none ? group : a->q_heads), (cuuint64_t)(none ? 1 : tokens->n_tokens)};
   const cuuint64_t q_strides[2] = {d * 2, (cuuint64_t)(none ? row : a->q_stride) * 2};
   const cuuint32_t q_box[3] = {64, (cuuint32_t)group, (cuuint32_t)q_tokens};
-  CUtensorMap map_kv, map_q;
+  const cuuint32_t pq_box[3] = {64, (cuuint32_t)group, (cuuint32_t)pq_tokens};
+  CUtensorMap map_kv, map_q, map_pq;
   if (!encode(&map_kv, kv->dtype, 5, v.base, kv_dims, kv_strides, kv_box) ||
-      !encode(&map_q, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, q_box))
-    return kv_fail(TC_ERR_UNSUPPORTED, "tc_attend: the sizes or strides do not fit a tensor map");
+      !encode(&map_q, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, q_box) ||
+      (sh && !encode(&map_pq, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, pq_box)))
+    return kv_fail(TC_ERR_UNSUPPORTED, who, ": the sizes or strides do not fit a tensor map");
+  if (!sh) map_pq = map_q;
   AttendParams p{};
   p.kv = v;
   p.tok = tokens_view(tokens);
@@ -1497,6 +1747,7 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   p.tile_tokens = tile_tokens;
   p.max_tokens = a->max_tokens;
   p.q_rows = group * q_tokens;
+  p.prefix_q_rows = group * pq_tokens;
   // A scale of zero weighs all slots alike; as a factor so small that every
   // product with a score is nothing, it keeps -inf times the factor -inf.
   p.c = fmaxf(fabsf(a->scale) * 1.4426950408889634f, 1e-30f);
@@ -1514,16 +1765,59 @@ extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens
   ws += part_rows(p.workers) * sizeof(float) * kv->head_dim;
   p.part_ml = reinterpret_cast<float2*>(ws);
   ws += part_rows(p.workers) * sizeof(float2);
-  p.descs = reinterpret_cast<Seg*>(ws);
-  ws += (size_t)p.workers * sizeof(Seg);
+  p.descs = reinterpret_cast<SharedSeg*>(ws);
+  ws += (size_t)p.workers * sizeof(SharedSeg);
   p.errs = reinterpret_cast<int32_t*>(ws);
+  if (sh) {
+    p.cu_seqs = sh->cu_seqs;
+    p.shared_lens = sh->shared_lens;
+    p.groups = sh->groups;
+    const size_t rows = 2 * (size_t)tokens->n_tokens * a->q_heads;
+    ws += ((size_t)p.workers * sizeof(int32_t) + 15) / 16 * 16;
+    ws += (128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127;
+    p.row_o = reinterpret_cast<float*>(ws);
+    p.row_ml = reinterpret_cast<float2*>(ws + rows * sizeof(float) * kv->head_dim);
+  }
   p.wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
   p.withhold = a->withhold;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (kv->dtype == TC_DT_BF16)
-    e = kv->head_dim == 128 ? launch<Bf16, 128>(p, map_kv, map_q, s) : launch<Bf16, 64>(p, map_kv, map_q, s);
-  else
-    e = kv->head_dim == 128 ? launch<F16, 128>(p, map_kv, map_q, s) : launch<F16, 64>(p, map_kv, map_q, s);
-  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_attend: ");
+  const cudaError_t e = sh ? launch<true>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, s)
+                           : launch<false>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, s);
+  return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, sh ? "tc_attend_shared: " : "tc_attend: ");
+}
+
+}  // namespace
+}  // namespace tcd
+
+using namespace tcd;
+
+extern "C" tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes) {
+  const tc_status rc = kv_check("tc_attend_workspace", kv);
+  if (rc != TC_OK) return rc;
+  if (!bytes) return kv_fail(TC_ERR_INVALID_ARG, "tc_attend_workspace: bytes is NULL");
+  const int sms = sm_count(kv->device);
+  if (sms < 1) return kv_fail(TC_ERR_CUDA, "tc_attend_workspace: no such device");
+  *bytes = (int64_t)workspace_bytes(sms, kv->head_dim);
+  return TC_OK;
+}
+
+extern "C" tc_status tc_attend_shared_workspace(const tc_kv_t* kv, int32_t n_tokens, int32_t q_heads, int64_t* bytes) {
+  const tc_status rc = tc_attend_workspace(kv, bytes);
+  if (rc != TC_OK) return rc;
+  if (n_tokens < 0 || q_heads < 1)
+    return kv_fail(TC_ERR_INVALID_ARG, "tc_attend_shared_workspace: n_tokens or q_heads out of range");
+  *bytes += (int64_t)shared_bytes((int64_t)n_tokens * q_heads, kv->head_dim);
+  return TC_OK;
+}
+
+extern "C" tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* a,
+                               void* workspace, int64_t workspace_bytes, int32_t* status, void* stream) {
+  return attend("tc_attend", kv, layer, tokens, a, nullptr, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" tc_status tc_attend_shared(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens,
+                                      const tc_attend_t* a, const tc_shared_t* shared, void* workspace,
+                                      int64_t workspace_bytes, int32_t* status, void* stream) {
+  if (!shared) return kv_fail(TC_ERR_INVALID_ARG, "tc_attend_shared: shared is NULL");
+  return attend("tc_attend_shared", kv, layer, tokens, a, shared, workspace, workspace_bytes, status, stream);
 }
