@@ -15,7 +15,9 @@ SIZES = [
     (15, 200, 127, 0), (16, 128, 128, 4), (17, 63, 65, 2), (33, 520, 300, 0), (64, 1024, 192, 16), (65, 72, 66, 0),
     (100, 333, 130, 5), (128, 256, 512, 0), (129, 320, 96, 0), (200, 4100, 70, 0), (255, 64, 257, 1),
     (256, 192, 100, 0), (257, 128, 128, 8), (300, 1000, 333, 0), (513, 96, 520, 4), (700, 640, 384, 0),
-    (1030, 200, 140, 1),
+    (1030, 200, 140, 1), (140, 2048, 132, 0), (190, 700, 1030, 0), (250, 3000, 1001, 0), (300, 2500, 600, 0),
+    (450, 1500, 257, 0), (600, 1300, 2050, 0), (900, 700, 4100, 0), (1300, 300, 5001, 0), (2100, 136, 9000, 0),
+    (2049, 400, 1999, 0),
 ]
 
 

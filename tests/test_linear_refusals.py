@@ -7,6 +7,9 @@ INVALID, CAPACITY, UNSUPPORTED = 1, 10, 11
 AT = 1 << 20   # (an address that is never read)
 
 
+CALL = ("n_tokens", "x", "x_stride", "residual", "residual_stride", "out", "out_stride", "wait_polls", "withhold")
+
+
 def layer(tcd, **kw):
     v = dict(device=0, dtype=0, in_features=64, out_features=32, weight=AT, weight_stride=64, gate=None, gate_stride=0,
              bias=None, gate_bias=None, act=0)
@@ -18,7 +21,7 @@ def call(tcd, **kw):
     v = dict(n_tokens=4, x=AT, x_stride=64, residual=None, residual_stride=0, out=AT, out_stride=32, wait_polls=0,
              withhold=0)
     v.update(kw)
-    return tcd._LinearCall(*[v[n] for n, _ in tcd._LinearCall._fields_])
+    return tcd._pack_call(*[v[n] or 0 for n in CALL])
 
 
 WEIGHTS = [
@@ -61,4 +64,9 @@ def test_no_tokens_is_no_launch(tcd):
 
 def test_structures_match_the_header(tcd):
     """Sizes of the C structures on a 64-bit host."""
-    assert ctypes.sizeof(tcd._LinearWeights) == 72 and ctypes.sizeof(tcd._LinearCall) == 72
+    assert ctypes.sizeof(tcd._LinearWeights) == 72
+    whole = type("Call", (ctypes.Structure,), {"_fields_": [
+        (n, ctypes.c_void_p if n in ("x", "residual", "out") else ctypes.c_int32 if n in ("n_tokens", "withhold") else
+         ctypes.c_int64) for n in CALL]})
+    c = whole.from_buffer_copy(tcd._pack_call(*range(1, 10)) + bytes(8))
+    assert [getattr(c, n) for n in CALL] == list(range(1, 10))

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -771,13 +772,9 @@ class _LinearWeights(ctypes.Structure):
                 ("gate_stride", ctypes.c_int64), ("bias", _vp), ("gate_bias", _vp), ("act", ctypes.c_int32)]
 
 
-class _LinearCall(ctypes.Structure):
-    _fields_ = [("n_tokens", ctypes.c_int32), ("x", _vp), ("x_stride", ctypes.c_int64), ("residual", _vp),
-                ("residual_stride", ctypes.c_int64), ("out", _vp), ("out_stride", ctypes.c_int64),
-                ("wait_polls", ctypes.c_int64), ("withhold", ctypes.c_int32)]
-
-
-_linear = _decl("tc_linear", ctypes.c_int, [ctypes.POINTER(_LinearWeights), ctypes.POINTER(_LinearCall), _vp, _vp])
+# (a call is packed into bytes: half of the time that a ctypes structure takes, and a call is microseconds long)
+_linear = _decl("tc_linear", ctypes.c_int, [ctypes.POINTER(_LinearWeights), ctypes.c_char_p, _vp, _vp])
+_pack_call = struct.Struct("@iPqPqPqqi").pack
 
 _words = {}    # per device: error words that are never freed (a captured call keeps its own), and how many are taken
 _words_lock = threading.Lock()
@@ -845,34 +842,40 @@ class Linear:
         self._word_at = self._word.data_ptr()
         index, raw = self.device.index, getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(index).cuda_stream)
+        self._index = index
         self._wait_test = (0, 0)
 
-    def _rows(self, t, n: int, features: int, what: str):
-        shape = t.shape
-        if len(shape) != 2 or shape[0] != n or shape[1] != features or t.dtype is not self.dtype or \
-                t.device != self.device:
-            raise ValueError(f"{what} must hold {n} rows of {features} {self.dtype} elements on {self.device}")
-        stride, step = t.stride()
-        if step != 1 and features > 1:
-            raise ValueError(f"{what} must have contiguous rows")
-        return t.data_ptr(), stride if n > 1 else features
+    def _refuse(self, t, n: int, features: int, what: str):
+        raise ValueError(f"{what} must hold {n} rows of {features} contiguous {self.dtype} elements on {self.device}")
 
     def apply(self, x, out, residual=None, status=None, stream=None):
         """tc_linear: x [n, in_features], out and residual [n, out_features] (rows may be slices of wider ones;
         residual may be out itself)."""
+        dtype, index, k, m = self.dtype, self._index, self.in_features, self.out_features
         n = x.shape[0]
-        at, stride = self._rows(x, n, self.in_features, "x")
-        call = _LinearCall(n, at, stride if n > 1 else self._x_stride,
-                           *((None, 0) if residual is None else self._rows(residual, n, self.out_features, "residual")),
-                           *self._rows(out, n, self.out_features, "out"), *self._wait_test)
+        # (the stride of a single row says nothing: torch keeps whatever it was)
+        if x.shape != (n, k) or x.dtype is not dtype or x.get_device() != index or (k > 1 and x.stride(1) != 1):
+            self._refuse(x, n, k, "x")
+        if out.shape != (n, m) or out.dtype is not dtype or out.get_device() != index or (m > 1 and out.stride(1) != 1):
+            self._refuse(out, n, m, "out")
+        r_at, r_stride = 0, 0
+        if residual is not None:
+            if residual.shape != (n, m) or residual.dtype is not dtype or residual.get_device() != index or \
+                    (m > 1 and residual.stride(1) != 1):
+                self._refuse(residual, n, m, "residual")
+            r_at, r_stride = residual.data_ptr(), residual.stride(0) if n > 1 else m
         if status is None:
             word = self._word_at
         else:
-            if status.dtype is not self._i32 or status.numel() != 1 or status.device != self.device:
+            if status.dtype is not self._i32 or status.numel() != 1 or status.get_device() != index:
                 raise ValueError(f"status must be an int32 tensor of one element on {self.device}")
             word = status.data_ptr()
         s = self._current() if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-        _check(_linear(self._layer_ref, call, word, s), "tc_linear")
+        code = _linear(self._layer_ref,
+                       _pack_call(n, x.data_ptr(), x.stride(0) if n > 1 else self._x_stride, r_at, r_stride,
+                                  out.data_ptr(), out.stride(0) if n > 1 else m, *self._wait_test), word, s)
+        if code != TC_OK:
+            raise TcError(code, "tc_linear")
 
     def wait_test(self, withhold: bool, wait_polls: int = 0):
         """Make the kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0) restores."""

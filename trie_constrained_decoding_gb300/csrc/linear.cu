@@ -21,7 +21,7 @@
 namespace tcd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kWeightBytes = 128 * kRowBytes;
 
@@ -52,65 +52,60 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// Four floats of CTA `rank`'s shared memory, at the place that `a` is in this one's.
-__device__ __forceinline__ float4 peer_float4(uint32_t a, uint32_t rank) {
-  uint32_t at;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
+// V floats of the shared memory of a CTA of the cluster.
+template <bool PEER>
+__device__ __forceinline__ void sums(uint32_t at, float (&v)[4]) {
+  if (PEER)
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(at)
+                 : "memory");
+  else
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+template <bool PEER>
+__device__ __forceinline__ void sums(uint32_t at, float (&v)[1]) {
+  if (PEER)
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[0]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(at) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  const float2 a = T::unpack(w.x), b = T::unpack(w.y);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+template <typename T>
+__device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[1]) {
+  v[0] = T::unpack(*p).x;
+}
+template <typename T>
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(T::pack(v[0], v[1]), T::pack(v[2], v[3]));
+}
+template <typename T>
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[1]) {
+  *p = (uint16_t)T::pack(v[0], 0.f);
 }
 
-template <typename T>
-__device__ __forceinline__ void finish4(const LinearParams& p, int64_t token, int f, float4 z4, float4 g4) {
-  const LinearOut& o = p.o;
-  float z[4] = {z4.x, z4.y, z4.z, z4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
-  const int n = min(4, o.features - f);
-  const uint16_t* res = o.residual ? o.residual + token * o.residual_stride + f : nullptr;
-  uint16_t* out = o.out + token * o.out_stride + f;
-  const bool wide = o.wide >= 4 && n == 4;
-  float r[4] = {0.f, 0.f, 0.f, 0.f};
-  if (res && wide) {
-    const uint2 v = *reinterpret_cast<const uint2*>(res);
-    const float2 a = T::unpack(v.x), b = T::unpack(v.y);
-    r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= n) continue;
-    if (res && !wide) r[i] = T::unpack(res[i]).x;
-    if (o.bias) z[i] += one<T>(o.bias + f + i);
-    if (p.gated) {
-      if (o.gate_bias) g[i] += one<T>(o.gate_bias + f + i);
-      z[i] *= activate(g[i], o.act);
-    } else {
-      z[i] = activate(z[i], o.act);
-    }
-    z[i] += r[i];
-  }
-  if (wide) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(T::pack(z[0], z[1]), T::pack(z[2], z[3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) out[i] = (uint16_t)T::pack(z[i], 0.f);
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+// V: features of a thread of the epilogue: four where rows are aligned, else one, so that a warp still writes whole pieces
+// of rows.
+template <typename T, int SPLIT, bool GATED, int V>
+__global__ void __launch_bounds__(kThreads, 2)
     linear_kernel(const LinearParams p, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_x) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ Hdr hdr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = p.split, rank = blockIdx.x % split, tile = blockIdx.x / split;
-  const int tok0 = tile % p.tok_tiles * p.tile, rows = p.gated ? 64 : 128;
+  const int rank = blockIdx.x % SPLIT, tile = blockIdx.x / SPLIT;
+  constexpr int rows = GATED ? 64 : 128;
+  const int tok0 = tile % p.tok_tiles * p.tile;
   const int f0 = tile / p.tok_tiles * rows;
-  const int kt0 = p.k_tiles * rank / split, n = p.k_tiles * (rank + 1) / split - kt0;
+  const int kt0 = p.k_tiles * rank / SPLIT, n = p.k_tiles * (rank + 1) / SPLIT - kt0;
   const int live = min(p.tile, p.o.n_tokens - tok0);
   const uint32_t stage_bytes = kWeightBytes + (uint32_t)p.tile * kRowBytes;
   // Tiles lie on 1024-byte boundaries.
@@ -133,11 +128,20 @@ __global__ void __launch_bounds__(kThreads)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // The setup above touches only this CTA; everything read or written from here on may belong to the kernel before.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  // The next kernel's CTAs may take the places of those that end: tensor memory is allocated, so that none of this
+  // kernel's CTAs can wait for it behind them.  The setup above touches only this CTA; everything read or written from
+  // here on may belong to the kernel before.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 0 && lane == 0)
+    // The first weights are on their way to L2 while the kernel before ends (L2 has what that one may still write).
+    for (int i = 0; i < min(n, stages); ++i) {
+      prefetch_tile(GATED ? &map_g : &map_w, (kt0 + i) * 64, f0);
+      prefetch_tile(&map_w, (kt0 + i) * 64, GATED ? f0 : f0 + 64);
+    }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = hdr.tmem;
 
   int armed = 0;
@@ -150,8 +154,8 @@ __global__ void __launch_bounds__(kThreads)
       bar_expect(bar, stage_bytes);
       const int k = (kt0 + armed) * 64;
       // (64 rows a copy: with a gate, its rows and then the weights')
-      load_tile(dst, p.gated ? &map_g : &map_w, k, f0, bar);
-      load_tile(dst + kWeightBytes / 2, &map_w, k, p.gated ? f0 : f0 + 64, bar);
+      load_tile(dst, GATED ? &map_g : &map_w, k, f0, bar);
+      load_tile(dst + kWeightBytes / 2, &map_w, k, GATED ? f0 : f0 + 64, bar);
       load_tile(dst + kWeightBytes, &map_x, k, tok0, bar);
     }
   } else if (warp == 1 && lane == 0) {
@@ -168,6 +172,30 @@ __global__ void __launch_bounds__(kThreads)
     commit(smem_at(&hdr.done));
   }
   __syncwarp();
+  // What a thread finishes: V features of every dt-th token.  Biases and the first residuals are fetched while the
+  // products run.
+  constexpr int kParts = rows / V, dt = SPLIT * kThreads / kParts;
+  constexpr int U = 16 / V / SPLIT ? 16 / V / SPLIT : 1;  // tokens at a time
+  const LinearOut& o = p.o;
+  const int part = tid % kParts, f = f0 + V * part;
+  const bool mine_is_out = f < o.features;  // (four features are all there, or none)
+  int t = rank * (kThreads / kParts) + tid / kParts;
+  float bias[V], gate_bias[V], res[U][V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    bias[j] = o.bias && mine_is_out ? one<T>(o.bias + f + j) : 0.f;
+    gate_bias[j] = GATED && o.gate_bias && mine_is_out ? one<T>(o.gate_bias + f + j) : 0.f;
+  }
+  const auto fetch = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) res[u][j] = 0.f;
+      if (o.residual && mine_is_out && t + u * dt < live)
+        load_row<T>(o.residual + (int64_t)(tok0 + t + u * dt) * o.residual_stride + f, res[u]);
+    }
+  };
+  fetch();
   // (after a wait that gave up as well: the issuer commits what it has issued)
   bool ok = bar_wait(smem_at(&hdr.done), 0, wl, abort);
   ok = __syncthreads_and(ok && !*abort);
@@ -182,18 +210,21 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   tmem_fence_after();
-  // This CTA's sums, [token][128 features], where the tiles were.
-  const uint32_t mine = at + (uint32_t)(warp * 32 + lane) * 4;
+  // This CTA's sums, [token][128 features], where the tiles were: a warp has a quarter of the features and half of the
+  // tokens.
+  const int quarter = warp & 3;
+  const uint32_t mine = at + (uint32_t)(quarter * 32 + lane) * 4;
+  const int cut = (live + 31) / 32 * 16, c1 = warp < 4 ? min(cut, live) : live;
 #pragma unroll 1
-  for (int c = 0; c < live; c += 16) {
+  for (int c = warp < 4 ? 0 : cut; c < c1; c += 16) {
     uint32_t v[16];
-    tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+    tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
 #pragma unroll
     for (int j = 0; j < 16; ++j)
-      if (c + j < live) asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (c + j) * 512), "r"(v[j]) : "memory");
+      if (c + j < c1) asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (c + j) * 512), "r"(v[j]) : "memory");
   }
   tmem_fence_before();
-  if (split > 1)
+  if (SPLIT > 1)
     cluster_sync();
   else
     __syncthreads();
@@ -201,24 +232,48 @@ __global__ void __launch_bounds__(kThreads)
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
   }
-  // Four features of a token at a time, shared out over the cluster.
-  const int shift = p.gated ? 4 : 5;
-  for (int u = rank * kThreads + tid; u < live << shift; u += split * kThreads) {
-    const int t = u >> shift, q = u & ((1 << shift) - 1);
-    if (f0 + 4 * q >= p.o.features) continue;
-    const uint32_t src = at + t * 512 + q * 16;
-    float4 z = make_float4(0.f, 0.f, 0.f, 0.f), g = z;
-    for (int r = 0; r < split; ++r) {
-      const float4 v = peer_float4(p.gated ? src + 256 : src, r);
-      z.x += v.x, z.y += v.y, z.z += v.z, z.w += v.w;
-      if (p.gated) {
-        const float4 w = peer_float4(src, r);
-        g.x += w.x, g.y += w.y, g.z += w.z, g.w += w.w;
-      }
-    }
-    finish4<T>(p, tok0 + t, f0 + 4 * q, z, g);
+  uint32_t peer[SPLIT];
+#pragma unroll
+  for (int r = 0; r < SPLIT; ++r) {
+    peer[r] = at + part * V * 4;
+    if (SPLIT > 1) asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(peer[r]) : "r"(r));
   }
-  if (split > 1) cluster_sync();  // (the others have read this CTA's sums)
+  if (mine_is_out) {
+#pragma unroll 1
+    while (t < live) {
+      float z[U][SPLIT][V], g[U][SPLIT][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r) {
+          const int at_t = min(t + u * dt, live - 1) * 512;
+          sums<(SPLIT > 1)>(peer[r] + at_t + (GATED ? 256 : 0), z[u][r]);
+          if (GATED) sums<(SPLIT > 1)>(peer[r] + at_t, g[u][r]);
+        }
+      with_act(o.act, [&](auto act) {
+        constexpr int kAct = decltype(act)::kAct;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float y[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            float a = z[u][0][j], b = GATED ? g[u][0][j] : 0.f;
+#pragma unroll
+            for (int r = 1; r < SPLIT; ++r) {
+              a += z[u][r][j];
+              if (GATED) b += g[u][r][j];
+            }
+            a += bias[j];
+            y[j] = (GATED ? a * activate(b + gate_bias[j], kAct) : activate(a, kAct)) + res[u][j];
+          }
+          if (t + u * dt < live) store_row<T>(o.out + (int64_t)(tok0 + t + u * dt) * o.out_stride + f, y);
+        }
+      });
+      t += U * dt;
+      if (t < live) fetch();
+    }
+  }
+  if (SPLIT > 1) cluster_sync();  // (the others have read this CTA's sums)
 }
 
 // --------------------------------------------------------------------- host
@@ -248,11 +303,10 @@ bool encode(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t r
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMaxDevices = 64;
 constexpr size_t kSmemHalf = 112 * 1024, kSmemWhole = 224 * 1024;  // two CTAs an SM, or one
 
 int sm_count(int device) {
-  static int known[kMaxDevices];  // (a race writes the same value)
+  static int known[kLinearDevices];  // (a race writes the same value)
   if (!known[device]) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
@@ -264,13 +318,13 @@ int sm_count(int device) {
   return known[device];
 }
 
-template <typename T>
+template <typename T, int SPLIT, bool GATED, int V>
 cudaError_t launch(const LinearParams& p, int device, unsigned grid, size_t smem, const CUtensorMap& w,
                    const CUtensorMap& g, const CUtensorMap& x, cudaStream_t s) {
-  static bool ready[kMaxDevices];
+  const auto kernel = linear_kernel<T, SPLIT, GATED, V>;
+  static bool ready[kLinearDevices];
   if (!ready[device]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(linear_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemWhole);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemWhole);
     if (e != cudaSuccess) return e;
     ready[device] = true;
   }
@@ -278,16 +332,96 @@ cudaError_t launch(const LinearParams& p, int device, unsigned grid, size_t smem
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.split;
+  attr[1].val.clusterDim.x = SPLIT;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = SPLIT > 1 ? 2 : 1;
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<T>, p, w, g, x);
+  return cudaLaunchKernelEx(&cfg, kernel, p, w, g, x);
+}
+
+template <typename T, bool GATED, int V>
+cudaError_t launch_split(const LinearParams& p, int device, unsigned grid, size_t smem, const CUtensorMap& w,
+                         const CUtensorMap& g, const CUtensorMap& x, cudaStream_t s) {
+  switch (p.split) {
+    case 2: return launch<T, 2, GATED, V>(p, device, grid, smem, w, g, x, s);
+    case 4: return launch<T, 4, GATED, V>(p, device, grid, smem, w, g, x, s);
+    case 8: return launch<T, 8, GATED, V>(p, device, grid, smem, w, g, x, s);
+    default: return launch<T, 1, GATED, V>(p, device, grid, smem, w, g, x, s);
+  }
+}
+
+template <typename T>
+cudaError_t launch_few(const LinearParams& p, int device, unsigned grid, size_t smem, const CUtensorMap& w,
+                       const CUtensorMap& g, const CUtensorMap& x, cudaStream_t s) {
+  if (p.gated)
+    return p.o.wide > 1 ? launch_split<T, true, 4>(p, device, grid, smem, w, g, x, s)
+                        : launch_split<T, true, 1>(p, device, grid, smem, w, g, x, s);
+  return p.o.wide > 1 ? launch_split<T, false, 4>(p, device, grid, smem, w, g, x, s)
+                      : launch_split<T, false, 1>(p, device, grid, smem, w, g, x, s);
+}
+
+// How a call is computed, and about how long it takes.
+//
+// Up to 128 tokens are one tile (pairs were never more than 4 % faster there).  More take the way with the lowest estimate.
+// The estimates' constants are a fit to 209 calls (in_features 304 to 14336, out_features 500 to 14336, with and without
+// a gate, 1 to 4000 tokens, each measured in all four ways): the way that they choose took 1.2 % longer than the best of
+// the four on average and 16 % at most.  A few of those calls, in us, as tokens of a tile 256 / 128 / pairs with 128 rows of
+// the weights a CTA / 64:
+//   4096 x 6144, 256 tokens     24.2 / 21.9 / 25.8 / 24.1       14336 x 4096, 512 tokens    50.9 / 54.4 / 71.0 / 69.8
+//   1000 x 2731, 512 tokens     15.8 / 14.6 / 14.8 / 11.2       4096 x 14336 gated, 512     89.2 / 93.8 / 72.5 / 117.4
+struct Plan {
+  double ns;
+  bool many;         // linear_pair.cu
+  int tile, tok_tiles, split;
+  int64_t grid;      // CTAs, or pairs
+};
+
+// Bytes of the weights at 6 TB/s.
+double weights_ns(const tc_linear_t& l) {
+  return (l.gate ? 4. : 2.) * l.in_features * l.out_features / 6000.;
+}
+
+// Tiles of up to `cap` tokens, of about the same size each.  Tiles of 128 leave room for two CTAs an SM, larger ones for
+// one.  The sums are cut while that keeps everything resident at once and each part has two steps or more; in clusters
+// of at most four where a CTA takes a whole SM (of eight, some had to wait for the others: 256 tokens of 2048 x 2048
+// 17.8 us instead of 10.3).
+Plan plan_few(const tc_linear_t& l, int n_tokens, int cap, int sms, bool wide) {
+  Plan r{};
+  r.tok_tiles = (n_tokens + cap - 1) / cap;
+  r.tile = ((n_tokens + r.tok_tiles - 1) / r.tok_tiles + 15) / 16 * 16;
+  const bool alone = r.tile > 128;
+  const int k_tiles = (l.in_features + 63) / 64, rows = l.gate ? 64 : 128;
+  const int64_t tiles = (int64_t)((l.out_features + rows - 1) / rows) * r.tok_tiles;
+  r.split = 1;
+  while (r.split < (alone ? 4 : 8) && tiles * r.split * 2 <= (alone ? sms : 2 * sms) && k_tiles >= r.split * 4)
+    r.split *= 2;
+  r.grid = tiles * r.split;
+  const double turns = (double)((r.grid + sms - 1) / sms);
+  const double products = turns * ((k_tiles + r.split - 1) / r.split) * (60. + 1.5 * r.tile);
+  r.ns = 5500. + (products > weights_ns(l) ? products : weights_ns(l)) + (wide ? 18. : 43.) * r.tile / r.split * turns;
+  return r;
+}
+
+Plan plan_many(const tc_linear_t& l, int n_tokens, int rows, int sms) {
+  Plan r{};
+  r.many = true;
+  r.tile = rows;
+  r.split = 1;
+  r.tok_tiles = (n_tokens + 255) / 256;
+  const int features = l.gate ? rows : 2 * rows, pairs = sms / 2 > 0 ? sms / 2 : 1;
+  const int64_t tiles = (int64_t)((l.out_features + features - 1) / features) * r.tok_tiles;
+  r.grid = tiles < pairs ? tiles : pairs;
+  const double products =
+      (double)((tiles + pairs - 1) / pairs) * ((l.in_features + 63) / 64) * (rows == 128 ? 333. : 310.);
+  r.ns = 3000. + (products > weights_ns(l) ? products : weights_ns(l)) + 29. * rows;
+  // (tiles are counted in 32 bits there)
+  if (tiles > INT32_MAX / 2) r.grid = tiles;
+  return r;
 }
 
 }  // namespace
@@ -297,7 +431,7 @@ using namespace tcd;
 
 extern "C" tc_status tc_linear(const tc_linear_t* l, const tc_linear_call_t* c, int32_t* status, void* stream) {
   if (!l || !c || !status) return fail_with(TC_ERR_INVALID_ARG, "tc_linear: an argument is NULL");
-  if (l->device < 0 || l->device >= kMaxDevices || l->in_features < 1 || l->out_features < 1 || c->n_tokens < 0 ||
+  if (l->device < 0 || l->device >= kLinearDevices || l->in_features < 1 || l->out_features < 1 || c->n_tokens < 0 ||
       l->act < TC_ACT_NONE || l->act > TC_ACT_GELU_TANH)
     return fail_with(TC_ERR_INVALID_ARG, "tc_linear: a size, the device or the activation is out of range");
   if (l->dtype != TC_DT_BF16 && l->dtype != TC_DT_F16)
@@ -334,41 +468,48 @@ extern "C" tc_status tc_linear(const tc_linear_t* l, const tc_linear_call_t* c, 
   p.o.n_tokens = c->n_tokens;
   p.o.features = l->out_features;
   p.o.act = l->act;
-  const auto aligned = [&](int elements) {
-    return !kv_misaligned(c->out, 2 * elements) && c->out_stride % elements == 0 &&
-           (!c->residual || (!kv_misaligned(c->residual, 2 * elements) && c->residual_stride % elements == 0));
-  };
-  p.o.wide = aligned(16) ? 16 : aligned(4) ? 4 : 1;
+  p.o.wide = l->out_features % 4 == 0 && !kv_misaligned(c->out, 8) && c->out_stride % 4 == 0 &&
+                     (!c->residual || (!kv_misaligned(c->residual, 8) && c->residual_stride % 4 == 0))
+                 ? 4
+                 : 1;
   p.k_tiles = (l->in_features + 63) / 64;
   p.gated = l->gate != nullptr;
   p.status = status;
   p.wait_limit = c->wait_polls > 0 ? (int32_t)(c->wait_polls < 1 << 30 ? c->wait_polls : 1 << 30) : kLinearWaitLimit;
   p.withhold = c->withhold;
 
-  p.tile = c->n_tokens >= 256 ? 256 : (c->n_tokens + 15) / 16 * 16;
-  p.tok_tiles = (c->n_tokens + p.tile - 1) / p.tile;
-  p.tmem_cols = 32;
-  while (p.tmem_cols < p.tile) p.tmem_cols *= 2;
-  const int rows = p.gated ? 64 : 128;
-  const int64_t tiles = (int64_t)((l->out_features + rows - 1) / rows) * p.tok_tiles;
+  Plan plan = plan_few(*l, c->n_tokens, 256, sms, p.o.wide > 1);
+  if (c->n_tokens > 128)
+    for (const Plan& other : {plan_few(*l, c->n_tokens, 128, sms, p.o.wide > 1), plan_many(*l, c->n_tokens, 128, sms),
+                              plan_many(*l, c->n_tokens, 64, sms)})
+      if (other.ns < plan.ns) plan = other;
+  if (plan.grid > INT32_MAX / 2) return fail_with(TC_ERR_CAPACITY, "tc_linear: the output has too many tiles");
+  p.tile = plan.tile;
+  p.tok_tiles = plan.tok_tiles;
+  p.split = plan.split;
   const size_t stage = kWeightBytes + (size_t)p.tile * kRowBytes;
-  const size_t room = p.tile > 128 ? kSmemWhole : kSmemHalf;
-  p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= (p.tile > 128 ? sms : 2 * sms) && p.k_tiles >= p.split * 2 * 2) p.split *= 2;
-  p.stages = (int)((room - 1024) / stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int64_t grid = tiles * p.split;
-  if (grid > INT32_MAX) return fail_with(TC_ERR_CAPACITY, "tc_linear: the output has too many tiles");
+  if (!plan.many) {
+    p.tmem_cols = 32;
+    while (p.tmem_cols < p.tile) p.tmem_cols *= 2;
+    p.stages = (int)(((p.tile > 128 ? kSmemWhole : kSmemHalf) - 1024) / stage);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+  }
+  const int w_box = plan.many ? plan.tile : 64, x_box = plan.many ? 128 : plan.tile;
 
   CUtensorMap w, g, x;
-  if (!encode(&w, l->dtype, l->weight, l->in_features, l->out_features, l->weight_stride, 64) ||
-      (l->gate && !encode(&g, l->dtype, l->gate, l->in_features, l->out_features, l->gate_stride, 64)) ||
-      !encode(&x, l->dtype, c->x, l->in_features, c->n_tokens, c->x_stride, p.tile))
+  if (!encode(&w, l->dtype, l->weight, l->in_features, l->out_features, l->weight_stride, w_box) ||
+      (l->gate && !encode(&g, l->dtype, l->gate, l->in_features, l->out_features, l->gate_stride, w_box)) ||
+      !encode(&x, l->dtype, c->x, l->in_features, c->n_tokens, c->x_stride, x_box))
     return fail_with(TC_ERR_UNSUPPORTED, "tc_linear: the sizes or strides do not fit a tensor map");
   if (!l->gate) g = w;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t smem = 1024 + p.stages * stage;
-  const cudaError_t e = l->dtype == TC_DT_BF16 ? launch<Bf16>(p, l->device, (unsigned)grid, smem, w, g, x, s)
-                                               : launch<F16>(p, l->device, (unsigned)grid, smem, w, g, x, s);
+  cudaError_t e;
+  if (plan.many) {
+    e = launch_linear_pair(p, l->device, l->dtype, (int)plan.grid, w, g, x, s);
+  } else {
+    const size_t smem = 1024 + p.stages * stage;
+    e = l->dtype == TC_DT_BF16 ? launch_few<Bf16>(p, l->device, (unsigned)plan.grid, smem, w, g, x, s)
+                               : launch_few<F16>(p, l->device, (unsigned)plan.grid, smem, w, g, x, s);
+  }
   return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, "tc_linear: ");
 }

@@ -18,7 +18,7 @@ struct LinearOut {
   int64_t residual_stride, out_stride;
   int32_t n_tokens, features;
   int32_t act;
-  int32_t wide;  // elements that an aligned access of rows may have (1, 4 or 16)
+  int32_t wide;  // elements that an access of rows may have: four where all rows are aligned and whole fours, else one
 };
 
 struct LinearParams {
@@ -28,14 +28,15 @@ struct LinearParams {
   int32_t* status;
   int32_t wait_limit;  // polls of one wait before it gives up
   int32_t withhold;    // test switch: the first load is left out
-  // few tokens (linear.cu)
-  int32_t tile;        // tokens of a tile
+  int32_t tile;        // tokens of a tile; linear_pair.cu: rows of the weights that a CTA loads
   int32_t tok_tiles;
+  // few tokens (linear.cu)
   int32_t split;       // CTAs of a cluster, which share out a sum
   int32_t stages;
   int32_t tmem_cols;
 };
 
+constexpr int kLinearDevices = 64;
 constexpr uint32_t kRowBytes = 128;         // 64 elements of a step: one row of the 128-byte swizzle
 constexpr int kLinearWaitLimit = 1 << 22;
 
@@ -77,6 +78,9 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
@@ -107,8 +111,19 @@ __device__ __forceinline__ float activate(float z, int act) {
       return z < 0.f ? 0.f : z;  // (NaN stays)
     case TC_ACT_SILU:
       return __fdividef(z, 1.f + __expf(-z));
-    case TC_ACT_GELU:
-      return 0.5f * z * erfcf(z * -0.70710678f);
+    case TC_ACT_GELU: {
+      // max(z, 0) - a / 2 erfc(a / sqrt 2), a = |z|, with erfc(x) = t exp(-x^2) P(t), t = 1 / (1 + 0.45 x): P is a
+      // least-squares fit whose relative error was levelled out over x = 0 ... 14 (3.6e-7, 3 units of 2^-23).
+      const float a = fminf(fabsf(z), 30.f), t = __fdividef(1.f, fmaf(a, 0.3181980515f, 1.f));
+      float p = fmaf(t, 0.06890339404f, -0.24888466299f);
+      p = fmaf(t, p, 0.22390307486f);
+      p = fmaf(t, p, 0.02623970434f);
+      p = fmaf(t, p, 0.19616602361f);
+      p = fmaf(t, p, 0.22578363121f);
+      p = fmaf(t, p, 0.25400400162f);
+      p = fmaf(t, p, 0.25388520956f);
+      return (z < 0.f ? 0.f : z) - 0.5f * a * (t * p) * exp2f(a * a * -0.7213475204f);
+    }
     case TC_ACT_GELU_TANH: {
       // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
       const float u = z * fmaf(0.044715f * z, z, 1.f) * -1.5957691216f;
@@ -118,5 +133,26 @@ __device__ __forceinline__ float activate(float z, int act) {
       return z;
   }
 }
+
+// Calls f with the activation as a constant.  (Around a loop of finished sums: inside of it each turn of an unrolled
+// loop would have code for every activation, and small calls are bound by the fetch of their instructions.)
+template <int A>
+struct Act {
+  static constexpr int kAct = A;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case TC_ACT_RELU: return f(Act<TC_ACT_RELU>());
+    case TC_ACT_SILU: return f(Act<TC_ACT_SILU>());
+    case TC_ACT_GELU: return f(Act<TC_ACT_GELU>());
+    case TC_ACT_GELU_TANH: return f(Act<TC_ACT_GELU_TANH>());
+    default: return f(Act<TC_ACT_NONE>());
+  }
+}
+
+// Many tokens, on pairs of SMs (linear_pair.cu).
+cudaError_t launch_linear_pair(const LinearParams& p, int device, int dtype, int pairs, const CUtensorMap& w,
+                               const CUtensorMap& g, const CUtensorMap& x, cudaStream_t s);
 
 }  // namespace tcd
