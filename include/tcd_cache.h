@@ -222,7 +222,7 @@ tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes);
  *               than its group shares, gets TC_ERR_BOUNDS, and so does a whole
  *               group whose length is out of range.
  *  workspace    (device) tc_attend_shared_workspace bytes for this number of
- *               tokens and heads (those of tc_attend, and two results of
+ *               tokens and heads (those of tc_attend, and about two results of
  *               head_dim + 2 floats for each token and query head).
  */
 typedef struct tc_shared_t {

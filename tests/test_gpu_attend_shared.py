@@ -96,6 +96,13 @@ CASES = [
     ([1] * 130, [7] * 130, [(0, 65, 256), (65, 130, 2000)], 3, 1, 64, 128, "bf16"),
     ([3, 2], [70, 1], [(0, 2, 48)], 128, 1, 64, 16, "bf16"),
     ([2, 3], [9, 0], [(0, 2, 129)], 100, 1, 128, 16, "f16"),
+    # rests that are just short enough for a kernel of their own, and just too long or with too many rows
+    ([1, 1, 1, 1], [1023, 1024, 1022, 0], [(0, 4, 64)], 2, 1, 64, 32, "bf16"),
+    ([16, 17, 15, 1], [60, 60, 1009, 1023], [(0, 4, 64)], 8, 2, 128, 64, "bf16"),
+    ([4, 3, 1, 2], [63, 64, 65, 129], [(0, 4, 128)], 4, 1, 128, 64, "f16"),
+    ([8, 5, 1, 7], [64, 59, 127, 1], [(0, 4, 128)], 4, 1, 64, 16, "f16"),
+    ([16, 11, 1, 13], [48, 500, 63, 0], [(0, 4, 96)], 4, 1, 128, 32, "bf16"),
+    ([64, 64], [0, 960], [(0, 2, 16)], 3, 3, 64, 16, "bf16"),
 ]
 
 
@@ -125,6 +132,125 @@ def test_drafts(tcd, case):
     masks = [m for n in w.tokens for m in ancestors(random_parents(w.rng, n))]
     out, lse = w.attend(q, masks, lse=True)
     w.check(kv, q64, out, masks, lse=lse)
+
+
+# Many sequences at once (more items than the GPU has SMs): heads of a group, kv_heads, head_dim, page, type, most tokens
+MANY = [
+    (4, 2, 128, 64, "bf16", 1), (4, 2, 128, 16, "f16", 16), (1, 2, 64, 128, "bf16", 64), (7, 2, 64, 32, "f16", 9),
+    (16, 2, 128, 128, "bf16", 4), (3, 2, 64, 16, "bf16", 21), (64, 2, 128, 32, "f16", 1), (2, 2, 128, 64, "bf16", 40),
+    (70, 2, 64, 64, "bf16", 2),
+]
+
+
+def many(tcd, case, seed):
+    """100 sequences in three groups (the last seven in none): no token to more than a short rest may have, nothing of
+    their own to more slots than that."""
+    group, hkv, d, page, dt, most = MANY[case]
+    rng = np.random.default_rng(seed)
+    tokens = rng.integers(0, most + 1, 100)
+    tokens[:8] = [1, most, 0, 1, most, 1, 1, max(1, 64 // group)]
+    behind = rng.integers(0, 260, 100)
+    behind[:8] = [0, 64 - min(most, 64), 5, 63, 64, 1024, 1023, 700]
+    groups = [(0, 40, 130), (40, 41, 300), (41, 93, 3 * page + 1)]
+    ctx = behind + np.repeat([g[2] for g in groups] + [0], [40, 1, 52, 7])
+    return Groups(tcd, [int(x) for x in tokens], [int(x) for x in ctx], groups, dt, hkv, d, page, seed), group * hkv
+
+
+@pytest.mark.parametrize("drafts", [False, True])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_sequences(tcd, case, drafts):
+    w, hq = many(tcd, case, 60 + case)
+    kv = w.fill()
+    q, q64 = w.normal(w.n, hq, w.head_dim)
+    words = -(-max(w.tokens) // 64)
+    masks = [m for n in w.tokens for m in ancestors(random_parents(w.rng, n))] if drafts else None
+    out, lse = w.attend(q, masks, words, lse=True)
+    w.check(kv, q64, out, masks, lse=lse, rows=[0, 1, 2, 7, 15, 20, 39, 63])
+
+
+def test_many_sequences_with_values_that_are_not_finite(tcd):
+    """Infinities and NaN in drafted values of many sequences: to the rows that see them, and to no other."""
+    torch = torch_mod()
+    for case in (1, 7):
+        w, hq = many(tcd, case, 3)
+        w.fill()
+        q, _ = w.normal(w.n, hq, w.head_dim)
+        masks = [m for n in w.tokens for m in ancestors(random_parents(w.rng, n))]
+        want = w.attend(q, masks)[0].clone()
+        plus, nan = torch.zeros_like(want, dtype=torch.bool), torch.zeros_like(want, dtype=torch.bool)
+        group = hq // w.kv_heads
+        for b, n in enumerate(w.tokens):
+            if n < 2 or b % 3:
+                continue
+            for x, column, value, to in ((n - 1, 5, float("inf"), plus), (n // 2, 9, float("nan"), nan)):
+                page, off = w.slots(b, w.ctx_list[b] + x, w.ctx_list[b] + x + 1)
+                w.pool[0, int(page[0]), 1, 1, int(off[0]), column] = value
+                for i in range(n):
+                    if masks[w.cu_host[b] + i] >> x & 1:
+                        to[w.cu_host[b] + i, group:, column] = True
+        out = w.attend(q, masks)[0]
+        keep = ~(plus | nan)
+        assert torch.equal(out[keep], want[keep])
+        assert bool((out[plus] == float("inf")).all()) and bool(out[nan].isnan().all())
+
+
+def test_many_sequences_in_graphs_and_out_of_them(tcd):
+    """The same bits each time, in a graph that is replayed beside plain calls on another stream."""
+    torch = torch_mod()
+    w, hq = many(tcd, 1, 5)
+    w.fill()
+    q, _ = w.normal(w.n, hq, w.head_dim)
+    want = w.attend(q)[0].clone()
+    for _ in range(3):
+        assert torch.equal(w.attend(q)[0], want)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = torch.zeros_like(want), torch.zeros_like(want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w.attend(q, out=a, status=None)
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            g.replay()
+        w.attend(q, out=b, status=None, stream=t)
+    w.cache.raise_on_error()
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
+def test_many_sequences_with_errors(tcd):
+    """Errors of single sequences among many; a wait that runs out; and the next call is right."""
+    torch = torch_mod()
+    w, hq = many(tcd, 0, 6)
+    kv = w.fill()
+    q, q64 = w.normal(w.n, hq, w.head_dim)
+    good = w.attend(q)[0].clone()
+    w.check(kv, q64, good)
+    w.ctx[3] = 10                                   # its group shares 128
+    w.table[4, 0] = w.table[6, 4]                   # a valid page, but another one
+    w.table[9, -1] = -5                             # (not read)
+    w.table[5, 2] = 1 << 20                         # a page that does not exist, behind the prefix
+    out, _ = w.attend(q)
+    assert [i for i, c in enumerate(w.status.tolist()) if c] == [3, 4, 5]
+    w.check(kv, q64, out, skip=(3, 4, 5))
+    w, hq = many(tcd, 0, 6)
+    w.fill()
+    w.cache.attend_wait_test(True, 2000)
+    w.attend(q)
+    assert tcd.TC_ERR_DEVICE_TIMEOUT in w.status.tolist()
+    w.cache.attend_wait_test(False, 0)
+    kv = w.fill()
+    out, _ = w.attend(q)
+    assert w.status.tolist() == [0] * 100
+    w.check(kv, q64, out)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_many_sequences_scales(tcd, scale):
+    w, hq = many(tcd, 3, 7)
+    kv = w.fill()
+    q, q64 = w.normal(w.n, hq, w.head_dim)
+    out, lse = w.attend(q, lse=True, scale=scale)
+    w.check(kv, q64, out, lse=lse, scale=scale, rows=[0, 3, 8])
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
@@ -192,6 +318,27 @@ def test_garbage_beside_the_slots_seen(tcd):
     out = w.attend(q, masks)[0]
     keep = [0, 2, 3, 4, 5, 6]
     assert torch.equal(out[keep], want[keep]) and bool(out[1].isnan().all())
+
+
+@pytest.mark.parametrize("hq", [1, 6, 15])
+def test_infinite_values(tcd, hq):
+    """An infinity among the drafted values reaches the rows that see it, unchanged, and no other row; and so does one
+    behind it that another part of the rows' slots holds."""
+    torch = torch_mod()
+    for dt, d in (("bf16", 64), ("f16", 128)):
+        w = Groups(tcd, [4, 3], [150, 33], [(0, 2, 32)], dt, 1, d, seed=4)
+        w.fill()
+        q, _ = w.normal(w.n, hq, d)
+        masks = [1, 2, 5, 8, 1, 2, 4]
+        want = w.attend(q, masks)[0].clone()
+        page, off = w.slots(0, 152, 153)              # draft 2 of sequence 0: its own row alone sees it
+        w.pool[0, int(page[0]), 1, 0, int(off[0]), 3] = float("inf")
+        w.pool[0, int(page[0]), 1, 0, int(off[0]), 5] = float("-inf")
+        out = w.attend(q, masks)[0]
+        inf = torch.zeros_like(out, dtype=torch.bool)
+        inf[2, :, 3], inf[2, :, 5] = True, True
+        assert torch.equal(out[~inf], want[~inf])
+        assert bool((out[2, :, 3] == float("inf")).all()) and bool((out[2, :, 5] == -float("inf")).all())
 
 
 def test_rows_of_no_sequence_are_left(tcd):

@@ -528,6 +528,7 @@ class KvCache:
         _check(_attend_workspace(self._kvp, ctypes.byref(need)), "tc_attend_workspace")
         self.workspace_bytes = need.value
         self._wait_test = (0, 0)
+        self._shared_need = {}               # workspace_bytes of attend_shared by tokens and heads
         self._own = {}                       # _Own per stream
         self._captured, self._graph_codes = {}, None   # _Own per capture and stream; their common codes
         self._capture = ctypes.c_uint64()
@@ -656,7 +657,10 @@ class KvCache:
         s = self._stream(stream)
         own = None if workspace is not None else self._buffers(s)
         kv, codes = self._codes(status, t.batch, s, own=own)
-        need = self.shared_workspace_bytes(t.n_tokens, a.q_heads)
+        sizes = t.n_tokens, a.q_heads
+        need = self._shared_need.get(sizes)
+        if need is None:
+            need = self._shared_need[sizes] = self.shared_workspace_bytes(*sizes)
         _check(_attend_shared(kv, layer, t, a, g, *self._workspace(workspace, s, own, need), codes, s),
                "tc_attend_shared")
 

@@ -139,6 +139,8 @@ struct Seg {
 // What an item of a call with common prefixes (SH) is: a sequence that shares nothing,
 // a group's prefix, the rest of one of its sequences.
 enum { kWhole = 0, kPrefix = 1, kRest = 2 };
+// In row_short.  (kBegun: in an item's first row only; it stays where a wait ran out.)
+enum { kLong = 0, kDone = 1, kBegun = 2 };
 struct SharedSeg : Seg {
   int32_t kind;
   int64_t pages;     // where the item's page ids begin in the table
@@ -173,8 +175,13 @@ struct AttendParams {
   const int32_t* shared_lens;
   int32_t groups;
   int32_t prefix_q_rows;  // rows of one query load of a prefix
-  float* row_o;      // [prefix or rest][token, head][D] results before they are joined,
-  float2* row_ml;    // [prefix or rest][token, head] and their maxima and sums
+  int32_t rest_q_rows;    // and of a short rest
+  int32_t rest_items;     // items of attend_rest_kernel; 0: it is not used
+  // Results of rows before they are joined, by key-value head, of the prefix and of the rest.  (Columns in fours outside:
+  // the threads of a warp have neighbouring rows.)
+  float* row_o;        // [prefix or rest][kv_head][D / 4][row][4]
+  float2* row_ml;      // [prefix or rest][kv_head][row] maxima and sums
+  int32_t* row_short;  // [kv_head][row] whether what the row's sequence has for itself is attend_rest_kernel's, and there
 };
 
 constexpr int kMisfit = 2;  // in errs: the groups do not ascend
@@ -512,6 +519,9 @@ __device__ __forceinline__ int prefix_of(const AttendParams& p, int g) {
   return __ldg(p.cu_seqs + g + 1) - __ldg(p.cu_seqs + g) < 2 ? 0 : len & -p.kv.page_size;
 }
 
+// What a sequence has for itself is short (attend_rest_kernel) up to so many rows (tokens and heads of a group) and slots.
+constexpr int kRestRows = 64, kRestSlots = 1024;
+
 // A line of the work: a sequence, or (SH: there are groups with a common prefix) first
 // each group's prefix, then what each sequence has for itself.
 struct Span : SeqSpan {
@@ -531,6 +541,19 @@ __device__ __forceinline__ void set_line(const AttendParams& p, const Span& s, i
   l->extra = extra;
   l->prefix = SH && s.kind == kPrefix;
 }
+// Sequence b without what its group shares.
+__device__ __forceinline__ bool rest_of(const AttendParams& p, int b, Span* s) {
+  bool ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
+  const int g = group_of(p, b), len = g < 0 ? 0 : prefix_of(p, g);
+  ok = ok && len >= 0 && len <= s->ctx;
+  s->kind = len > 0 ? kRest : kWhole;
+  s->pages = (int64_t)b * p.tok.width + (len >> p.kv.page_shift);
+  s->ctx -= len;
+  return ok;
+}
+__device__ __forceinline__ bool is_short(const AttendParams& p, const Span& s) {
+  return p.rest_items > 0 && s.kind == kRest && (int64_t)s.n * p.group <= kRestRows && (int64_t)s.ctx + s.n <= kRestSlots;
+}
 template <bool SH>
 __device__ __forceinline__ bool line_of(const AttendParams& p, int v, int extra, Span* s, Line* l) {
   if constexpr (SH) {
@@ -548,13 +571,8 @@ __device__ __forceinline__ bool line_of(const AttendParams& p, int v, int extra,
         ok = s->row0 >= 0 && end >= s->row0 && end <= p.tok.n_tokens;
       }
     } else {
-      const int b = v - p.groups;
-      ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
-      const int g = group_of(p, b), len = g < 0 ? 0 : prefix_of(p, g);
-      ok = ok && len >= 0 && len <= s->ctx;
-      s->kind = len > 0 ? kRest : kWhole;
-      s->pages = (int64_t)b * p.tok.width + (len >> p.kv.page_shift);
-      s->ctx -= len;
+      ok = rest_of(p, v - p.groups, s);
+      if (ok && is_short(p, *s)) s->n = s->ctx = 0;  // (attend_rest_kernel's)
     }
     if (!ok) s->n = s->ctx = 0;
     set_line<SH>(p, *s, extra, l);
@@ -649,6 +667,29 @@ template <typename T>
 __device__ __forceinline__ float2 non_finite(uint32_t v) {
   const float2 f = T::unpack(v);
   return make_float2((v & T::kExp) == T::kExp ? f.x : 0.f, (v & (T::kExp << 16)) == (T::kExp << 16) ? f.y : 0.f);
+}
+
+// A row's places in row_ml (and row_short), and in row_o (columns c .. c + 3).
+__device__ __forceinline__ size_t ml_at(const AttendParams& p, int rest, int head, int64_t row) {
+  return ((size_t)rest * p.kv.kv_heads + head) * ((size_t)p.tok.n_tokens * p.group) + row;
+}
+template <int D>
+__device__ __forceinline__ float4* o_at(const AttendParams& p, int rest, int head, int64_t row, int c) {
+  return reinterpret_cast<float4*>(p.row_o) +
+         (((size_t)rest * p.kv.kv_heads + head) * (D / 4) + c / 4) * ((size_t)p.tok.n_tokens * p.group) + row;
+}
+
+// Two results over different slots as one: factors of their values, and its maximum and sum.
+struct Pair {
+  float e, f, m, l;
+};
+__device__ __forceinline__ Pair join(float2 x, float2 y, float c) {
+  Pair r;
+  r.m = fmaxf(x.x, y.x);
+  r.e = r.m == -INFINITY ? 0.f : ex2((x.x - r.m) * c);
+  r.f = r.m == -INFINITY ? 0.f : ex2((y.x - r.m) * c);
+  r.l = fmaf(x.y, r.e, y.y * r.f);
+  return r;
 }
 
 // Logarithm of a row's sum of exponentials.
@@ -749,8 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // The setup above touches only this CTA; everything read or written from
-  // here on may belong to the kernel before.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // here on may belong to the kernel before.  (With attend_rest_kernel in front, which
+  // lets this one begin when it has waited itself, that kernel's results are the only
+  // ones that are not there yet: they are waited for where they are joined.  64 tokens
+  // behind 8003 slots WAIT_A us instead of 57.7, drafts of 256 sequences WAIT_B instead of 212.)
+  if (!SH || p.rest_items == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Tiles and items of every sequence: thread i counts a run of them, then a
   // scan over the CTA gives the totals and who holds this worker's first unit.
@@ -1355,11 +1399,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i) any_bad |= bad[i];
       const int head = g.head * p.group + r % p.group;
       uint8_t* out = p.out + ((int64_t)(g.row0 + tok) * p.out_stride + (int64_t)head * D) * 2;
-      bool joined = false;  // (a result to be joined with another's)
-      size_t row_at = 0;
+      bool joined = false;  // (a result to be joined with another's later)
+      const int64_t row = SH ? (int64_t)(g.row0 + tok) * p.group + r % p.group : 0;
+      int kind = kWhole;
+      Pair pair;
+      bool with_rest = false;
       if constexpr (SH) {
-        joined = g.kind != kWhole;
-        row_at = ((size_t)(g.kind == kRest) * p.tok.n_tokens + g.row0 + tok) * p.q_heads + head;
+        kind = g.kind;
+        joined = kind != kWhole;
+        if (kind == kPrefix && g.part < 0 && live) {
+          // What the row's sequence has for itself is there, if it is short: joined here.
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          const float2 y = __ldcg(p.row_ml + ml_at(p, 1, g.head, row));
+          if (p.rest_items > 0 && __ldcg(p.row_short + ml_at(p, 0, g.head, row)) == kDone) {
+            pair = join(make_float2(m, l), y, p.c);
+            m = pair.m;
+            l = pair.l;
+            with_rest = true;
+            joined = false;
+          }
+        }
       }
       const float norm = g.part >= 0 || joined ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
       const int rr = (g.two ? grp * kTile : 0) + r;
@@ -1383,10 +1442,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(o1[j]), f1, v[j]);
           }
           if (live && any_bad) add_taken_out<T, D, SH>(p, g, bad, hidden, tok, c, v);
-          if (joined && live && g.part < 0) {
-            float* dst = p.row_o + row_at * D + c;
+          if constexpr (SH) {
+            if (with_rest) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) stg256(dst + j, reinterpret_cast<const uint32_t*>(v) + j);
+              for (int j = 0; j < 8; ++j) {
+                const float4 y = __ldcg(o_at<D>(p, 1, g.head, row, c + 4 * j));
+                v[4 * j] = fmaf(v[4 * j], pair.e, y.x * pair.f);
+                v[4 * j + 1] = fmaf(v[4 * j + 1], pair.e, y.y * pair.f);
+                v[4 * j + 2] = fmaf(v[4 * j + 2], pair.e, y.z * pair.f);
+                v[4 * j + 3] = fmaf(v[4 * j + 3], pair.e, y.w * pair.f);
+              }
+            }
+          }
+          if (joined && live && g.part < 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *o_at<D>(p, kind == kRest, g.head, row, c + 4 * j) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           } else if (live && g.part < 0) {
             // (64 bytes of a row: whole sectors, and no shared memory is held up
             // for the next item.  16 bytes a store: four prompts of 2048
@@ -1419,7 +1491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g.part >= 0)
           p.part_ml[part + rr] = make_float2(m, l);
         else if (joined)
-          p.row_ml[row_at] = make_float2(m, l);
+          p.row_ml[ml_at(p, kind == kRest, g.head, row)] = make_float2(m, l);
         else if (p.lse)
           p.lse[(int64_t)(g.row0 + tok) * p.q_heads + head] = log_sum<T>(m, l, p.c);
       }
@@ -1453,11 +1525,507 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
+  if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");  // (the next kernel waits for this one only)
   if (tid == 0) p.errs[worker] = hdr->abort ? 1 : fits ? 0 : kMisfit;
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// --------------------------------------------- short rests behind a prefix
+//
+// What a sequence has for itself behind a shared prefix is mostly one token or a
+// draft over a few hundred slots.  Through the kernel above each of them has a
+// whole SM, and 6 us, for itself.  Here two CTAs share an SM and go through items (a
+// sequence and a key-value head, up to 64 rows) one after another, six warps each:
+//  - warp 0 takes items (the next one is that of a CTA of the grid which has not
+//    begun: it is called off, so that long and short items even out), looks their
+//    pages up and loads queries, keys and values of 64 slots by TMA, ahead of the
+//    others over the ends of items;
+//  - warp 1 issues the products: S = Q K^T of the next tile beside the softmax of
+//    this one, then O += P V;
+//  - warps 2 to 5 have a row per thread, as in the kernel above, with the same lazy
+//    maximum, masks and treatment of infinities and NaN in drafted values.
+// Results are left in 32 bits, to be joined with the prefix's.
+//
+// REST_FIGURES
+
+constexpr int kRestThreads = 192, kRestTile = 64, kRestPerSm = 2, kUnits = 4;
+constexpr int kRestAhead = 8;   // items that have been told of; the loader is at most three ahead of the slowest warp
+
+struct RestItem {
+  int64_t pages;  // where its page ids begin in the table
+  int32_t valid, row0, n, ctx, head;
+};
+struct alignas(16) RestHdr {
+  uint32_t answer[4];                       // which CTA was called off
+  uint64_t full[kUnits], empty[kUnits];     // keys or values of a tile
+  uint64_t q_full[2], q_empty[2];
+  uint64_t item_full[kRestAhead];
+  uint64_t answer_full;
+  uint64_t s_full, s_read, p_ready, pv_done, o_free, meet, drain;
+  uint32_t tmem_base;
+  int32_t abort;
+  uint32_t bad[3][2];                       // drafted tokens with values that are not finite, by item
+  RestItem item[kRestAhead];
+};
+template <int D>
+struct RestCfg {
+  static constexpr uint32_t kHalf = kRestTile * 128, kHalves = D / 64;
+  static constexpr uint32_t kUnit = kHalves * kHalf;   // queries of 64 rows, keys or values of 64 slots
+  // Tensor memory: scores, weights, accumulator.
+  static constexpr uint32_t kCols = 256, kP = 64, kO = 128;
+  // (a product reads 128 rows of queries: what lies behind their place, units of keys and values, makes rows that
+  // nothing reads)
+  static constexpr size_t kSmem = (2 + kUnits) * (size_t)kUnit + sizeof(RestHdr);
+  static_assert(kRestPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+// Calls off a CTA of the grid that has not begun; 16 bytes at `to` will tell which.
+__device__ __forceinline__ void call_off(uint32_t to, uint32_t bar) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the answer before has been read)
+  mbar_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+               "r"(bar)
+               : "memory");
+}
+// Its number, or -1 if there was none.
+__device__ __forceinline__ int called_off(uint32_t at) {
+  int x;
+  asm volatile(
+      "{\n .reg .b128 a;\n .reg .pred p;\n .reg .b32 y, z;\n ld.shared.b128 a, [%1];\n mov.b32 %0, -1;\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, a;\n}\n"
+      : "=r"(x)
+      : "r"(at)
+      : "memory");
+  return x;
+}
+
+// The call's tokens of a sequence (64 at most) that one of them sees.
+__device__ __forceinline__ unsigned long long tokens_seen(const AttendParams& p, int row0, int n, int tok) {
+  const unsigned long long m =
+      p.tree ? (unsigned long long)__ldg(p.tree + (int64_t)(row0 + tok) * p.words) : (2ull << tok) - 1ull;
+  return n < 64 ? m & ((1ull << n) - 1ull) : m;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRestThreads, kRestPerSm)
+    attend_rest_kernel(const AttendParams p, const __grid_constant__ CUtensorMap map_kv,
+                       const __grid_constant__ CUtensorMap map_q) {
+  using C = RestCfg<D>;
+  extern __shared__ __align__(1024) unsigned char rest_smem[];
+  RestHdr* hdr = reinterpret_cast<RestHdr*>(rest_smem + (2 + kUnits) * (size_t)C::kUnit);
+  const uint32_t q_s = smem_u32(rest_smem), kv_s = q_s + 2 * C::kUnit;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int32_t* abort = &hdr->abort;
+  const int wl = p.wait_limit;
+  if (tid == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(smem_u32(&hdr->full[i]), 1);
+      mbar_init(smem_u32(&hdr->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&hdr->q_full[i]), 1);
+      mbar_init(smem_u32(&hdr->q_empty[i]), 1);
+    }
+    for (int i = 0; i < 3; ++i) hdr->bad[i][0] = hdr->bad[i][1] = 0u;
+    for (int i = 0; i < kRestAhead; ++i) mbar_init(smem_u32(&hdr->item_full[i]), 1);
+    mbar_init(smem_u32(&hdr->answer_full), 1);
+    mbar_init(smem_u32(&hdr->s_full), 1);
+    mbar_init(smem_u32(&hdr->s_read), kTile);
+    mbar_init(smem_u32(&hdr->p_ready), kTile);
+    mbar_init(smem_u32(&hdr->pv_done), 1);
+    mbar_init(smem_u32(&hdr->o_free), kTile);
+    mbar_init(smem_u32(&hdr->meet), kTile);
+    mbar_init(smem_u32(&hdr->drain), 1);
+    // (the swizzle wants tiles on 1024-byte boundaries; dynamic shared memory begins on one)
+    hdr->abort = (q_s & 1023u) != 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_kv)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hdr->tmem_base)),
+                 "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = hdr->tmem_base;
+  // (after the wait: what was there for this kernel is there for the next one, which does not wait itself)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const bool held = p.withhold != 0 && blockIdx.x == 0, sound = hdr->abort == 0;
+  __syncthreads();
+
+  // The loader's next item (-1: none is left), calls, tiles and items.
+  int i = blockIdx.x, asked = 1, armed = 0, k_sent = 0;
+  if (!sound) {
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ loader
+    const int box = min(p.kv.page_size, kRestTile), pieces = kRestTile / box;
+    const int half = lane % C::kHalves, is_v = lane / C::kHalves & 1, piece = lane / (2 * C::kHalves);
+    const uint32_t dst = kv_s + is_v * C::kUnit + half * C::kHalf + piece * box * 128;
+    bool stop = false;
+    if (lane == 0) call_off(smem_u32(hdr->answer), smem_u32(&hdr->answer_full));
+    while (!stop) {
+      // the next short item
+      Span s;
+      bool found = false;
+      int head = 0;
+      while (i >= 0 && !found) {
+        head = i % p.kv.kv_heads;
+        if (rest_of(p, i / p.kv.kv_heads, &s) && s.kind == kRest && s.n > 0) {
+          found = is_short(p, s);
+          const int64_t row = (int64_t)s.row0 * p.group;
+          for (int64_t r = lane; !found && r < (int64_t)s.n * p.group; r += 32)
+            p.row_short[ml_at(p, 0, head, row + r)] = kLong;
+          if (found && lane == 0) p.row_short[ml_at(p, 0, head, row)] = kBegun;
+        }
+        if (!warp_wait(smem_u32(&hdr->answer_full), (asked - 1) & 1, wl, abort)) {
+          stop = true;
+          break;
+        }
+        i = called_off(smem_u32(hdr->answer));
+        __syncwarp();
+        if (i >= 0) {
+          ++asked;
+          if (lane == 0) call_off(smem_u32(hdr->answer), smem_u32(&hdr->answer_full));
+        }
+      }
+      // (the place of the queries: those of the item before the last have been used)
+      if (found && !warp_wait(smem_u32(&hdr->q_empty[k_sent & 1]), ((k_sent >> 1) & 1) ^ 1, wl, abort)) stop = true;
+      if (stop) break;
+      if (lane == 0) {
+        hdr->item[k_sent % kRestAhead] = RestItem{s.pages, found, s.row0, s.n, s.ctx, head};
+        mbar_arrive(smem_u32(&hdr->item_full[k_sent % kRestAhead]));
+      }
+      __syncwarp();
+      if (!found) break;
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&hdr->q_full[k_sent & 1]);
+        mbar_expect_tx(bar, (uint32_t)p.rest_q_rows * 128u * C::kHalves);
+        for (int h = 0; h < (int)C::kHalves; ++h)
+          tma_q(q_s + (k_sent & 1) * C::kUnit + h * C::kHalf, &map_q, h * 64, head * p.group, s.row0, bar);
+      }
+      __syncwarp();
+      ++k_sent;
+      const int end = s.ctx + s.n, tiles = (end + kRestTile - 1) / kRestTile;
+      const int32_t* table = p.tok.table + s.pages;
+      int slot = piece * box;
+      bool load = piece < pieces && slot < end;
+      int page = load ? __ldg(table + (slot >> p.kv.page_shift)) : 0;
+      for (int t = 0; t < tiles; ++t, ++armed) {
+        // (the next tile's pages are looked up before this one's places are waited for)
+        const int slot2 = slot + kRestTile;
+        const bool load2 = piece < pieces && slot2 < end;
+        const int page2 = load2 ? __ldg(table + (slot2 >> p.kv.page_shift)) : 0;
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, load && is_v == 0));
+        const int u = 2 * (armed & 1);
+        for (int v = 0; v < 2 && !stop; ++v) {
+          if (armed > 1 && !warp_wait(smem_u32(&hdr->empty[u + v]), ((armed >> 1) - 1) & 1, wl, abort)) {
+            stop = true;
+            break;
+          }
+          const uint32_t bar = smem_u32(&hdr->full[u + v]);
+          const bool leave = held && armed == 0 && v == 0;
+          if (lane == 0 && !leave) mbar_expect_tx(bar, count * box * 128);
+          __syncwarp();
+          if (load && is_v == v && !leave)
+            tma_kv(dst + u * C::kUnit, &map_kv, slot & (p.kv.page_size - 1), half, v * p.kv.kv_heads + head, page, bar);
+        }
+        if (stop) break;
+        slot = slot2;
+        load = load2;
+        page = page2;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ issuer
+    if (lane == 0) {
+      const uint32_t id_s = idesc<T>(kRestTile, false, p.negate != 0);
+      constexpr uint32_t id_o = idesc<T>(D, true);
+      int done = 0;    // tiles
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        ok = ok && mbar_wait(smem_u32(bar), parity & 1, wl, abort);
+        return ok;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!wait(&hdr->item_full[k % kRestAhead], k / kRestAhead)) break;
+        const RestItem s = hdr->item[k % kRestAhead];
+        if (!s.valid) break;
+        const int end = s.ctx + s.n, tiles = (end + kRestTile - 1) / kRestTile;
+        const uint64_t q = desc_k_major(q_s + (k & 1) * C::kUnit);
+        if (!wait(&hdr->q_full[k & 1], k >> 1)) break;
+        const auto scores = [&](int t) {   // of tile t, when the scores before have been read
+          const int x = done + t, u = 2 * (x & 1);
+          if (!wait(&hdr->full[u], x >> 1) || (x > 0 && !wait(&hdr->s_read, x - 1))) return;
+          tc_fence_after();
+          const uint64_t b = desc_k_major(kv_s + u * C::kUnit);
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t o = (uint32_t)(e & 3) * 2 + (uint32_t)(e >> 2) * (C::kHalf >> 4);
+            mma_ss(tmem, q + o, b + o, id_s, e > 0);
+          }
+          mma_commit(smem_u32(&hdr->s_full));
+          mma_commit(smem_u32(&hdr->empty[u]));
+          if (t + 1 == tiles) mma_commit(smem_u32(&hdr->q_empty[k & 1]));
+        };
+        scores(0);
+        for (int t = 0; t < tiles && ok; ++t) {
+          if (t + 1 < tiles) scores(t + 1);
+          const int x = done + t, u = 2 * (x & 1) + 1;
+          // (the accumulator of the item before has been read)
+          if (t == 0 && k > 0 && !wait(&hdr->o_free, k - 1)) break;
+          if (!wait(&hdr->p_ready, x) || !wait(&hdr->full[u], x >> 1)) break;
+          tc_fence_after();
+          // Values: rows of 64 columns, groups of 8 slots 1024 bytes apart, blocks of 64 columns C::kHalf apart.
+          const uint32_t at = kv_s + u * C::kUnit;
+          const uint64_t b = (uint64_t)((at & 0x3FFFFu) >> 4) | (uint64_t)(C::kHalf >> 4) << 16 |
+                             (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+          const int groups = (min(kRestTile, end - t * kRestTile) + 15) / 16;
+#pragma unroll
+          for (int e = 0; e < kRestTile / 16; ++e)
+            if (e < groups) mma_ts(tmem + C::kO, tmem + C::kP + e * 8, b + e * (2048 >> 4), id_o, t > 0 || e > 0);
+          mma_commit(smem_u32(&hdr->pv_done));
+          mma_commit(smem_u32(&hdr->empty[u]));
+        }
+        done += tiles;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ rows
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16), t_p = t_s + C::kP, t_o = t_s + C::kO;
+    const uint64_t c2 = f2(p.c, p.c);
+    int n_s = 0;
+    for (int k = 0;; ++k) {
+      if (!warp_wait(smem_u32(&hdr->item_full[k % kRestAhead]), (k / kRestAhead) & 1, wl, abort)) break;
+      const RestItem s = hdr->item[k % kRestAhead];
+      if (!s.valid) break;
+      const int rows = s.n * p.group, end = s.ctx + s.n, tiles = (end + kRestTile - 1) / kRestTile;
+      const bool live = r < rows, any = quarter * 32 < rows;
+      const int tok = r / p.group;
+      const unsigned long long seen = live ? tokens_seen(p, s.row0, s.n, tok) : 0ull;
+      uint32_t* bad = hdr->bad[k % 3];
+      float m = -INFINITY, l = 0.f, off = 0.f;
+      bool stop = false;
+#pragma unroll 1
+      for (int t = 0; t < tiles; ++t, ++n_s) {
+        const int start = t * kRestTile;
+        const bool tail = start + kRestTile > s.ctx;       // drafted tokens among the slots, or the end
+        if (!warp_wait(smem_u32(&hdr->s_full), n_s & 1, wl, abort)) {
+          stop = true;
+          break;
+        }
+        bool ok = true;
+        if (any) {
+          tc_fence_after();
+          uint32_t w[kRestTile];
+          tmem_ld32(t_s, w);
+          tmem_ld32(t_s + 32, w + 32);
+          tmem_ld_wait();
+          tmem_arrived(w);
+          tmem_arrived(w + 32);
+          tc_fence_before();
+          mbar_arrive(smem_u32(&hdr->s_read));
+          if (tail) {
+            const int x0 = start - s.ctx;                  // the tile's first slot as a drafted token, above -64
+            const unsigned long long v = x0 >= 0 ? (x0 < 64 ? seen >> x0 : 0ull)
+                                                 : live ? seen << -x0 | ((1ull << -x0) - 1ull) : 0ull;
+            const uint32_t word[2] = {(uint32_t)v, (uint32_t)(v >> 32)};
+#pragma unroll
+            for (int j = 0; j < kRestTile; ++j) w[j] = word[j >> 5] & (1u << (j & 31)) ? w[j] : 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(w[j]);
+#pragma unroll
+          for (int j = 4; j < kRestTile; j += 2)
+            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          // (the product before is done: the weights' place is free, the accumulator at rest)
+          ok = t == 0 || mbar_wait(smem_u32(&hdr->pv_done), (n_s - 1) & 1, wl, abort);
+          __syncwarp();
+          tc_fence_after();
+          const bool grow = (top - m) * p.c > kRescale;
+          if (__any_sync(0xffffffffu, grow)) {
+            if (t > 0) {
+              const float f = grow ? ex2((m - top) * p.c) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(t_o + c, o);
+                tmem_ld_wait();
+                tmem_arrived(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(t_o + c, o);
+                tmem_st16(t_o + c + 16, o + 16);
+              }
+              l *= f;
+            }
+            if (grow) {
+              m = top;
+              off = T::kShift - m * p.c;
+            }
+          }
+          const uint64_t off2 = f2(off, off);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x =
+                  unf2(fma2(f2(__uint_as_float(w[q * 32 + 2 * j]), __uint_as_float(w[q * 32 + 2 * j + 1])), c2, off2));
+              const float a = ex2(x.x), b = ex2(x.y);
+              sum[j & 1] = add2(sum[j & 1], f2(a, b));
+              pk[j] = T::pack(a, b);
+            }
+            tmem_st16(t_p + q * 16, pk);
+          }
+          const float2 y = unf2(add2(sum[0], sum[1]));
+          l += y.x + y.y;
+          tmem_st_wait();
+        } else {
+          mbar_arrive(smem_u32(&hdr->s_read));
+          // (or this warp would announce weights before others have announced those before)
+          ok = t == 0 || mbar_wait(smem_u32(&hdr->pv_done), (n_s - 1) & 1, wl, abort);
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          stop = true;
+          break;
+        }
+        if (tail) {
+          // Values of slots that some row must not see: zero past the end (as far as products read), infinities and NaN
+          // of drafted tokens out (kept in `bad`).  Two threads a slot.
+          const int u = 2 * (n_s & 1) + 1;
+          if (!warp_wait(smem_u32(&hdr->full[u]), (n_s >> 1) & 1, wl, abort)) {
+            stop = true;
+            break;
+          }
+          const int j = r >> 1, slot = start + j, slots = min(kRestTile, end - start);
+          const uint32_t row = kv_s + u * C::kUnit + j * 128;
+          if (slot >= end) {
+            if (j < ((slots + 15) & ~15))
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                const int x = (r & 1) * (D / 16) + c;
+                sts128(row + (x >> 3) * C::kHalf + (((x ^ j) & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+              }
+          } else if (slot >= s.ctx) {
+            bool odd = false;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const int x = (r & 1) * (D / 16) + c;
+              const uint32_t at = row + (x >> 3) * C::kHalf + (((x ^ j) & 7) << 4);
+              const uint4 v = lds128(at);
+              if (T::trace(v.w, T::trace(v.z, T::trace(v.y, T::trace(v.x, 0u)))) & 0x7fff7fffu) {
+                odd = true;
+                sts128(at, make_uint4(only_finite<T>(v.x), only_finite<T>(v.y), only_finite<T>(v.z),
+                                      only_finite<T>(v.w)));
+              }
+            }
+            if (odd) atomicOr(&bad[(slot - s.ctx) >> 5], 1u << ((slot - s.ctx) & 31));
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&hdr->p_ready));
+      }
+      if (stop) break;
+      // All have noted what they found, and the last product is done.
+      if (r == 0) hdr->bad[(k + 1) % 3][0] = hdr->bad[(k + 1) % 3][1] = 0u;  // (last read before all met an item ago)
+      mbar_arrive(smem_u32(&hdr->meet));
+      if (!warp_wait(smem_u32(&hdr->meet), k & 1, wl, abort) ||
+          !warp_wait(smem_u32(&hdr->pv_done), (n_s - 1) & 1, wl, abort))
+        break;
+      tc_fence_after();
+      const unsigned long long lost = ((unsigned long long)bad[1] << 32 | bad[0]) & seen;
+      const int64_t row = (int64_t)s.row0 * p.group + r;
+      if (any) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_o + c, o);
+          tmem_ld_wait();
+          tmem_arrived(o);
+          if (!live) continue;
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]);
+          // the infinities and NaN that were taken out (from the cache itself; rare)
+#pragma unroll 1
+          for (unsigned long long x = lost; x; x &= x - 1) {
+            const int slot = s.ctx + __ffsll(x) - 1;
+            const int page = __ldg(p.tok.table + s.pages + (slot >> p.kv.page_shift));
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                p.kv.base + ((((int64_t)page * 2 + 1) * p.kv.kv_heads + s.head) * p.kv.page_size +
+                             (slot & (p.kv.page_size - 1))) * D * 2 + c * 2);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 y = non_finite<T>(__ldg(src + j));
+              v[2 * j] += y.x;
+              v[2 * j + 1] += y.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *o_at<D>(p, 1, s.head, row, c + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        if (live) {
+          p.row_ml[ml_at(p, 1, s.head, row)] = make_float2(m, l);
+          p.row_short[ml_at(p, 0, s.head, row)] = kDone;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&hdr->o_free));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort) {
+    // A wait ran out.  What this CTA started has to end before it leaves (waits bounded again), and items that it was to
+    // take have not been begun by any other.
+    int32_t none = 0;
+    if (warp == 1 && lane == 0 && sound) {
+      mma_commit(smem_u32(&hdr->drain));
+      mbar_wait(smem_u32(&hdr->drain), 0u, wl, &none);
+    }
+    if (warp == 0) {
+      bool answered = false;
+      if (sound) {
+        // (of the last tile maybe only the keys were sent for, and no one waits long for the others)
+        for (int j = max(0, armed - 2); j <= armed; ++j)
+          for (int v = 0; v < 2; ++v)
+            if (!(held && j == 0 && v == 0))
+              mbar_wait(smem_u32(&hdr->full[2 * (j & 1) + v]), (j >> 1) & 1, j < armed ? wl : min(wl, 4096), &none);
+        for (int j = max(0, k_sent - 2); j < k_sent; ++j)
+          mbar_wait(smem_u32(&hdr->q_full[j & 1]), (j >> 1) & 1, wl, &none);
+        answered = mbar_wait(smem_u32(&hdr->answer_full), (asked - 1) & 1, wl, &none);
+      }
+      for (int x = 0; x < 2; ++x) {
+        const int j = x == 0 ? i : answered && i >= 0 ? called_off(smem_u32(hdr->answer)) : -1;
+        Span s;
+        if (j >= 0 && rest_of(p, j / p.kv.kv_heads, &s) && s.n > 0 && is_short(p, s) && lane == 0)
+          p.row_short[ml_at(p, 0, j % p.kv.kv_heads, (int64_t)s.row0 * p.group)] = kBegun;
+      }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
   }
 }
 
@@ -1475,7 +2043,7 @@ constexpr int kJoinThreads = 256, kJoinBlocks = 8;
 // Letting the blocks start while the first kernel still runs is slower (one token
 // 18.1 us against 17.4).  The blocks after these write the status of a sequence
 // each (one block, as a warp takes 10 us for the pages of 131,000 slots).
-template <typename T, int D, bool SH>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x >= (unsigned)(p.workers * kJoinBlocks)) {
@@ -1487,25 +2055,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
 #pragma unroll 4
     for (int i = threadIdx.x; i < pages; i += kJoinThreads) ok &= (uint32_t)__ldg(row + i) < (uint32_t)p.kv.pages;
     bool late = false;
-    if constexpr (SH) {
-      bool fits = true;
-      for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) {
-        const int e = __ldcg(p.errs + i);
-        late |= e == 1;
-        fits &= e != kMisfit;
-      }
-      fits = __syncthreads_and(fits);
-      const int g = fits ? group_of(p, b) : -1, len = g < 0 ? 0 : prefix_of(p, g);
-      ok &= fits && len >= 0 && (!ok || s.n == 0 || len <= s.ctx);
-      // the prefix lies in the same pages as the group's first sequence's
-      if (ok && len > 0) {
-        const int32_t* first = p.tok.table + (int64_t)__ldg(p.cu_seqs + g) * p.tok.width;
-        for (int i = threadIdx.x; i < len >> p.kv.page_shift && s.n > 0; i += kJoinThreads)
-          ok &= __ldg(row + i) == __ldg(first + i);
-      }
-    } else {
-      for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) late |= __ldcg(p.errs + i) != 0;
-    }
+    for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) late |= __ldcg(p.errs + i) != 0;
     ok = __syncthreads_and(ok);
     late = __syncthreads_or(late);
     if (threadIdx.x == 0)
@@ -1513,7 +2063,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
     return;
   }
   const int w0 = blockIdx.x / kJoinBlocks, y = blockIdx.x % kJoinBlocks;
-  const SegOf<SH> g = p.descs[w0];
+  const Seg g = p.descs[w0];
   if (!g.valid) return;
   const int full = p.tile_tokens * p.group, left = (g.n - g.tok0) * p.group;
   const int v0 = min(left, full), rows = g.two ? min(left, 2 * full) : v0;  // rows of the first M tile, of both
@@ -1540,14 +2090,6 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
     const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
     const int tok = g.tok0 + k / p.group, head = g.head * p.group + k % p.group;
     const int64_t row = g.row0 + tok;
-    if constexpr (SH) {
-      if (g.kind != kWhole) {
-        const size_t to = ((size_t)(g.kind == kRest) * p.tok.n_tokens + row) * p.q_heads + head;
-        *reinterpret_cast<float4*>(p.row_o + to * D + 4 * c) = v;
-        if (c == 0) p.row_ml[to] = make_float2(m, l);
-        continue;
-      }
-    }
     *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + (int64_t)head * D + 4 * c) * 2) =
         make_uint2(T::pack(v.x * norm, v.y * norm), T::pack(v.z * norm, v.w * norm));
     if (p.lse && c == 0)
@@ -1555,38 +2097,137 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
   }
 }
 
-// The prefix's part and the own part of each row: out = sum of the parts, each
-// times exp(its maximum - the larger one), over the sum of theirs.  A block takes
-// every blocks-th group of rows of its sequence, a row's 4 columns a thread.
+// The same for calls with common prefixes.  Few items may hold all rows (a long prefix with a part in every worker), or
+// every worker may start one: the blocks share out the tasks of all of them.  A prefix's row takes what its sequence
+// has for itself with it, if that is there.  Bound: latencies, among them the fetch of instructions, so the code is short
+// (eight parts at a time, unrolled: 64 tokens behind 8003 slots 16.4 us instead of JOIN_US).
+constexpr int kJoinSharedBlocks = 4;  // for each worker
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const AttendParams p) {
+  __shared__ uint32_t starts[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int blocks = gridDim.x - p.tok.batch;
+  if (blockIdx.x >= (unsigned)blocks) {
+    const int b = blockIdx.x - blocks;
+    Span s;
+    bool late = false, fits = true;
+    for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) {
+      const int e = __ldcg(p.errs + i);
+      late |= e == 1;
+      fits &= e != kMisfit;
+    }
+    bool ok = __syncthreads_and(fits) && rest_of(p, b, &s);  // (that it fits the group as well)
+    if (ok && s.n > 0) {
+      const int32_t* row = p.tok.table + (int64_t)b * p.tok.width;
+      const int shared = (int)((s.pages - (int64_t)b * p.tok.width));  // pages
+      const int pages = shared + (s.ctx + s.n - 1) / p.kv.page_size + 1;
+      const int32_t* first = shared ? p.tok.table + (int64_t)__ldg(p.cu_seqs + group_of(p, b)) * p.tok.width : row;
+      if (is_short(p, s))
+        for (int i = threadIdx.x; i < p.kv.kv_heads; i += kJoinThreads)
+          late |= __ldcg(p.row_short + ml_at(p, 0, i, (int64_t)s.row0 * p.group)) == kBegun;
+      // the prefix lies in the same pages as the group's first sequence's
+      for (int i = threadIdx.x; i < pages; i += kJoinThreads) {
+        const int page = __ldg(row + i);
+        ok &= (uint32_t)page < (uint32_t)p.kv.pages && (i >= shared || page == __ldg(first + i));
+      }
+    }
+    ok = __syncthreads_and(ok);
+    late = __syncthreads_or(late);
+    if (threadIdx.x == 0)
+      set_status(p.status, b, late ? TC_ERR_DEVICE_TIMEOUT : ok ? TC_OK : TC_ERR_BOUNDS, p.kv.keep);
+    return;
+  }
+  if (threadIdx.x < 32) starts[threadIdx.x] = 0u;
+  __syncthreads();
+  for (int w = threadIdx.x; w / 32 * 32 < p.workers; w += kJoinThreads) {
+    const uint32_t m = __ballot_sync(0xffffffffu, w < p.workers && __ldcg(&p.descs[w].valid) != 0);
+    if (w % 32 == 0) starts[w / 32] = m;
+  }
+  __syncthreads();
+  constexpr int kChunks = 2 * kTile * (D / 4) / kJoinThreads;  // of an item
+  int before = 0, word = 0;
+  for (int slot = blockIdx.x;; slot += blocks) {
+    const int item = slot / kChunks;
+    // the item-th worker that starts one
+    while (word < 32 && item - before >= __popc(starts[word])) before += __popc(starts[word++]);
+    if (word == 32) break;
+    uint32_t bits = starts[word];
+    for (int i = before; i < item; ++i) bits &= bits - 1;
+    const int w0 = word * 32 + __ffs(bits) - 1;
+    const SharedSeg g = p.descs[w0];
+    const int full = p.tile_tokens * p.group, left = (g.n - g.tok0) * p.group;
+    const int v0 = min(left, full), rows = g.two ? min(left, 2 * full) : v0;  // rows of the first M tile, of both
+    const int i = slot % kChunks * kJoinThreads + threadIdx.x;
+    if (i >= rows * (D / 4)) continue;
+    const int c = i / rows * 4, k = i % rows;        // columns c .. c + 3 of row k
+    const int rr = k < v0 ? k : kTile + k - v0;      // its place in a part
+    const int tok = g.tok0 + k / p.group, of = k % p.group;
+    const int64_t row = g.row0 + tok, r = row * p.group + of;
+    int there = kLong;
+    float2 rest_ml;
+    float4 rest_o;
+    if (g.kind == kPrefix && p.rest_items > 0) {  // (on their way together with the parts)
+      there = __ldcg(p.row_short + ml_at(p, 0, g.head, r));
+      rest_ml = __ldcg(p.row_ml + ml_at(p, 1, g.head, r));
+      rest_o = __ldcg(o_at<D>(p, 1, g.head, r, c));
+    }
+    float m = -INFINITY, l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](float2 ml, float4 o) {
+      const Pair z = join(make_float2(m, l), ml, p.c);
+      m = z.m;
+      l = z.l;
+      v = make_float4(fmaf(v.x, z.e, o.x * z.f), fmaf(v.y, z.e, o.y * z.f), fmaf(v.z, z.e, o.z * z.f),
+                      fmaf(v.w, z.e, o.w * z.f));
+    };
+#pragma unroll 4
+    for (int w = w0; w <= g.last; ++w) {
+      const size_t at = ((size_t)w * 2 + (w == w0)) * 2 * kTile;
+      add(__ldcg(p.part_ml + at + rr),
+          __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + (size_t)(c / 4) * (2 * kTile) + rr));
+    }
+    bool done = g.kind == kWhole;
+    if (there == kDone) {
+      add(rest_ml, rest_o);
+      done = true;
+    }
+    if (!done) {
+      *o_at<D>(p, g.kind == kRest, g.head, r, c) = v;
+      if (c == 0) p.row_ml[ml_at(p, g.kind == kRest, g.head, r)] = make_float2(m, l);
+      continue;
+    }
+    const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    const int head = g.head * p.group + of;
+    *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + (int64_t)head * D + c) * 2) =
+        make_uint2(T::pack(v.x * norm, v.y * norm), T::pack(v.z * norm, v.w * norm));
+    if (p.lse && c == 0) p.lse[row * p.q_heads + head] = log_sum<T>(m, l, p.c);
+  }
+}
+
+// Rows whose sequence has much for itself: the prefix's part and the own part, out =
+// sum of the parts, each times exp(its maximum - the larger one), over the sum of
+// theirs.  A few blocks a sequence; a thread takes 4 columns of a row.
 constexpr int kPairThreads = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kPairThreads) attend_pair_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x;
-  SeqSpan s;
-  if (__ldcg(p.errs) == kMisfit || !seq_span(p.tok, p.kv.page_size, b, &s) || s.n > p.max_tokens) return;
-  const int g = group_of(p, b), len = g < 0 ? 0 : prefix_of(p, g);
-  if (len <= 0 || len > s.ctx) return;
-  constexpr int kRow = D / 4;  // threads of a row
-  const size_t first = (size_t)s.row0 * p.q_heads, rest = (size_t)p.tok.n_tokens * p.q_heads;
-  const int64_t rows = (int64_t)s.n * p.q_heads;
-  for (int64_t r = blockIdx.y * (kPairThreads / kRow) + threadIdx.x / kRow; r < rows;
-       r += gridDim.y * (kPairThreads / kRow)) {
-    const size_t at = first + r;
-    const int c = threadIdx.x % kRow * 4;
-    const float2 x = __ldcg(p.row_ml + at), y = __ldcg(p.row_ml + rest + at);
-    const float4 u = __ldcg(reinterpret_cast<const float4*>(p.row_o + at * D + c));
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(p.row_o + (rest + at) * D + c));
-    const float m = fmaxf(x.x, y.x);
-    const float e = m == -INFINITY ? 0.f : ex2((x.x - m) * p.c), f = m == -INFINITY ? 0.f : ex2((y.x - m) * p.c);
-    const float l = fmaf(x.y, e, y.y * f);
-    const float norm = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
-    const int64_t row = s.row0 + r / p.q_heads, head = r % p.q_heads;
-    *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + head * D + c) * 2) =
-        make_uint2(T::pack(fmaf(u.x, e, v.x * f) * norm, fmaf(u.y, e, v.y * f) * norm),
-                   T::pack(fmaf(u.z, e, v.z * f) * norm, fmaf(u.w, e, v.w * f) * norm));
-    if (p.lse && c == 0) p.lse[at] = log_sum<T>(m, l, p.c);
+  Span s;
+  if (__ldcg(p.errs) == kMisfit || !rest_of(p, b, &s) || s.kind != kRest || is_short(p, s)) return;
+  const int64_t rows = (int64_t)s.n * p.group, all = rows * p.kv.kv_heads * (D / 4);
+  for (int64_t i = blockIdx.y * kPairThreads + threadIdx.x; i < all; i += gridDim.y * kPairThreads) {
+    const int64_t r = (int64_t)s.row0 * p.group + i % rows, x = i / rows;
+    const int c = (int)(x % (D / 4)) * 4, head = (int)(x / (D / 4));
+    const Pair z = join(__ldcg(p.row_ml + ml_at(p, 0, head, r)), __ldcg(p.row_ml + ml_at(p, 1, head, r)), p.c);
+    const float4 u = __ldcg(o_at<D>(p, 0, head, r, c)), v = __ldcg(o_at<D>(p, 1, head, r, c));
+    const float norm = z.l > 0.f ? 1.f / z.l : z.l == 0.f ? 0.f : z.l;  // (NaN stays)
+    const int64_t row = r / p.group, q_head = (int64_t)head * p.group + r % p.group;
+    *reinterpret_cast<uint2*>(p.out + (row * p.out_stride + q_head * D + c) * 2) =
+        make_uint2(T::pack(fmaf(u.x, z.e, v.x * z.f) * norm, fmaf(u.y, z.e, v.y * z.f) * norm),
+                   T::pack(fmaf(u.z, z.e, v.z * z.f) * norm, fmaf(u.w, z.e, v.w * z.f) * norm));
+    if (p.lse && c == 0) p.lse[row * p.q_heads + q_head] = log_sum<T>(z.m, z.l, p.c);
   }
 }
 
@@ -1639,11 +2280,30 @@ size_t workspace_bytes(int workers, int head_dim) {
 
 // What joining two results of every row takes beside that.
 size_t shared_bytes(int64_t rows, int head_dim) {
-  return 2 * (size_t)rows * (sizeof(float2) + sizeof(float) * head_dim) + 256;
+  return 2 * (size_t)rows * (sizeof(float2) + sizeof(float) * head_dim) + (size_t)rows * sizeof(int32_t) + 256;
+}
+
+template <typename T, int D>
+cudaError_t launch_rest(const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q, cudaLaunchConfig_t& cfg) {
+  static bool ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(attend_rest_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)RestCfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  cfg.gridDim = dim3((unsigned)p.rest_items);
+  cfg.blockDim = dim3(kRestThreads);
+  cfg.dynamicSmemBytes = RestCfg<D>::kSmem;
+  return cudaLaunchKernelEx(&cfg, attend_rest_kernel<T, D>, p, kv, q);
 }
 
 template <typename T, int D, bool SH>
 cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q, const CUtensorMap& pq,
+                   const CUtensorMap& rest, const CUtensorMap& rest_q,
                    cudaStream_t s) {
   static bool ready[kMaxDevices];
   int dev = 0;
@@ -1662,29 +2322,34 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorM
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if constexpr (SH) {
+    if (p.rest_items > 0) e = launch_rest<T, D>(p, rest, rest_q, cfg);
+    if (e != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3((unsigned)p.workers);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes<D>();
   e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D, SH>, p, kv, q, pq);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(p.workers * kJoinBlocks + p.tok.batch));
+  cfg.gridDim = dim3((unsigned)(p.workers * (SH ? kJoinSharedBlocks : kJoinBlocks) + p.tok.batch));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, SH>, p);
+  e = cudaLaunchKernelEx(&cfg, SH ? attend_join_shared_kernel<T, D> : attend_join_kernel<T, D>, p);
   if (!SH || e != cudaSuccess) return e;
-  const int64_t most = (int64_t)(p.max_tokens < p.tok.n_tokens ? p.max_tokens : p.tok.n_tokens) * p.q_heads;
-  const int64_t blocks = (most + 2 * (kPairThreads / (D / 4)) - 1) / (2 * (kPairThreads / (D / 4)));
-  cfg.gridDim = dim3((unsigned)p.tok.batch, (unsigned)(blocks < 1 ? 1 : blocks < 256 ? blocks : 256));
+  const int64_t most = (int64_t)(p.max_tokens < p.tok.n_tokens ? p.max_tokens : p.tok.n_tokens) * p.q_heads * (D / 4);
+  const int64_t room = (8 * p.workers + p.tok.batch - 1) / p.tok.batch, want = (most + kPairThreads - 1) / kPairThreads;
+  cfg.gridDim = dim3((unsigned)p.tok.batch, (unsigned)(want < 1 ? 1 : want < room ? want : room));
   cfg.blockDim = dim3(kPairThreads);
   return cudaLaunchKernelEx(&cfg, attend_pair_kernel<T, D>, p);
 }
 
 template <bool SH>
 cudaError_t launch(int dtype, int head_dim, const AttendParams& p, const CUtensorMap& kv, const CUtensorMap& q,
-                   const CUtensorMap& pq, cudaStream_t s) {
+                   const CUtensorMap& pq, const CUtensorMap& rest, const CUtensorMap& rest_q,
+                   cudaStream_t s) {
   if (dtype == TC_DT_BF16)
-    return head_dim == 128 ? launch<Bf16, 128, SH>(p, kv, q, pq, s) : launch<Bf16, 64, SH>(p, kv, q, pq, s);
-  return head_dim == 128 ? launch<F16, 128, SH>(p, kv, q, pq, s) : launch<F16, 64, SH>(p, kv, q, pq, s);
+    return head_dim == 128 ? launch<Bf16, 128, SH>(p, kv, q, pq, rest, rest_q, s) : launch<Bf16, 64, SH>(p, kv, q, pq, rest, rest_q, s);
+  return head_dim == 128 ? launch<F16, 128, SH>(p, kv, q, pq, rest, rest_q, s) : launch<F16, 64, SH>(p, kv, q, pq, rest, rest_q, s);
 }
 
 tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* a,
@@ -1733,12 +2398,17 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
   const cuuint64_t q_strides[2] = {d * 2, (cuuint64_t)(none ? row : a->q_stride) * 2};
   const cuuint32_t q_box[3] = {64, (cuuint32_t)group, (cuuint32_t)q_tokens};
   const cuuint32_t pq_box[3] = {64, (cuuint32_t)group, (cuuint32_t)pq_tokens};
-  CUtensorMap map_kv, map_q, map_pq;
+  const cuuint32_t rest_box[5] = {64, (cuuint32_t)(kv->page_size < kRestTile ? kv->page_size : kRestTile), 1, 1, 1};
+  const int rest_tokens = kRestRows / group < 1 ? 1 : q_tokens < kRestRows / group ? q_tokens : kRestRows / group;
+  const cuuint32_t rest_q_box[3] = {64, (cuuint32_t)group, (cuuint32_t)rest_tokens};
+  CUtensorMap map_kv, map_q, map_pq, map_rest, map_rest_q;
   if (!encode(&map_kv, kv->dtype, 5, v.base, kv_dims, kv_strides, kv_box) ||
       !encode(&map_q, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, q_box) ||
-      (sh && !encode(&map_pq, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, pq_box)))
+      (sh && (!encode(&map_pq, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, pq_box) ||
+              !encode(&map_rest, kv->dtype, 5, v.base, kv_dims, kv_strides, rest_box) ||
+              !encode(&map_rest_q, kv->dtype, 3, none ? kv->pool : a->q, q_dims, q_strides, rest_q_box))))
     return kv_fail(TC_ERR_UNSUPPORTED, who, ": the sizes or strides do not fit a tensor map");
-  if (!sh) map_pq = map_q;
+  if (!sh) map_pq = map_rest_q = map_q, map_rest = map_kv;
   AttendParams p{};
   p.kv = v;
   p.tok = tokens_view(tokens);
@@ -1748,6 +2418,7 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
   p.max_tokens = a->max_tokens;
   p.q_rows = group * q_tokens;
   p.prefix_q_rows = group * pq_tokens;
+  p.rest_q_rows = group * rest_tokens;
   // A scale of zero weighs all slots alike; as a factor so small that every
   // product with a score is nothing, it keeps -inf times the factor -inf.
   p.c = fmaxf(fabsf(a->scale) * 1.4426950408889634f, 1e-30f);
@@ -1777,12 +2448,17 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
     ws += (128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127;
     p.row_o = reinterpret_cast<float*>(ws);
     p.row_ml = reinterpret_cast<float2*>(ws + rows * sizeof(float) * kv->head_dim);
+    p.row_short = reinterpret_cast<int32_t*>(p.row_ml + rows);
+    // With fewer items than SMs each has an SM in the main kernel anyway, and a launch less counts: four sequences of 3 to
+    // 21 slots behind 32 SHORT_A us without, SHORT_B with it.
+    const int64_t items = (int64_t)tokens->batch * kv->kv_heads;
+    p.rest_items = items <= p.workers || items > INT32_MAX || group > kRestRows ? 0 : (int)items;
   }
   p.wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
   p.withhold = a->withhold;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = sh ? launch<true>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, s)
-                           : launch<false>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, s);
+  const cudaError_t e = sh ? launch<true>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, map_rest, map_rest_q, s)
+                           : launch<false>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, map_rest, map_rest_q, s);
   return e == cudaSuccess ? TC_OK : kv_cuda_fail(e, sh ? "tc_attend_shared: " : "tc_attend: ");
 }
 
