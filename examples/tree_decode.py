@@ -7,9 +7,12 @@ and forked (its pages are shared until they are written).  Then each round
   1. drafts, for every sequence, the branches of the catalog's trie below the
      token it emitted last (PagePool.reserve makes room, and says which shared
      page has to be copied first: KvCache.copy_pages);
-  2. runs the model over the drafts: per layer KvCache.append (norms of queries
-     and keys, rotation, write into the cache) and KvCache.attend under the
-     trees' masks (tree_masks);
+  2. runs the model over the drafts: per layer the projection to queries, keys
+     and values (Linear), KvCache.append (norms of queries and keys, rotation,
+     write into the cache), KvCache.attend_shared under the trees' masks
+     (tree_masks), which reads the prompt's pages once for all four, the
+     projection back onto the residual, and a gated feed-forward block (two more
+     Linear);
   3. takes constrained steps (Context.step) along the branches, as long as every
      sequence's emitted token was drafted;
   4. moves the accepted branches together (KvCache.compact) and gives the pages
@@ -34,7 +37,7 @@ Q_HEADS, KV_HEADS, HEAD_DIM, LAYERS = 8, 2, 64, 2
 
 
 class Model:
-    """A small pre-norm attention model (no feed-forward layers) over a tied embedding."""
+    """A small pre-norm model over a tied embedding."""
 
     def __init__(self, tcd, emb, seed: int = 7):
         import torch
@@ -42,11 +45,15 @@ class Model:
         g = torch.Generator(device="cuda").manual_seed(seed)
         hidden = emb.shape[1]
 
-        def weights(rows, cols):
-            return (torch.randn((rows, cols), generator=g, device="cuda") * rows ** -0.5).bfloat16()
+        def weights(features, inputs):
+            return (torch.randn((features, inputs), generator=g, device="cuda") * inputs ** -0.5).bfloat16()
 
-        self.qkv = [weights(hidden, (Q_HEADS + 2 * KV_HEADS) * HEAD_DIM) for _ in range(LAYERS)]
-        self.out = [weights(Q_HEADS * HEAD_DIM, hidden) for _ in range(LAYERS)]
+        wide = 4 * hidden
+        self.qkv = [tcd.Linear(weights((Q_HEADS + 2 * KV_HEADS) * HEAD_DIM, hidden)) for _ in range(LAYERS)]
+        self.out = [tcd.Linear(weights(hidden, Q_HEADS * HEAD_DIM)) for _ in range(LAYERS)]
+        self.up = [tcd.Linear(weights(wide, hidden), gate=weights(wide, hidden), act=tcd.ACT_SILU)
+                   for _ in range(LAYERS)]
+        self.down = [tcd.Linear(weights(hidden, wide)) for _ in range(LAYERS)]
         self.norm = torch.ones(HEAD_DIM, dtype=torch.bfloat16, device="cuda")
         pool = torch.zeros((LAYERS, PAGES, 2, KV_HEADS, PAGE, HEAD_DIM), dtype=torch.bfloat16, device="cuda")
         self.cache = tcd.KvCache(pool)
@@ -54,20 +61,39 @@ class Model:
             -torch.arange(0, HEAD_DIM, 2, device="cuda") / HEAD_DIM)
         self.rope = torch.stack((angle.cos(), angle.sin()), -1).float().contiguous()
 
-    def forward(self, tokens, cu, ctx, table, max_tokens, tree=None, positions=None):
-        """Hidden states [tokens, hidden] of packed tokens behind `ctx` cached ones."""
-        torch = self.torch
-        x = self.emb[tokens].float() * 4
+    def normed(self, x):
+        x = x.float()
+        return (x * self.torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6)).bfloat16()
+
+    def forward(self, tokens, cu, ctx, table, max_tokens, tree=None, positions=None, shared=None):
+        """Hidden states [tokens, hidden] of packed tokens behind `ctx` cached ones; shared: the groups of sequences
+        and the slots that each shares."""
+        n = len(tokens)
+        x = self.emb[tokens] * 4
+
+        def rows(linear):
+            return self.torch.empty((n, linear.out_features), dtype=x.dtype, device="cuda")
+
         for layer in range(LAYERS):
-            y = (x * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6)).bfloat16()
-            qkv = y @ self.qkv[layer]
-            q = torch.empty((len(tokens), Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device="cuda")
-            o = torch.empty_like(q)
+            qkv, up = rows(self.qkv[layer]), rows(self.up[layer])
+            self.qkv[layer].apply(self.normed(x), qkv)
+            q = self.torch.empty((n, Q_HEADS, HEAD_DIM), dtype=x.dtype, device="cuda")
+            o = self.torch.empty_like(q)
             self.cache.append(layer, qkv, cu, ctx, table, q, q_weight=self.norm, k_weight=self.norm, rope=self.rope,
                               positions=positions)
-            self.cache.attend(layer, q, cu, ctx, table, o, max_tokens, tree=tree)
-            x = x + (o.flatten(1) @ self.out[layer]).float()
-        return (x * torch.rsqrt((x * x).mean(-1, keepdim=True) + 1e-6)).bfloat16()
+            if shared is None:
+                self.cache.attend(layer, q, cu, ctx, table, o, max_tokens, tree=tree)
+            else:
+                self.cache.attend_shared(layer, q, cu, ctx, table, o, max_tokens, *shared, tree=tree)
+            self.out[layer].apply(o.flatten(1), x, residual=x)
+            self.up[layer].apply(self.normed(x), up)
+            self.down[layer].apply(up, x, residual=x)
+        return self.normed(x)
+
+    def raise_on_error(self):
+        self.cache.raise_on_error()
+        for linear in self.qkv + self.out + self.up + self.down:
+            linear.raise_on_error()
 
 
 class Catalog:
@@ -131,6 +157,7 @@ def decode(tcd, draft: int, batch: int = 4, prompt_len: int = 37, k: int = 3):
     prompt = torch.from_numpy(rng.integers(0, w.vocab, prompt_len)).cuda()
     model.forward(prompt, ints([0, prompt_len]), ints([0]), table(), prompt_len)
     seqs = [shared] + [pages.fork(shared, prompt_len) for _ in range(batch - 1)]
+    together = ints([0, batch]), ints([prompt_len])
     lens = [prompt_len] * batch
     pending = [int(t) for t in rng.integers(0, w.vocab, batch)]   # emitted (or given), not cached yet
     node = [0] * batch                                            # the trie's node after it
@@ -146,8 +173,8 @@ def decode(tcd, draft: int, batch: int = 4, prompt_len: int = 37, k: int = 3):
         masks = torch.zeros((len(flat), 1), dtype=torch.int64, device="cuda")
         positions = ints([0] * len(flat))
         bad = tcd.tree_masks(ints([p for d in drafts for p in d[1]]), cu, lens_dev, masks, positions)
-        hidden = model.forward(flat, cu, lens_dev, rows, max(count), masks, positions)
-        model.cache.raise_on_error()    # (of every call since the last look: all layers, page copies, the prompt)
+        hidden = model.forward(flat, cu, lens_dev, rows, max(count), masks, positions, together)
+        model.raise_on_error()    # (of every call since the last look: all layers, page copies, the prompt)
         assert not bool(bad.any())
         # constrained steps along the drafts, while every sequence's next token is one of them
         first = np.concatenate(([0], np.cumsum(count)))
