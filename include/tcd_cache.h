@@ -207,7 +207,9 @@ tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes);
  * contexts (tc_pages_fork): a shared prefix is read once for all tokens of its
  * sequences, and the result of each token is joined with that over the slots its
  * sequence has for itself.  The outputs are tc_attend's (their sums are split at
- * the end of the prefix, so that last bits may differ).
+ * the end of the prefix, so that last bits may differ).  Where the page tables have
+ * room for few slots altogether, contexts are read sequence by sequence, as that is
+ * faster then.
  *
  *  groups       1 .. batch: runs of neighbouring sequences.
  *  cu_seqs      (device) int32[groups + 1], ascending within [0, batch]: group g

@@ -12,10 +12,13 @@ pytestmark = pytest.mark.gpu
 
 
 class Groups(Batch):
-    """A batch whose groups ([first, end) sequences, shared slots) hold their whole shared pages in common."""
+    """A batch whose groups ([first, end) sequences, shared slots) hold their whole shared pages in common.
 
-    def __init__(self, tcd, tokens, ctx, groups, dt="bf16", kv_heads=2, head_dim=128, page=16, seed=0):
-        super().__init__(tcd, tokens, ctx, dt, kv_heads, head_dim, page, seed=seed)
+    room: MB of slots that the page tables have place for (below 16, contexts are read sequence by sequence)."""
+
+    def __init__(self, tcd, tokens, ctx, groups, dt="bf16", kv_heads=2, head_dim=128, page=16, seed=0, room=17):
+        wide = (room << 20) // (len(tokens) * page * kv_heads * head_dim * 4) + 1 if room else 2
+        super().__init__(tcd, tokens, ctx, dt, kv_heads, head_dim, page, seed=seed, extra_width=wide)
         torch = torch_mod()
         self.groups = groups
         self.prefix = [0] * len(tokens)
@@ -106,18 +109,19 @@ CASES = [
 ]
 
 
-def build(tcd, case, seed):
+def build(tcd, case, seed, room=17):
     tokens, behind, groups, hq, hkv, d, page, dt = case
     ctx = list(behind)
     for lo, hi, shared in groups:
         for b in range(lo, hi):
             ctx[b] += shared
-    return Groups(tcd, tokens, ctx, groups, dt, hkv, d, page, seed), hq
+    return Groups(tcd, tokens, ctx, groups, dt, hkv, d, page, seed, room), hq
 
 
+@pytest.mark.parametrize("room", [17, 0])
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_causal(tcd, case):
-    w, hq = build(tcd, CASES[case], case)
+def test_causal(tcd, case, room):
+    w, hq = build(tcd, CASES[case], case, room)
     kv = w.fill()
     q, q64 = w.normal(w.n, hq, w.head_dim)
     out, lse = w.attend(q, lse=True)
@@ -125,8 +129,9 @@ def test_causal(tcd, case):
 
 
 @pytest.mark.parametrize("case", [i for i, c in enumerate(CASES) if max(c[0]) <= 64])
-def test_drafts(tcd, case):
-    w, hq = build(tcd, CASES[case], 50 + case)
+@pytest.mark.parametrize("room", [17, 0])
+def test_drafts(tcd, case, room):
+    w, hq = build(tcd, CASES[case], 50 + case, room)
     kv = w.fill()
     q, q64 = w.normal(w.n, hq, w.head_dim)
     masks = [m for n in w.tokens for m in ancestors(random_parents(w.rng, n))]
@@ -242,6 +247,25 @@ def test_many_sequences_with_errors(tcd):
     out, _ = w.attend(q)
     assert w.status.tolist() == [0] * 100
     w.check(kv, q64, out)
+
+
+def test_pages_far_into_a_large_pool(tcd):
+    """Offsets in the cache beyond 2^32 bytes."""
+    torch = torch_mod()
+    w, hq = many(tcd, 4, 8)
+    kv = w.fill()
+    q, q64 = w.normal(w.n, hq, w.head_dim)
+    want = w.attend(q)[0].clone()
+    w.check(kv, q64, want, rows=[0, 1, 3])
+    pages = 36000 + w.pages
+    pool = torch.empty((1, pages) + tuple(w.pool.shape[2:]), dtype=w.pool.dtype, device="cuda")
+    assert pool.numel() > 1 << 31
+    pool[:, -w.pages:] = w.pool
+    w.table += 36000
+    cache = tcd.KvCache(pool)
+    out = torch.empty_like(q)
+    cache.attend_shared(0, q, w.cu, w.ctx, w.table, out, max(w.tokens), w.cu_seqs, w.shared, status=w.status)
+    assert w.status.tolist() == [0] * 100 and torch.equal(out, want)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
@@ -369,14 +393,15 @@ def test_slices_of_wider_rows(tcd):
     assert bool((got == 55).all())
 
 
-def test_errors_by_sequence(tcd):
+@pytest.mark.parametrize("room", [17, 0])
+def test_errors_by_sequence(tcd, room):
     """A page that differs, fewer slots than shared: that sequence; a length out of range: its group."""
     torch = torch_mod()
     case = ([1] * 6, [5] * 6, [(0, 3, 64), (3, 6, 100)], 4, 2, 64, 16, "bf16")
     bounds = tcd.TC_ERR_BOUNDS
 
     def fresh():
-        w, hq = build(tcd, case, 1)
+        w, hq = build(tcd, case, 1, room)
         kv = w.fill()
         q, q64 = w.normal(w.n, hq, 64)
         return w, kv, q, q64
@@ -531,7 +556,7 @@ def test_forked_pages(tcd):
             cache.copy_pages(torch.tensor([a], dtype=torch.int32, device="cuda"),
                              torch.tensor([b], dtype=torch.int32, device="cuda"))
     ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
-    table, ctx, cu = ints(np.stack([pool.row(s, 4) for s in seqs])), ints([prompt] * n), ints(list(range(n + 1)))
+    table, ctx, cu = ints(np.stack([pool.row(s, 700) for s in seqs])), ints([prompt] * n), ints(list(range(n + 1)))
     q = torch.randn((n, 8, 64), generator=g, device="cuda").bfloat16()
     out, plain = torch.empty_like(q), torch.empty_like(q)
     cache.attend_shared(0, q, cu, ctx, table, out, 1, ints([0, n]), ints([prompt]))

@@ -46,7 +46,7 @@ class Step:
         copies = [c for s in seqs for c in self.pages.reserve(s, PROMPT, PROMPT + 1)]
         if copies:
             self.cache.copy_pages(ints([a for a, _ in copies]), ints([b for _, b in copies]))
-        self.table_host = np.stack([self.pages.row(s, 6) for s in seqs])
+        self.table_host = np.stack([self.pages.row(s, 24) for s in seqs])
         self.table, self.ctx = ints(self.table_host), ints([PROMPT] * batch)
         self.cu, self.groups = ints(range(batch + 1)), (ints([0, batch]), ints([PROMPT]))
         angle = torch.arange(PROMPT + 1, device="cuda")[:, None] * 1e4 ** (-torch.arange(0, D, 2, device="cuda") / D)

@@ -183,3 +183,74 @@ def test_refusals(tcd):
         tcd.Linear(z(4, 8), act=9).apply(z(1, 8), z(1, 4))
     torch.cuda.synchronize()
     assert bool((w.big == w.MARK).all())
+
+
+def test_rows_far_apart(tcd):
+    """Offsets of rows beyond 2^31 elements, few tokens and many."""
+    torch = torch_mod()
+    for n, stride in ((100, 1 << 25), (40000, 1 << 17)):
+        w = Layer(tcd, n, 64, 64, residual=True, seed=9)
+        w.run()
+        w.check()
+        big = torch.empty((n, stride), dtype=w.y.dtype, device="cuda")
+        big[:, :64] = w.r
+        w.linear.apply(w.x, big[:, :64], residual=big[:, :64])
+        w.linear.raise_on_error()
+        assert torch.equal(big[:, :64], w.y)
+        del big
+        torch.cuda.empty_cache()
+
+
+def test_made_and_dropped_while_a_graph_is_captured(tcd):
+    """An object whose error word is new memory in the middle of a capture, and a graph that outlives its objects."""
+    torch = torch_mod()
+    w = Layer(tcd, 33, 256, 192, bias=True, seed=4)
+    want = w.run().clone()
+    s, out = torch.cuda.Stream(), torch.zeros_like(want)
+    words = dict(tcd._words)
+    tcd._words.clear()                                     # (the next object needs new memory)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        tcd.Linear(w.w, bias=w.b[0]).apply(w.x, out)
+    tcd._words.update(words)
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_one_object_from_two_threads(tcd):
+    import threading
+    torch = torch_mod()
+    layers = [Layer(tcd, n, 1024, 320, bias=True, seed=n) for n in (3, 500)]
+    one = layers[0].linear
+    ins = [layers[0].x, torch.randn((500, 1024), device="cuda").to(layers[0].x.dtype)]
+    want = []
+    for x in ins:
+        y = torch.empty((x.shape[0], 320), dtype=x.dtype, device="cuda")
+        one.apply(x, y)
+        want.append(y)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        y = torch.empty_like(want[i])
+        s.synchronize()
+        for _ in range(300):
+            one.apply(ins[i], y, stream=s)
+        s.synchronize()
+        if not torch.equal(y, want[i]):
+            bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i % 2,)) for i in range(4)]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    one.raise_on_error()
+    assert not bad

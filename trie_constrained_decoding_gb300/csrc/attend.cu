@@ -173,7 +173,7 @@ struct AttendParams {
   // Groups with a common prefix:
   const int32_t* cu_seqs;
   const int32_t* shared_lens;
-  int32_t groups;
+  int32_t all_groups, groups;  // 0 of them: their prefixes are not taken by themselves
   int32_t prefix_q_rows;  // rows of one query load of a prefix
   int32_t rest_q_rows;    // and of a short rest
   int32_t rest_items;     // items of attend_rest_kernel; 0: it is not used
@@ -498,9 +498,9 @@ struct Line {
   }
 };
 
-// The group of sequence b among ascending ones, or -1.
-__device__ __forceinline__ int group_of(const AttendParams& p, int b) {
-  int lo = -1, hi = p.groups;
+// The group of sequence b among the first `groups`, which ascend, or -1.
+__device__ __forceinline__ int group_of(const AttendParams& p, int b, int groups) {
+  int lo = -1, hi = groups;
 #pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -541,16 +541,17 @@ __device__ __forceinline__ void set_line(const AttendParams& p, const Span& s, i
   l->extra = extra;
   l->prefix = SH && s.kind == kPrefix;
 }
-// Sequence b without what its group shares.
-__device__ __forceinline__ bool rest_of(const AttendParams& p, int b, Span* s) {
+// Sequence b without what its group among the first `groups` shares.
+__device__ __forceinline__ bool rest_of(const AttendParams& p, int b, Span* s, int groups) {
   bool ok = seq_span(p.tok, p.kv.page_size, b, s) && s->n <= p.max_tokens;
-  const int g = group_of(p, b), len = g < 0 ? 0 : prefix_of(p, g);
+  const int g = group_of(p, b, groups), len = g < 0 ? 0 : prefix_of(p, g);
   ok = ok && len >= 0 && len <= s->ctx;
   s->kind = len > 0 ? kRest : kWhole;
   s->pages = (int64_t)b * p.tok.width + (len >> p.kv.page_shift);
   s->ctx -= len;
   return ok;
 }
+__device__ __forceinline__ bool rest_of(const AttendParams& p, int b, Span* s) { return rest_of(p, b, s, p.groups); }
 __device__ __forceinline__ bool is_short(const AttendParams& p, const Span& s) {
   return p.rest_items > 0 && s.kind == kRest && (int64_t)s.n * p.group <= kRestRows && (int64_t)s.ctx + s.n <= kRestSlots;
 }
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool fits = true;
   if constexpr (SH) {
     // Groups that do not ascend: no work, and an error of every sequence.
-    for (int g = tid; g < p.groups; g += kThreads) {
+    for (int g = tid; g < p.all_groups; g += kThreads) {
       const int lo = __ldg(p.cu_seqs + g), hi = __ldg(p.cu_seqs + g + 1);
       fits &= lo >= 0 && hi >= lo && hi <= p.tok.batch;
     }
@@ -2123,12 +2124,13 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
       late |= e == 1;
       fits &= e != kMisfit;
     }
-    bool ok = __syncthreads_and(fits) && rest_of(p, b, &s);  // (that it fits the group as well)
+    // (that it fits its group as well, whether or not the group's prefix was taken by itself)
+    bool ok = __syncthreads_and(fits) && rest_of(p, b, &s, p.all_groups);
     if (ok && s.n > 0) {
       const int32_t* row = p.tok.table + (int64_t)b * p.tok.width;
       const int shared = (int)((s.pages - (int64_t)b * p.tok.width));  // pages
       const int pages = shared + (s.ctx + s.n - 1) / p.kv.page_size + 1;
-      const int32_t* first = shared ? p.tok.table + (int64_t)__ldg(p.cu_seqs + group_of(p, b)) * p.tok.width : row;
+      const int32_t* first = shared ? p.tok.table + (int64_t)__ldg(p.cu_seqs + group_of(p, b, p.all_groups)) * p.tok.width : row;
       if (is_short(p, s))
         for (int i = threadIdx.x; i < p.kv.kv_heads; i += kJoinThreads)
           late |= __ldcg(p.row_short + ml_at(p, 0, i, (int64_t)s.row0 * p.group)) == kBegun;
@@ -2284,6 +2286,8 @@ size_t workspace_bytes(int workers, int head_dim) {
   return (size_t)workers * (sizeof(SharedSeg) + 16) + part_rows(workers) * (sizeof(float2) + sizeof(float) * head_dim) + 64;
 }
 
+constexpr int64_t kShareBytes = 16 << 20;
+
 // What joining two results of every row takes beside that.
 size_t shared_bytes(int64_t rows, int head_dim) {
   return 2 * (size_t)rows * (sizeof(float2) + sizeof(float) * head_dim) + (size_t)rows * sizeof(int32_t) + 256;
@@ -2341,7 +2345,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorM
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, SH ? attend_join_shared_kernel<T, D> : attend_join_kernel<T, D>, p);
-  if (!SH || e != cudaSuccess) return e;
+  if (!SH || p.groups == 0 || e != cudaSuccess) return e;
   const int64_t most = (int64_t)(p.max_tokens < p.tok.n_tokens ? p.max_tokens : p.tok.n_tokens) * p.q_heads * (D / 4);
   const int64_t room = (8 * p.workers + p.tok.batch - 1) / p.tok.batch, want = (most + kPairThreads - 1) / kPairThreads;
   cfg.gridDim = dim3((unsigned)p.tok.batch, (unsigned)(want < 1 ? 1 : want < room ? want : room));
@@ -2448,7 +2452,12 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
   if (sh) {
     p.cu_seqs = sh->cu_seqs;
     p.shared_lens = sh->shared_lens;
-    p.groups = sh->groups;
+    // Contexts that are small together, whatever the lengths, are read sequence by sequence: sharing them saves less than
+    // the joining takes (four sequences of 560 slots, 9 MB: 22.4 us shared, 19.6 not; four of 1060, 17 MB: 22.2 and 21.3;
+    // 16 of 310, 20 MB: 21.9 and 24.1).  The errors of their groups are found all the same.
+    const int64_t most = (int64_t)tokens->batch * tokens->table_width * kv->page_size * kv->kv_heads * kv->head_dim * 4;
+    p.all_groups = sh->groups;
+    p.groups = most <= kShareBytes ? 0 : sh->groups;
     const size_t rows = 2 * (size_t)tokens->n_tokens * a->q_heads;
     ws += ((size_t)p.workers * sizeof(int32_t) + 15) / 16 * 16;
     ws += (128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127;
@@ -2458,7 +2467,7 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
     // With fewer items than SMs each has an SM in the main kernel anyway, and a launch less counts: four sequences of 3 to
     // 21 slots behind 32 19.9 us without, 21.4 with it.
     const int64_t items = (int64_t)tokens->batch * kv->kv_heads;
-    p.rest_items = items <= p.workers || items > INT32_MAX || group > kRestRows ? 0 : (int)items;
+    p.rest_items = p.groups == 0 || items <= p.workers || items > INT32_MAX || group > kRestRows ? 0 : (int)items;
   }
   p.wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
   p.withhold = a->withhold;
