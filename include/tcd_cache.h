@@ -222,7 +222,10 @@ tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes);
  *               ids in every sequence's page table.  A sequence where they
  *               differ from the group's first one's, or with fewer slots cached
  *               than its group shares, gets TC_ERR_BOUNDS, and so does a whole
- *               group whose length is out of range.
+ *               group whose length is out of range.  (A bounded wait that gives
+ *               up fails the sequences whose results it may have touched with
+ *               TC_ERR_DEVICE_TIMEOUT: all of them, or those whose own slots
+ *               its block had taken.)
  *  workspace    (device) tc_attend_shared_workspace bytes for this number of
  *               tokens and heads (those of tc_attend, and about two results of
  *               head_dim + 2 floats for each token and query head).

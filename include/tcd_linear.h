@@ -78,7 +78,8 @@ typedef struct tc_linear_t {
  *            stride of at least out_features); NULL: none.  May be `out` itself
  *            (with the same stride), but must not overlap it in another way.
  *  out       (device) rows of out_features elements, out_stride apart (the same);
- *            must not overlap x or the weights.
+ *            must not overlap x, the weights or the biases (an overlap is
+ *            refused; of rows with different strides, any that interleave).
  *  status    (device) one int32 that the caller has set to TC_OK: it becomes
  *            TC_ERR_DEVICE_TIMEOUT if a bounded wait of the kernel gave up (the
  *            outputs are then invalid), and is not written otherwise, so that

@@ -3,7 +3,7 @@ import ctypes
 
 import pytest
 
-INVALID, CAPACITY, UNSUPPORTED = 1, 10, 11
+INVALID, CAPACITY, UNSUPPORTED, CUDA = 1, 10, 11, 32
 AT = 1 << 20   # (an address that is never read)
 
 
@@ -49,6 +49,50 @@ def test_weights(tcd, change, code):
 @pytest.mark.parametrize("change,code", CALLS, ids=str)
 def test_call(tcd, change, code):
     assert tcd._linear(layer(tcd), call(tcd, **change), AT, None) == code
+
+
+# Elements of 2 bytes; x has rows of 64, out and the residual rows of 32, four of each.
+OUT = AT + (1 << 16)
+OVERLAPS = [
+    (dict(out=AT), True),                                              # x itself
+    (dict(out=AT, out_stride=64), True),
+    (dict(out=AT - 2 * (3 * 32 + 32)), False),                         # up to where x begins
+    (dict(out=AT - 2 * (3 * 32 + 31)), True),
+    (dict(out=AT + 2 * (3 * 64 + 64)), False),                         # from where x ends
+    (dict(out=AT + 2 * (3 * 64 + 63)), True),
+    (dict(x_stride=96, out=AT + 2 * 64, out_stride=96), False),        # columns beside x in common rows
+    (dict(x_stride=96, out=AT + 2 * 63, out_stride=96), True),
+    (dict(x_stride=96, out=AT + 2 * 65, out_stride=96), True),         # (the next row's x)
+    (dict(x_stride=96, out=AT - 2 * 32, out_stride=96), False),
+    (dict(x_stride=96, out=AT - 2 * 31, out_stride=96), True),
+    (dict(x_stride=96, out=AT + 2 * (64 + 96 * 2), out_stride=96), False),
+    (dict(x_stride=96, out=AT + 2 * 64, out_stride=192), True),        # (interleaved rows of other strides)
+    (dict(n_tokens=1, out=AT + 2 * 64), False),
+    (dict(n_tokens=1, out=AT + 2 * 63), True),
+    (dict(residual=OUT, residual_stride=32), False),                   # in place
+    (dict(residual=OUT, residual_stride=40), True),
+    (dict(residual=OUT + 2, residual_stride=32), True),
+    (dict(residual=OUT + 2 * 32, out_stride=64, residual_stride=64), False),
+    (dict(n_tokens=1, residual=OUT, residual_stride=40), False),
+    (dict(residual=AT, residual_stride=32), False),                    # x, which is read as well
+]
+
+
+@pytest.mark.parametrize("change,refused", OVERLAPS, ids=str)
+def test_out_overlaps(tcd, change, refused):
+    """(Device 63 is not there: what is not refused ends at that.)"""
+    w = AT + (1 << 18)
+    change = dict(dict(out=OUT), **change)
+    code = tcd._linear(layer(tcd, weight=w, device=63), call(tcd, **change), AT, None)
+    assert code == (INVALID if refused else CUDA)
+
+
+@pytest.mark.parametrize("what", ["weight", "gate", "bias", "gate_bias"])
+def test_out_overlaps_weights(tcd, what):
+    w = dict(weight=AT + (1 << 18), gate=AT + (1 << 19), gate_stride=64, bias=AT + (1 << 17),
+             gate_bias=AT + (1 << 17) + 64)
+    for at, refused in ((OUT, False), (w[what], True), (w[what] - 2 * 127, True)):
+        assert tcd._linear(layer(tcd, device=63, **w), call(tcd, out=at), AT, None) == (INVALID if refused else CUDA)
 
 
 def test_missing(tcd):

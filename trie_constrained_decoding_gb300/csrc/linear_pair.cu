@@ -13,9 +13,13 @@
 // each.  Tensor memory gives a thread one token's sums; they are turned in
 // shared memory, so that a thread has the same features of many tokens: biases stay
 // in registers, rows are read and written in whole pieces whatever their
-// alignment, and the code is a short loop (with 32 features of a token a thread
-// at a time, unrolled, a call of one tile per pair spent 14 us here, most of them
-// on the fetch of instructions).
+// alignment, and the code is a short loop.  (A thread takes several tokens' values
+// before it stores the first: one by one nothing would overlap.)  Rows on
+// whole fours are still cheaper: 1111 tokens of 1000 x 2731 take 17.9 us, of 1000 x 2732 14.2.
+//
+// Bound: the tensor cores, busy 88 to 90 % of the kernel, and the power limit in
+// continuous runs: 8192 tokens of 14336 x 4096 527 us in short runs and 609 in
+// continuous ones, 4096 gated of 4096 x 14336 511 and 584.
 #include <type_traits>
 
 #include "linear.h"
