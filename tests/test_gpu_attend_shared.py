@@ -139,6 +139,29 @@ def test_drafts(tcd, case, room):
     w.check(kv, q64, out, masks, lse=lse)
 
 
+# One prefix in many parts: sequences, heads of a group, kv_heads, head_dim, page, type, prefix.  A row's parts are added
+# up by one thread or by two, as the call's tokens and heads fill tasks: few rows, rows that end inside a task, and on
+# either side of the change (9 and 10 tiles of 64 tokens with 152 SMs).
+LONG = [
+    (2, 1, 1, 128, 64, "bf16", 20011), (2, 1, 1, 64, 16, "f16", 3001), (9, 4, 8, 128, 64, "bf16", 3011),
+    (75, 3, 3, 64, 32, "f16", 2500), (64, 4, 8, 128, 64, "f16", 1500), (64, 4, 9, 128, 64, "bf16", 1300),
+    (64, 4, 10, 128, 64, "bf16", 1300), (70, 4, 8, 64, 128, "bf16", 1500), (3, 100, 2, 128, 32, "bf16", 2100),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_long_prefix(tcd, case):
+    batch, group, hkv, d, page, dt, prefix = LONG[case]
+    tokens = [1 + b % 2 for b in range(batch)] if batch < 64 else [1] * batch
+    w = Groups(tcd, tokens, [prefix + 7 * b % 90 for b in range(batch)], [(0, batch, prefix)], dt, hkv, d, page, 90 + case)
+    kv = w.fill()
+    q, q64 = w.normal(w.n, group * hkv, d)
+    out, lse = w.attend(q, lse=True)
+    w.check(kv, q64, out, lse=lse)
+    again, lse2 = w.attend(q, lse=True)
+    assert torch_mod().equal(out, again) and torch_mod().equal(lse, lse2)
+
+
 # Many sequences at once (more items than the GPU has SMs): heads of a group, kv_heads, head_dim, page, type, most tokens
 MANY = [
     (4, 2, 128, 64, "bf16", 1), (4, 2, 128, 16, "f16", 16), (1, 2, 64, 128, "bf16", 64), (7, 2, 64, 32, "f16", 9),

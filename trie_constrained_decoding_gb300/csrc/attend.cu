@@ -177,6 +177,7 @@ struct AttendParams {
   int32_t prefix_q_rows;  // rows of one query load of a prefix
   int32_t rest_q_rows;    // and of a short rest
   int32_t rest_items;     // items of attend_rest_kernel; 0: it is not used
+  int32_t join_shift;     // log2 of attend_join_shared_kernel's tasks for an item
   // Results of rows before they are joined, by key-value head, of the prefix and of the rest.  (Columns in fours outside:
   // the threads of a warp have neighbouring rows.)
   float* row_o;        // [prefix or rest][kv_head][D / 4][row][4]
@@ -2108,10 +2109,18 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendP
 // has for itself with it, if that is there.  Bound: latencies, among them the fetch of instructions, so the code is short
 // (eight parts at a time, unrolled: 64 tokens behind 8003 slots 16.4 us instead of 11.4; blocks for each worker, as
 // above, take 13).
-constexpr int kJoinSharedBlocks = 4;  // for each worker
-template <typename T, int D>
+//
+// WAYS: 2 where prefixes are so few that their tasks leave half of the blocks idle: two threads share out a row's parts,
+// the first half of them and the second, in that order (64 tokens behind 8003 slots, the whole call 49.2 us instead of
+// 52.0, 8 tokens 31.7 and 33.9; for drafts of 256 sequences, 206 instead of 197, each task would cost more and none is
+// idle.  Four threads: 51.2 and 228).  The host chooses: the kernel itself takes 2 us longer with both ways in it.
+constexpr int kJoinSharedBlocks = 4;  // for each worker, at most
+template <typename T, int D, int WAYS>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const AttendParams p) {
+  constexpr int kTask = kJoinThreads / WAYS;  // pieces of four columns
   __shared__ uint32_t starts[32];
+  __shared__ float4 other_o[WAYS > 1 ? kTask : 1];
+  __shared__ float2 other_ml[WAYS > 1 ? kTask : 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int blocks = gridDim.x - p.tok.batch;
@@ -2153,10 +2162,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
     if (w % 32 == 0) starts[w / 32] = m;
   }
   __syncthreads();
-  constexpr int kChunks = 2 * kTile * (D / 4) / kJoinThreads;  // of an item
+  const bool second = WAYS > 1 && threadIdx.x >= kTask;
   int before = 0, word = 0;
   for (int slot = blockIdx.x;; slot += blocks) {
-    const int item = slot / kChunks;
+    const int item = slot >> p.join_shift, piece0 = (slot & ((1 << p.join_shift) - 1)) * kTask;
     // the item-th worker that starts one
     while (word < 32 && item - before >= __popc(starts[word])) before += __popc(starts[word++]);
     if (word == 32) break;
@@ -2166,8 +2175,15 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
     const SharedSeg g = p.descs[w0];
     const int full = p.tile_tokens * p.group, left = (g.n - g.tok0) * p.group;
     const int v0 = min(left, full), rows = g.two ? min(left, 2 * full) : v0;  // rows of the first M tile, of both
-    const int i = slot % kChunks * kJoinThreads + threadIdx.x;
-    if (i >= rows * (D / 4)) continue;
+    int i = piece0 + threadIdx.x % kTask;
+    bool mine = i < rows * (D / 4);
+    if (WAYS == 1) {
+      if (!mine) continue;
+    } else {
+      if (piece0 >= rows * (D / 4)) continue;  // (all threads of the block)
+      if (!mine) i = 0;
+      mine = mine && !second;
+    }
     const int c = i / rows * 4, k = i % rows;        // columns c .. c + 3 of row k
     const int rr = k < v0 ? k : kTile + k - v0;      // its place in a part
     const int tok = g.tok0 + k / p.group, of = k % p.group;
@@ -2175,7 +2191,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
     int there = kLong;
     float2 rest_ml;
     float4 rest_o;
-    if (g.kind == kPrefix && p.rest_items > 0) {  // (on their way together with the parts)
+    if (mine && g.kind == kPrefix && p.rest_items > 0) {  // (on their way together with the parts)
       there = __ldcg(p.row_short + ml_at(p, 0, g.head, r));
       rest_ml = __ldcg(p.row_ml + ml_at(p, 1, g.head, r));
       rest_o = __ldcg(o_at<D>(p, 1, g.head, r, c));
@@ -2189,11 +2205,23 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
       v = make_float4(fmaf(v.x, z.e, o.x * z.f), fmaf(v.y, z.e, o.y * z.f), fmaf(v.z, z.e, o.z * z.f),
                       fmaf(v.w, z.e, o.w * z.f));
     };
+    const int mid = (w0 + g.last) / 2;
+    const int wa = second ? mid + 1 : w0, wb = WAYS == 1 || second ? g.last : mid;
 #pragma unroll 4
-    for (int w = w0; w <= g.last; ++w) {
+    for (int w = wa; w <= wb; ++w) {
       const size_t at = ((size_t)w * 2 + (w == w0)) * 2 * kTile;
       add(__ldcg(p.part_ml + at + rr),
           __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + (size_t)(c / 4) * (2 * kTile) + rr));
+    }
+    if constexpr (WAYS > 1) {
+      __syncthreads();  // (what the task before left has been read)
+      if (second) {
+        other_o[threadIdx.x - kTask] = v;
+        other_ml[threadIdx.x - kTask] = make_float2(m, l);
+      }
+      __syncthreads();
+      if (!mine) continue;
+      add(other_ml[threadIdx.x], other_o[threadIdx.x]);
     }
     bool done = g.kind == kWhole;
     if (there == kDone) {
@@ -2341,10 +2369,29 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kv, const CUtensorM
   cfg.dynamicSmemBytes = smem_bytes<D>();
   e = cudaLaunchKernelEx(&cfg, attend_kernel<T, D, SH>, p, kv, q, pq);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(p.workers * (SH ? kJoinSharedBlocks : kJoinBlocks) + p.tok.batch));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, SH ? attend_join_shared_kernel<T, D> : attend_join_kernel<T, D>, p);
+  if constexpr (SH) {
+    // An item's rows are of two tiles at most, and of no more tokens than the call has (without prefixes: a sequence).  No
+    // more blocks than the tasks of the items that can be in parts: four sequences behind 32 slots 14.2 us, with all blocks
+    // 15.9.
+    const int64_t blocks = p.workers * kJoinSharedBlocks, step = 2 * p.tile_tokens, n = p.tok.n_tokens;
+    const int64_t one = p.groups > 0 || p.max_tokens > n ? n : p.max_tokens;
+    const int64_t pieces = (one < 1 ? 1 : one < step ? one : step) * p.group * (D / 4);
+    const auto items_of = [&](int64_t runs) { return (n + runs * (step - 1)) / step * p.kv.kv_heads; };
+    const int64_t prefixes = items_of(p.groups), items = (p.groups > 0 ? prefixes : 0) + items_of(p.tok.batch);
+    AttendParams j = p;
+    while ((int64_t)kJoinThreads << j.join_shift < pieces) ++j.join_shift;
+    const bool halves = p.groups > 0 && prefixes << (j.join_shift + 1) <= blocks;
+    if (halves) ++j.join_shift;
+    const int64_t most = (items < p.workers ? items : p.workers) << j.join_shift;
+    cfg.gridDim = dim3((unsigned)((most < blocks ? most : blocks) + p.tok.batch));
+    e = halves ? cudaLaunchKernelEx(&cfg, attend_join_shared_kernel<T, D, 2>, j)
+               : cudaLaunchKernelEx(&cfg, attend_join_shared_kernel<T, D, 1>, j);
+  } else {
+    cfg.gridDim = dim3((unsigned)(p.workers * kJoinBlocks + p.tok.batch));
+    e = cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p);
+  }
   if (!SH || p.groups == 0 || e != cudaSuccess) return e;
   const int64_t most = (int64_t)(p.max_tokens < p.tok.n_tokens ? p.max_tokens : p.tok.n_tokens) * p.q_heads * (D / 4);
   const int64_t room = (8 * p.workers + p.tok.batch - 1) / p.tok.batch, want = (most + kPairThreads - 1) / kPairThreads;
