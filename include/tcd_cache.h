@@ -208,8 +208,8 @@ tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes);
  * sequences, and the result of each token is joined with that over the slots its
  * sequence has for itself.  The outputs are tc_attend's (their sums are split at
  * the end of the prefix, so that last bits may differ).  Where the page tables have
- * room for few slots altogether, contexts are read sequence by sequence, as that is
- * faster then.
+ * room for few slots altogether, for the number of tokens that a sequence has in the
+ * mean, contexts are read sequence by sequence, as that is faster then.
  *
  *  groups       1 .. batch: runs of neighbouring sequences.
  *  cu_seqs      (device) int32[groups + 1], ascending within [0, batch]: group g

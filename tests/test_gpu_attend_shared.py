@@ -14,10 +14,12 @@ pytestmark = pytest.mark.gpu
 class Groups(Batch):
     """A batch whose groups ([first, end) sequences, shared slots) hold their whole shared pages in common.
 
-    room: MB of slots that the page tables have place for (below 16, contexts are read sequence by sequence)."""
+    room: MB of slots that the page tables have place for, and 4 for each row that a sequence has in the mean, of up to
+    `heads` heads of a group (up to 16 and 4 contexts are read sequence by sequence)."""
 
-    def __init__(self, tcd, tokens, ctx, groups, dt="bf16", kv_heads=2, head_dim=128, page=16, seed=0, room=17):
-        wide = (room << 20) // (len(tokens) * page * kv_heads * head_dim * 4) + 1 if room else 2
+    def __init__(self, tcd, tokens, ctx, groups, dt="bf16", kv_heads=2, head_dim=128, page=16, seed=0, room=17, heads=16):
+        place = (room << 20) + (4 << 20) * heads * sum(tokens) // len(tokens)
+        wide = place // (len(tokens) * page * kv_heads * head_dim * 4) + 1 if room else 2
         super().__init__(tcd, tokens, ctx, dt, kv_heads, head_dim, page, seed=seed, extra_width=wide)
         torch = torch_mod()
         self.groups = groups
@@ -115,7 +117,7 @@ def build(tcd, case, seed, room=17):
     for lo, hi, shared in groups:
         for b in range(lo, hi):
             ctx[b] += shared
-    return Groups(tcd, tokens, ctx, groups, dt, hkv, d, page, seed, room), hq
+    return Groups(tcd, tokens, ctx, groups, dt, hkv, d, page, seed, room, hq // hkv), hq
 
 
 @pytest.mark.parametrize("room", [17, 0])
@@ -153,7 +155,8 @@ LONG = [
 def test_long_prefix(tcd, case):
     batch, group, hkv, d, page, dt, prefix = LONG[case]
     tokens = [1 + b % 2 for b in range(batch)] if batch < 64 else [1] * batch
-    w = Groups(tcd, tokens, [prefix + 7 * b % 90 for b in range(batch)], [(0, batch, prefix)], dt, hkv, d, page, 90 + case)
+    w = Groups(tcd, tokens, [prefix + 7 * b % 90 for b in range(batch)], [(0, batch, prefix)], dt, hkv, d, page, 90 + case,
+               heads=group)
     kv = w.fill()
     q, q64 = w.normal(w.n, group * hkv, d)
     out, lse = w.attend(q, lse=True)
@@ -181,7 +184,8 @@ def many(tcd, case, seed):
     behind[:8] = [0, 64 - min(most, 64), 5, 63, 64, 1024, 1023, 700]
     groups = [(0, 40, 130), (40, 41, 300), (41, 93, 3 * page + 1)]
     ctx = behind + np.repeat([g[2] for g in groups] + [0], [40, 1, 52, 7])
-    return Groups(tcd, [int(x) for x in tokens], [int(x) for x in ctx], groups, dt, hkv, d, page, seed), group * hkv
+    return Groups(tcd, [int(x) for x in tokens], [int(x) for x in ctx], groups, dt, hkv, d, page, seed,
+                  heads=group), group * hkv
 
 
 @pytest.mark.parametrize("drafts", [False, True])

@@ -2314,7 +2314,7 @@ size_t workspace_bytes(int workers, int head_dim) {
   return (size_t)workers * (sizeof(SharedSeg) + 16) + part_rows(workers) * (sizeof(float2) + sizeof(float) * head_dim) + 64;
 }
 
-constexpr int64_t kShareBytes = 16 << 20;
+constexpr int64_t kShareBytes = 16 << 20, kShareRowBytes = 4 << 20;
 
 // What joining two results of every row takes beside that.
 size_t shared_bytes(int64_t rows, int head_dim) {
@@ -2500,11 +2500,15 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
     p.cu_seqs = sh->cu_seqs;
     p.shared_lens = sh->shared_lens;
     // Contexts that are small together, whatever the lengths, are read sequence by sequence: sharing them saves less than
-    // the joining takes (four sequences of 560 slots, 9 MB: 22.4 us shared, 19.6 not; four of 1060, 17 MB: 22.2 and 21.3;
-    // 16 of 310, 20 MB: 21.9 and 24.1).  The errors of their groups are found all the same.
+    // the joining takes, and what it saves is less the more rows a sequence has, as these share the reads and products of
+    // a tile by themselves (the mean is what counts, so that a prompt among single tokens does not decide).  In us, shared
+    // and not, rows of a sequence / MB: 4 / 16 21.6 and 19.1, 32 21.9 and 23.8 (four sequences), 42 36.9 and 34.8, 85 38.0
+    // and 41.1 (64 of them); 10 / 65 26.5 and 26.1, 72 39.5 and 41.1; 18 / 72 45.3 and 41.6, 128 33.1 and 33.6; 48 / 135
+    // 53.4 and 49.7, 252 48.4 and 50.4; 180 / 510 191 and 144.  The errors of their groups are found all the same.
+    const int64_t rows_each = (int64_t)tokens->n_tokens * group / tokens->batch;
     const int64_t most = (int64_t)tokens->batch * tokens->table_width * kv->page_size * kv->kv_heads * kv->head_dim * 4;
     p.all_groups = sh->groups;
-    p.groups = most <= kShareBytes ? 0 : sh->groups;
+    p.groups = most <= kShareBytes + rows_each * kShareRowBytes ? 0 : sh->groups;
     const size_t rows = 2 * (size_t)tokens->n_tokens * a->q_heads;
     ws += ((size_t)p.workers * sizeof(int32_t) + 15) / 16 * 16;
     ws += (128 - (reinterpret_cast<uintptr_t>(ws) & 127)) & 127;
