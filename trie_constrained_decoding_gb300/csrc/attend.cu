@@ -2504,7 +2504,8 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
     // a tile by themselves (the mean is what counts, so that a prompt among single tokens does not decide).  In us, shared
     // and not, rows of a sequence / MB: 4 / 16 21.6 and 19.1, 32 21.9 and 23.8 (four sequences), 42 36.9 and 34.8, 85 38.0
     // and 41.1 (64 of them); 10 / 65 26.5 and 26.1, 72 39.5 and 41.1; 18 / 72 45.3 and 41.6, 128 33.1 and 33.6; 48 / 135
-    // 53.4 and 49.7, 252 48.4 and 50.4; 180 / 510 191 and 144.  The errors of their groups are found all the same.
+    // 53.4 and 49.7, 252 48.4 and 50.4 (16 sequences; four take 41.8 and 47.8 and are not shared); 180 / 510 191 and 144.
+    // The errors of their groups are found all the same.
     const int64_t rows_each = (int64_t)tokens->n_tokens * group / tokens->batch;
     const int64_t most = (int64_t)tokens->batch * tokens->table_width * kv->page_size * kv->kv_heads * kv->head_dim * 4;
     p.all_groups = sh->groups;
