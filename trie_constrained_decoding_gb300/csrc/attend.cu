@@ -1554,7 +1554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // What it measured (32 query and 8 key-value heads of 128): one token of 64 sequences
 // with 20 to 300 slots 20 us; 3 to 16 tokens of 256 sequences with 50 to 500 slots 72 us,
-// 4.4 TB/s.  Calls as a whole, behind 8003 and 1001 to 4001 shared slots: 52 and 198 us,
+// 4.4 TB/s.  Calls as a whole, behind 8003 and 1001 to 4001 shared slots: 49 and 198 us,
 // with these items in the kernel above 59 and 278.  Bound: latencies where items begin
 // and end.  (A form of it with the matrix instructions of single warps, mma.sync,
 // three CTAs an SM, took 104 us for the drafts.)
