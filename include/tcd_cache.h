@@ -73,8 +73,8 @@ typedef struct tc_kv_t {
  *  n_tokens     rows of the packed token arrays (>= 0; 0 only does the status).
  *  cu_tokens    (device) int32[batch + 1], ascending: sequence b's tokens are
  *               rows [cu_tokens[b], cu_tokens[b + 1]); none is allowed.  (Where
- *               it descends, that sequence gets TC_ERR_BOUNDS; a row that other
- *               sequences then have in common belongs to any one of them.)
+ *               it descends, that sequence gets TC_ERR_BOUNDS; in a row that other
+ *               sequences then have in common each element is any one's of them.)
  *  ctx_lens     (device) int32[batch]: tokens of sequence b already cached.
  *               Its new token t lies in slot ctx_lens[b] + t.
  *  page_table   (device) int32[batch][table_width] page ids; entries past a
@@ -209,7 +209,8 @@ tc_status tc_attend_workspace(const tc_kv_t* kv, int64_t* bytes);
  * sequence has for itself.  The outputs are tc_attend's (their sums are split at
  * the end of the prefix, so that last bits may differ).  Where the page tables have
  * room for few slots altogether, for the number of tokens that a sequence has in the
- * mean, contexts are read sequence by sequence, as that is faster then.
+ * mean, contexts are read sequence by sequence, as that is faster then; and so they are
+ * where rows of some sequence are out of range or descend.
  *
  *  groups       1 .. batch: runs of neighbouring sequences.
  *  cu_seqs      (device) int32[groups + 1], ascending within [0, batch]: group g

@@ -185,7 +185,8 @@ struct AttendParams {
   int32_t* row_short;  // [kv_head][row] whether what the row's sequence has for itself is attend_rest_kernel's, and there
 };
 
-constexpr int kMisfit = 2;  // in errs: the groups do not ascend
+// In errs: the groups do not ascend; rows of some sequence are out of range or descend, and nothing was shared.
+constexpr int kMisfit = 2, kAlone = 3;
 
 constexpr size_t part_rows(int workers) { return (size_t)workers * 2 * 2 * kTile; }
 
@@ -524,15 +525,11 @@ __device__ __forceinline__ int prefix_of(const AttendParams& p, int g) {
 constexpr int kRestRows = 64, kRestSlots = 1024;
 
 // A line of the work: a sequence, or (SH: there are groups with a common prefix) first
-// each group's prefix, then what each sequence has for itself.
+// the prefix of each of `groups` groups, then what each sequence has for itself.
 struct Span : SeqSpan {
   int32_t kind = kWhole;
   int64_t pages = 0;
 };
-template <bool SH>
-__device__ __forceinline__ int lines(const AttendParams& p) {
-  return SH ? p.groups + p.tok.batch : p.tok.batch;
-}
 template <bool SH>
 __device__ __forceinline__ void set_line(const AttendParams& p, const Span& s, int extra, Line* l) {
   l->n = s.n;
@@ -557,10 +554,10 @@ __device__ __forceinline__ bool is_short(const AttendParams& p, const Span& s) {
   return p.rest_items > 0 && s.kind == kRest && (int64_t)s.n * p.group <= kRestRows && (int64_t)s.ctx + s.n <= kRestSlots;
 }
 template <bool SH>
-__device__ __forceinline__ bool line_of(const AttendParams& p, int v, int extra, Span* s, Line* l) {
+__device__ __forceinline__ bool line_of(const AttendParams& p, int groups, int v, int extra, Span* s, Line* l) {
   if constexpr (SH) {
     bool ok;
-    if (v < p.groups) {
+    if (v < groups) {
       const int lo = __ldg(p.cu_seqs + v), hi = __ldg(p.cu_seqs + v + 1), len = prefix_of(p, v);
       s->kind = kPrefix;
       ok = len > 0;
@@ -573,7 +570,7 @@ __device__ __forceinline__ bool line_of(const AttendParams& p, int v, int extra,
         ok = s->row0 >= 0 && end >= s->row0 && end <= p.tok.n_tokens;
       }
     } else {
-      ok = rest_of(p, v - p.groups, s);
+      ok = rest_of(p, v - groups, s, groups);
       if (ok && is_short(p, *s)) s->n = s->ctx = 0;  // (attend_rest_kernel's)
     }
     if (!ok) s->n = s->ctx = 0;
@@ -800,23 +797,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Tiles and items of every sequence: thread i counts a run of them, then a
   // scan over the CTA gives the totals and who holds this worker's first unit.
-  const int n_lines = lines<SH>(p), run = (n_lines + kThreads - 1) / kThreads;
   bool fits = true;
+  int groups = p.groups;  // (SH)
   if constexpr (SH) {
     // Groups that do not ascend: no work, and an error of every sequence.
     for (int g = tid; g < p.all_groups; g += kThreads) {
       const int lo = __ldg(p.cu_seqs + g), hi = __ldg(p.cu_seqs + g + 1);
       fits &= lo >= 0 && hi >= lo && hi <= p.tok.batch;
     }
-    fits = __syncthreads_and(fits);
+    // The rows of a group are those from its first sequence's to its last one's, and each of them is one sequence's, only
+    // where all sequences' rows ascend.  Else every sequence is read by itself: those whose rows are in range are right.
+    bool ascend = true;
+    for (int b = tid; groups > 0 && b < p.tok.batch; b += kThreads) {
+      const int lo = __ldg(p.tok.cu + b), hi = __ldg(p.tok.cu + b + 1);
+      ascend &= lo >= 0 && hi >= lo && hi <= p.tok.n_tokens;
+    }
+    if (!__syncthreads_and(fits && ascend)) {
+      fits = __syncthreads_and(fits);
+      if (!__syncthreads_and(ascend)) groups = 0;
+    }
   }
+  const int n_lines = (SH ? groups : 0) + p.tok.batch, run = (n_lines + kThreads - 1) / kThreads;
   int64_t* sums = reinterpret_cast<int64_t*>(hdr->ml);
   int64_t tiles = 0, items = 0;
   for (int i = 0; i < run; ++i) {
     const int b = tid * run + i;
     Span s;
     Line l;
-    if (b < n_lines && fits && line_of<SH>(p, b, 0, &s, &l) && s.n > 0) {
+    if (b < n_lines && fits && line_of<SH>(p, groups, b, 0, &s, &l) && s.n > 0) {
       tiles += l.units() * p.kv.kv_heads;
       items += (int64_t)l.items() * p.kv.kv_heads;
     }
@@ -859,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = tid * run + i;
       Span s;
       Line l;
-      if (b >= n_lines || !line_of<SH>(p, b, extra, &s, &l)) continue;
+      if (b >= n_lines || !line_of<SH>(p, groups, b, extra, &s, &l)) continue;
       const int64_t u = l.units() * p.kv.kv_heads;
       if (begin < at + u) {
         hdr->seq0 = b;
@@ -1066,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             per = l.units();
           } else {
             // (sequences without units are passed over)
-            while (b < n_lines && !(line_of<SH>(p, b, extra, &s, &l) && (per = l.units()) > 0)) ++b;
+            while (b < n_lines && !(line_of<SH>(p, groups, b, extra, &s, &l) && (per = l.units()) > 0)) ++b;
             if (b >= n_lines) break;  // (cannot be: the units add up)
           }
           // (kv_heads < 2^16)
@@ -1528,7 +1536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
   if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");  // (the next kernel waits for this one only)
-  if (tid == 0) p.errs[worker] = hdr->abort ? 1 : fits ? 0 : kMisfit;
+  if (tid == 0) p.errs[worker] = hdr->abort ? 1 : !fits ? kMisfit : SH && groups != p.groups ? kAlone : 0;
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
@@ -2128,6 +2136,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
     const int b = blockIdx.x - blocks;
     Span s;
     bool late = false, fits = true;
+    const bool shares = __ldcg(p.errs) != kAlone;  // (all workers find the same)
     for (int i = threadIdx.x; i < p.workers; i += kJoinThreads) {
       const int e = __ldcg(p.errs + i);
       late |= e == 1;
@@ -2140,7 +2149,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_shared_kernel(const 
       const int shared = (int)((s.pages - (int64_t)b * p.tok.width));  // pages
       const int pages = shared + (s.ctx + s.n - 1) / p.kv.page_size + 1;
       const int32_t* first = shared ? p.tok.table + (int64_t)__ldg(p.cu_seqs + group_of(p, b, p.all_groups)) * p.tok.width : row;
-      if (is_short(p, s))
+      if (shares && is_short(p, s))
         for (int i = threadIdx.x; i < p.kv.kv_heads; i += kJoinThreads)
           late |= __ldcg(p.row_short + ml_at(p, 0, i, (int64_t)s.row0 * p.group)) == kBegun;
       // the prefix lies in the same pages as the group's first sequence's
@@ -2251,7 +2260,8 @@ __global__ void __launch_bounds__(kPairThreads) attend_pair_kernel(const AttendP
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x;
   Span s;
-  if (__ldcg(p.errs) == kMisfit || !rest_of(p, b, &s) || s.kind != kRest || is_short(p, s)) return;
+  const int e = __ldcg(p.errs);
+  if (e == kMisfit || e == kAlone || !rest_of(p, b, &s) || s.kind != kRest || is_short(p, s)) return;
   const int64_t rows = (int64_t)s.n * p.group, all = rows * p.kv.kv_heads * (D / 4);
   for (int64_t i = blockIdx.y * kPairThreads + threadIdx.x; i < all; i += gridDim.y * kPairThreads) {
     const int64_t r = (int64_t)s.row0 * p.group + i % rows, x = i / rows;
