@@ -693,10 +693,10 @@ class KvCache:
                     words, *_rows(out, dtype, device, "out", hq, d), sums, *self._wait_test)
         return a, self._tokens(n, cu_tokens, ctx_lens, page_table)
 
-    def attend_wait_test(self, withhold: bool, wait_polls: int = 0):
-        """Make attend's kernel leave out its first load (withhold) with waits of `wait_polls` polls; (False, 0)
-        restores."""
-        self._wait_test = (int(wait_polls), int(bool(withhold)))
+    def attend_wait_test(self, withhold: int, wait_polls: int = 0):
+        """Make attend's kernel leave out its first load (True) with waits of `wait_polls` polls (2: of attend_shared
+        only the kernel for what sequences have for themselves); (False, 0) restores."""
+        self._wait_test = (int(wait_polls), int(withhold))
 
     def copy_pages(self, src, dst, status=None, stream=None):
         """tc_kv_copy_pages: page dst[i] becomes page src[i] in every layer."""

@@ -171,6 +171,7 @@ struct AttendParams {
   int32_t wait_limit;
   int32_t withhold;  // test switch: the first workers' first loads are not issued
   // Groups with a common prefix:
+  int32_t rest_wait_limit, rest_withhold;  // attend_rest_kernel's
   const int32_t* cu_seqs;
   const int32_t* shared_lens;
   int32_t all_groups, groups;  // 0 of them: their prefixes are not taken by themselves
@@ -1636,7 +1637,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
   const uint32_t q_s = smem_u32(rest_smem), kv_s = q_s + 2 * C::kUnit;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int32_t* abort = &hdr->abort;
-  const int wl = p.wait_limit;
+  const int wl = p.rest_wait_limit;
   if (tid == 0) {
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(smem_u32(&hdr->full[i]), 1);
@@ -1675,9 +1676,20 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
   const uint32_t tmem = hdr->tmem_base;
   // (after the wait: what was there for this kernel is there for the next one, which does not wait itself)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const bool held = p.withhold != 0 && blockIdx.x == 0, sound = hdr->abort == 0;
+  const bool held = p.rest_withhold != 0 && blockIdx.x == 0, sound = hdr->abort == 0;
   __syncthreads();
 
+  // Whether an item is a short rest; row_short is told of it, for all of its rows if it is a long one.
+  const auto take = [&](int item, Span* s) {
+    const int head = item % p.kv.kv_heads;
+    if (!rest_of(p, item / p.kv.kv_heads, s) || s->kind != kRest || s->n == 0) return false;
+    const bool found = is_short(p, *s);
+    const int64_t row = (int64_t)s->row0 * p.group;
+    for (int64_t r = lane; !found && r < (int64_t)s->n * p.group; r += 32)
+      p.row_short[ml_at(p, 0, head, row + r)] = kLong;
+    if (found && lane == 0) p.row_short[ml_at(p, 0, head, row)] = kBegun;
+    return found;
+  };
   // The loader's next item (-1: none is left), calls, tiles and items.
   int i = blockIdx.x, asked = 1, armed = 0, k_sent = 0;
   if (!sound) {
@@ -1695,13 +1707,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
       int head = 0;
       while (i >= 0 && !found) {
         head = i % p.kv.kv_heads;
-        if (rest_of(p, i / p.kv.kv_heads, &s) && s.kind == kRest && s.n > 0) {
-          found = is_short(p, s);
-          const int64_t row = (int64_t)s.row0 * p.group;
-          for (int64_t r = lane; !found && r < (int64_t)s.n * p.group; r += 32)
-            p.row_short[ml_at(p, 0, head, row + r)] = kLong;
-          if (found && lane == 0) p.row_short[ml_at(p, 0, head, row)] = kBegun;
-        }
+        found = take(i, &s);
         if (!warp_wait(smem_u32(&hdr->answer_full), (asked - 1) & 1, wl, abort)) {
           stop = true;
           break;
@@ -2010,7 +2016,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
   __syncthreads();
   if (*abort) {
     // A wait ran out.  What this CTA started has to end before it leaves (waits bounded again), and items that it was to
-    // take have not been begun by any other.
+    // take are begun by no other: short ones will not be done, long ones are others' work all the same.
     int32_t none = 0;
     if (warp == 1 && lane == 0 && sound) {
       mma_commit(smem_u32(&hdr->drain));
@@ -2031,8 +2037,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
       for (int x = 0; x < 2; ++x) {
         const int j = x == 0 ? i : answered && i >= 0 ? called_off(smem_u32(hdr->answer)) : -1;
         Span s;
-        if (j >= 0 && rest_of(p, j / p.kv.kv_heads, &s) && s.n > 0 && is_short(p, s) && lane == 0)
-          p.row_short[ml_at(p, 0, j % p.kv.kv_heads, (int64_t)s.row0 * p.group)] = kBegun;
+        if (j >= 0) take(j, &s);
       }
     }
     __syncwarp();
@@ -2531,8 +2536,11 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
     const int64_t items = (int64_t)tokens->batch * kv->kv_heads;
     p.rest_items = p.groups == 0 || items <= p.workers || items > INT32_MAX || group > kRestRows ? 0 : (int)items;
   }
-  p.wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
-  p.withhold = a->withhold;
+  p.rest_wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
+  p.rest_withhold = a->withhold != 0;
+  const bool rest_only = sh && a->withhold == 2;
+  p.wait_limit = rest_only ? kWaitLimit : p.rest_wait_limit;
+  p.withhold = !rest_only && a->withhold != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = sh ? launch<true>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, map_rest, map_rest_q, s)
                            : launch<false>(kv->dtype, kv->head_dim, p, map_kv, map_q, map_pq, map_rest, map_rest_q, s);
