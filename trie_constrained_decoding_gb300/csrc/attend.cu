@@ -105,7 +105,8 @@ constexpr int kThreads = 512;
 constexpr uint32_t kHalfBytes = kTile * 128; // 128 rows of 64 elements
 constexpr float kRescale = 8.f;             // log2 of the growth that moves the reference maximum
 constexpr int kSegs = 4;                    // segments ahead of the softmax groups
-constexpr int kWaitLimit = 1 << 22; // default polls of one wait before giving up
+constexpr int kWaitLimit = 1 << 22; // default polls of one wait before giving up, and the fewest of those at a CTA's end
+                                    // for what it has in flight, which must not outlive it, however soon others give up
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -1516,6 +1517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A wait ran out.  Everything this CTA started has to end before it
     // leaves (waits bounded again): the products that were issued, and the
     // loads of stages that no product has consumed.
+    const int wl = max(p.wait_limit, kWaitLimit);
     if ((warp == 1 || warp == 3 || warp == 4 || warp == 6) && lane == 0) {
       mma_commit(smem_u32(&hdr->drain));
       int32_t none = 0;
@@ -1690,8 +1692,8 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
     if (found && lane == 0) p.row_short[ml_at(p, 0, head, row)] = kBegun;
     return found;
   };
-  // The loader's next item (-1: none is left), calls, tiles and items.
-  int i = blockIdx.x, asked = 1, armed = 0, k_sent = 0;
+  // The loader's next item (-1: none is left), calls, tiles, keys and values of tiles, and items.
+  int i = blockIdx.x, asked = 1, armed = 0, sent = 0, k_sent = 0;
   if (!sound) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ loader
@@ -1759,6 +1761,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
           __syncwarp();
           if (load && is_v == v && !leave)
             tma_kv(dst + u * C::kUnit, &map_kv, slot & (p.kv.page_size - 1), half, v * p.kv.kv_heads + head, page, bar);
+          ++sent;
         }
         if (stop) break;
         slot = slot2;
@@ -2017,6 +2020,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
   if (*abort) {
     // A wait ran out.  What this CTA started has to end before it leaves (waits bounded again), and items that it was to
     // take are begun by no other: short ones will not be done, long ones are others' work all the same.
+    const int wl = max(p.rest_wait_limit, kWaitLimit);
     int32_t none = 0;
     if (warp == 1 && lane == 0 && sound) {
       mma_commit(smem_u32(&hdr->drain));
@@ -2025,11 +2029,8 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
     if (warp == 0) {
       bool answered = false;
       if (sound) {
-        // (of the last tile maybe only the keys were sent for, and no one waits long for the others)
-        for (int j = max(0, armed - 2); j <= armed; ++j)
-          for (int v = 0; v < 2; ++v)
-            if (!(held && j == 0 && v == 0))
-              mbar_wait(smem_u32(&hdr->full[2 * (j & 1) + v]), (j >> 1) & 1, j < armed ? wl : min(wl, 4096), &none);
+        for (int j = max(0, sent - kUnits); j < sent; ++j)
+          if (!(held && j == 0)) mbar_wait(smem_u32(&hdr->full[j % kUnits]), (j / kUnits) & 1, wl, &none);
         for (int j = max(0, k_sent - 2); j < k_sent; ++j)
           mbar_wait(smem_u32(&hdr->q_full[j & 1]), (j >> 1) & 1, wl, &none);
         answered = mbar_wait(smem_u32(&hdr->answer_full), (asked - 1) & 1, wl, &none);

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!ok && warp == 0 && lane == 0) {
     // What was issued has to end before this CTA goes on (waits bounded again): the products, and loads that no
     // product has waited for.
+    const int wl = max(p.wait_limit, kLinearWaitLimit);
     int32_t none = 0;
     bar_wait(smem_at(&hdr.done), 0, wl, &none);
     for (int i = max(0, armed - stages); i < armed; ++i)

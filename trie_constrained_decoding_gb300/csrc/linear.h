@@ -38,6 +38,7 @@ struct LinearParams {
 
 constexpr int kLinearDevices = 64;
 constexpr uint32_t kRowBytes = 128;         // 64 elements of a step: one row of the 128-byte swizzle
+// Default polls of one wait, and the fewest of those at a CTA's end for what it has in flight, which must not outlive it.
 constexpr int kLinearWaitLimit = 1 << 22;
 
 // ------------------------------------------------------------- instructions

@@ -407,12 +407,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                : "r"(rank ? in_first(smem_at(&hdr->abort)) : in_second(smem_at(&hdr->abort)))
                : "memory");
   if (*abort || other) {
+    const int wl = max(p.wait_limit, kLinearWaitLimit);
     int32_t none = 0;
-    if (rank == 0 && warp == 1 && lane == 0) {
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                       smem_at(&hdr->drain))
-                   : "memory");
-      bar_wait(smem_at(&hdr->drain), 0, wl, &none);
+    if (warp == 1 && lane == 0) {
+      // (in both CTAs, behind the issuer's other arrivals there)
+      if (rank == 0) pair_commit(smem_at(&hdr->drain));
+      pair_wait(smem_at(&hdr->drain), 0, wl, &none);
     }
     if (rank == 0 && tid == 0) {
       // (the arrivals that a CTA which stopped earlier has left out)
