@@ -195,7 +195,7 @@ typedef struct tc_attend_t {
   int64_t wait_polls;  /* polls of one wait inside the kernel before it gives up; 0: the default (seconds) */
   int32_t withhold;    /* 0; tests: the kernel leaves out its first load, so that its waits run out (2: of
                           tc_attend_shared only the kernel for what sequences have for themselves, and wait_polls is
-                          only for its waits) */
+                          only for its waits; 3: there one warp of a block gives up at the end of the first item) */
 } tc_attend_t;
 
 tc_status tc_attend(const tc_kv_t* kv, int32_t layer, const tc_tokens_t* tokens, const tc_attend_t* args,

@@ -73,3 +73,23 @@ def test_only_the_sequences_that_are_reported(tcd, kind):
         assert not bool(wrong.any()), np.unique(np.searchsorted(w.cu_host, wrong.nonzero()[:, 0].cpu().numpy(), "right") - 1)
     w.cache.attend_wait_test(False)
     assert torch.equal(w.attend(q)[0], good) and not w.status.any()
+
+
+@pytest.mark.parametrize("group,n", [(16, 4), (64, 1), (2, 32), (32, 2)])
+def test_an_item_that_one_warp_has_finished(tcd, group, n):
+    """One of the two warps that have an item's rows gives up, the other one does not."""
+    torch = torch_mod()
+    w, hq = build(tcd, lambda b: False, group, n, n)
+    w.fill()
+    q, _ = w.normal(w.n, hq, D)
+    good = w.attend(q)[0].clone()
+    assert not w.status.any()
+    for polls in (2000, 2500) * 3:
+        w.cache.attend_wait_test(3, polls)
+        out, _ = w.attend(q, workspace=left_by_another_call(w, hq))
+        status = w.status.tolist()
+        assert set(status) == {0, tcd.TC_ERR_DEVICE_TIMEOUT} and status[0] != 0
+        rows = torch.tensor([c == 0 for c in status], device="cuda").repeat_interleave(n)
+        assert not bool(((out != good).flatten(1).any(1) & rows).any())
+    w.cache.attend_wait_test(False)
+    assert torch.equal(w.attend(q)[0], good) and not w.status.any()

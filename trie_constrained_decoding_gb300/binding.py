@@ -695,7 +695,8 @@ class KvCache:
 
     def attend_wait_test(self, withhold: int, wait_polls: int = 0):
         """Make attend's kernel leave out its first load (True) with waits of `wait_polls` polls (2: of attend_shared
-        only the kernel for what sequences have for themselves); (False, 0) restores."""
+        only the kernel for what sequences have for themselves; 3: one of its warps gives up where an item ends);
+        (False, 0) restores."""
         self._wait_test = (int(wait_polls), int(withhold))
 
     def copy_pages(self, src, dst, status=None, stream=None):

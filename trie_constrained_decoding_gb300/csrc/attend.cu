@@ -140,7 +140,7 @@ struct Seg {
 // What an item of a call with common prefixes (SH) is: a sequence that shares nothing,
 // a group's prefix, the rest of one of its sequences.
 enum { kWhole = 0, kPrefix = 1, kRest = 2 };
-// In row_short.  (kBegun: in an item's first row only; it stays where a wait ran out.)
+// In row_short.  (kBegun: in an item's first row only; where a wait ran out it stays, or is put back.)
 enum { kLong = 0, kDone = 1, kBegun = 2 };
 struct SharedSeg : Seg {
   int32_t kind;
@@ -1571,7 +1571,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // three CTAs an SM, took 104 us for the drafts.)
 
 constexpr int kRestThreads = 192, kRestTile = 64, kRestPerSm = 2, kUnits = 4;
-constexpr int kRestAhead = 8;   // items that have been told of; the loader is at most three ahead of the slowest warp
+constexpr int kRestAhead = 8;   // items that have been told of
+constexpr int kRestHeld = 4;    // those that some warp may not have finished: the loader is at most three ahead of it
 
 struct RestItem {
   int64_t pages;  // where its page ids begin in the table
@@ -1678,7 +1679,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
   const uint32_t tmem = hdr->tmem_base;
   // (after the wait: what was there for this kernel is there for the next one, which does not wait itself)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const bool held = p.rest_withhold != 0 && blockIdx.x == 0, sound = hdr->abort == 0;
+  const bool held = p.rest_withhold == 1 && blockIdx.x == 0, sound = hdr->abort == 0;
   __syncthreads();
 
   // Whether an item is a short rest; row_short is told of it, for all of its rows if it is a long one.
@@ -1973,6 +1974,10 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
       if (!warp_wait(smem_u32(&hdr->meet), k & 1, wl, abort) ||
           !warp_wait(smem_u32(&hdr->pv_done), (n_s - 1) & 1, wl, abort))
         break;
+      if (p.rest_withhold > 1 && blockIdx.x == 0 && quarter == 1) {  // (test switch: as if that wait had run out here)
+        *abort = 1;
+        break;
+      }
       tc_fence_after();
       const unsigned long long lost = ((unsigned long long)bad[1] << 32 | bad[0]) & seen;
       const int64_t row = (int64_t)s.row0 * p.group + r;
@@ -2018,8 +2023,9 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
   tc_fence_before();
   __syncthreads();
   if (*abort) {
-    // A wait ran out.  What this CTA started has to end before it leaves (waits bounded again), and items that it was to
-    // take are begun by no other: short ones will not be done, long ones are others' work all the same.
+    // A wait ran out.  What this CTA started has to end before it leaves (waits bounded again).  Items that it was to
+    // take are begun by no other: short ones will not be done, long ones are others' work all the same.  Those in hand may
+    // have been finished by some warps and not by others: the first row says of each that it has been begun, no more.
     const int wl = max(p.rest_wait_limit, kWaitLimit);
     int32_t none = 0;
     if (warp == 1 && lane == 0 && sound) {
@@ -2039,6 +2045,10 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
         const int j = x == 0 ? i : answered && i >= 0 ? called_off(smem_u32(hdr->answer)) : -1;
         Span s;
         if (j >= 0) take(j, &s);
+      }
+      for (int k = max(0, k_sent - kRestHeld); k < k_sent; ++k) {
+        const RestItem& s = hdr->item[k % kRestAhead];
+        if (lane == 0) p.row_short[ml_at(p, 0, s.head, (int64_t)s.row0 * p.group)] = kBegun;
       }
     }
     __syncwarp();
@@ -2538,8 +2548,8 @@ tc_status attend(const char* who, const tc_kv_t* kv, int32_t layer, const tc_tok
     p.rest_items = p.groups == 0 || items <= p.workers || items > INT32_MAX || group > kRestRows ? 0 : (int)items;
   }
   p.rest_wait_limit = a->wait_polls > 0 ? (int32_t)(a->wait_polls < 1 << 30 ? a->wait_polls : 1 << 30) : kWaitLimit;
-  p.rest_withhold = a->withhold != 0;
-  const bool rest_only = sh && a->withhold == 2;
+  p.rest_withhold = a->withhold == 3 ? 2 : a->withhold != 0;
+  const bool rest_only = sh && (a->withhold == 2 || a->withhold == 3);
   p.wait_limit = rest_only ? kWaitLimit : p.rest_wait_limit;
   p.withhold = !rest_only && a->withhold != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
