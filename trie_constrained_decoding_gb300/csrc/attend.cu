@@ -784,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_kv)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
   }
+  __syncwarp();
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hdr->tmem_base)),
                  "r"(512)
@@ -1249,10 +1250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             l *= f;
           }
-          if (grow) {
-            m = top;
-            off = T::kShift - m * p.c;
-          }
+          m = grow ? top : m;
+          off = grow ? T::kShift - m * p.c : off;
         }
         first = false;
         const uint64_t off2 = f2(off, off);
@@ -1419,16 +1418,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (SH) {
         kind = g.kind;
         joined = kind != kWhole;
-        if (kind == kPrefix && g.part < 0 && live) {
+        if (kind == kPrefix && g.part < 0 && any) {
           // What the row's sequence has for itself is there, if it is short: joined here.
           asm volatile("griddepcontrol.wait;" ::: "memory");
-          const float2 y = __ldcg(p.row_ml + ml_at(p, 1, g.head, row));
-          if (p.rest_items > 0 && __ldcg(p.row_short + ml_at(p, 0, g.head, row)) == kDone) {
-            pair = join(make_float2(m, l), y, p.c);
-            m = pair.m;
-            l = pair.l;
-            with_rest = true;
-            joined = false;
+          if (live) {
+            const float2 y = __ldcg(p.row_ml + ml_at(p, 1, g.head, row));
+            if (p.rest_items > 0 && __ldcg(p.row_short + ml_at(p, 0, g.head, row)) == kDone) {
+              pair = join(make_float2(m, l), y, p.c);
+              m = pair.m;
+              l = pair.l;
+              with_rest = true;
+              joined = false;
+            }
           }
         }
       }
@@ -1441,6 +1442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; c += 32) {
           uint32_t o[32], o1[32];
+          __syncwarp();  // (rows without work, or with other results to join, went other ways)
           tmem_ld32((g.two ? t_o : t_o0) + c, o);
           if (!g.two && used1) tmem_ld32(t_o0 + C::kCols + c, o1);
           tmem_ld_wait();
@@ -1898,10 +1900,8 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
               }
               l *= f;
             }
-            if (grow) {
-              m = top;
-              off = T::kShift - m * p.c;
-            }
+            m = grow ? top : m;
+            off = grow ? T::kShift - m * p.c : off;
           }
           const uint64_t off2 = f2(off, off);
           uint64_t sum[2] = {0ull, 0ull};
@@ -1985,6 +1985,7 @@ __global__ void __launch_bounds__(kRestThreads, kRestPerSm)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
+          __syncwarp();  // (rows of no token, or with values that were taken out, went other ways)
           tmem_ld32(t_o + c, o);
           tmem_ld_wait();
           tmem_arrived(o);
