@@ -242,6 +242,7 @@ __device__ __forceinline__ void finish_tile(const LinearParams& p, Hdr* hdr, flo
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
     uint32_t v[32];
+    __syncwarp();  // (the chunk before has been read, by threads that went ways of their own)
     tmem_ld16(acc + (GATED ? p.tile : 0) + c * F::W, v);
     tmem_ld16(acc + (GATED ? 0 : 16) + c * F::W, v + 16);
     tmem_arrived(v);
@@ -251,7 +252,6 @@ __device__ __forceinline__ void finish_tile(const LinearParams& p, Hdr* hdr, flo
       __syncwarp();
       if (lane == 0) pair_arrive(in_first(smem_at(&hdr->read[a])));
     }
-    __syncwarp();  // (the chunk before has been read)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<uint4*>(pass + sums_place(lane, i)) =
