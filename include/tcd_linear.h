@@ -86,8 +86,8 @@ typedef struct tc_linear_t {
  *            one word may gather the errors of many calls.
  *
  * Sums, activation, product and residual are held in 32 bits and rounded once.
- * The order of a sum depends on the sizes only: a call gives the same bits each
- * time.
+ * The order of a sum depends on the sizes and the GPU's number of SMs only: a call
+ * gives the same bits each time, wherever its output and residual lie.
  */
 typedef struct tc_linear_call_t {
   int32_t n_tokens;

@@ -378,6 +378,10 @@ cudaError_t launch_few(const LinearParams& p, int device, unsigned grid, size_t 
 
 // How a call is computed, and about how long it takes.
 //
+// The sizes and the number of SMs decide, and not where the output lies: the order of a sum follows from this, and the same
+// inputs have the same bits in any output.  (Where rows of 1024 or 2732 features lie at odd addresses and the way with the
+// lowest estimate would be another one for that: 11 % less to 14 % more time than with it, for 130 to 520 tokens.)
+//
 // Up to 128 tokens are one tile (pairs were never more than 4 % faster there).  More take the way with the lowest estimate.
 // The estimates' constants are a fit to 209 calls (in_features 304 to 14336, out_features 500 to 14336, with and without
 // a gate, 1 to 4000 tokens, each measured in all four ways): the way that they choose took 1.2 % longer than the best of
@@ -402,7 +406,8 @@ double weights_ns(const tc_linear_t& l) {
 // of at most four where a CTA takes a whole SM (of eight, some had to wait for the others: 256 tokens of 2048 x 2048
 // 17.8 us instead of 10.3), and in halves only (clusters of six do not fill the GPU either: 64 tokens of 4096 x 6144
 // 21.8 us instead of 14.2 with four).
-Plan plan_few(const tc_linear_t& l, int n_tokens, int cap, int sms, bool wide) {
+Plan plan_few(const tc_linear_t& l, int n_tokens, int cap, int sms) {
+  const bool wide = l.out_features % 4 == 0;  // (if the output's and the residual's rows are aligned as well)
   Plan r{};
   r.tok_tiles = (n_tokens + cap - 1) / cap;
   r.tile = ((n_tokens + r.tok_tiles - 1) / r.tok_tiles + 15) / 16 * 16;
@@ -516,9 +521,9 @@ extern "C" tc_status tc_linear(const tc_linear_t* l, const tc_linear_call_t* c, 
   p.wait_limit = c->wait_polls > 0 ? (int32_t)(c->wait_polls < 1 << 30 ? c->wait_polls : 1 << 30) : kLinearWaitLimit;
   p.withhold = c->withhold;
 
-  Plan plan = plan_few(*l, c->n_tokens, 256, sms, p.o.wide > 1);
+  Plan plan = plan_few(*l, c->n_tokens, 256, sms);
   if (c->n_tokens > 128)
-    for (const Plan& other : {plan_few(*l, c->n_tokens, 128, sms, p.o.wide > 1), plan_many(*l, c->n_tokens, 128, sms),
+    for (const Plan& other : {plan_few(*l, c->n_tokens, 128, sms), plan_many(*l, c->n_tokens, 128, sms),
                               plan_many(*l, c->n_tokens, 64, sms)})
       if (other.ns < plan.ns) plan = other;
   if (plan.grid > INT32_MAX / 2) return fail_with(TC_ERR_CAPACITY, "tc_linear: the output has too many tiles");
