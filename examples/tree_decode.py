@@ -10,9 +10,10 @@ and forked (its pages are shared until they are written).  Then each round
   2. runs the model over the drafts: per layer the projection to queries, keys
      and values (Linear), KvCache.append (norms of queries and keys, rotation,
      write into the cache), KvCache.attend_shared under the trees' masks
-     (tree_masks), which reads the prompt's pages once for all four, the
-     projection back onto the residual, and a gated feed-forward block (two more
-     Linear);
+     (tree_masks), which can read the prompt's pages once for all four (it does so
+     where page tables have room for tens of megabytes; sequences as short as these
+     are faster read by themselves, and are), the projection back onto the residual,
+     and a gated feed-forward block (two more Linear);
   3. takes constrained steps (Context.step) along the branches, as long as every
      sequence's emitted token was drafted;
   4. moves the accepted branches together (KvCache.compact) and gives the pages
