@@ -803,7 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool fits = true;
   int groups = p.groups;  // (SH)
   if constexpr (SH) {
-    // Groups that do not ascend: no work, and an error of every sequence.
+    // Groups that do not ascend: no work, and an error of every sequence.  (Short code: with these loops unrolled a call
+    // takes 0.3 us longer.)
+#pragma unroll 1
     for (int g = tid; g < p.all_groups; g += kThreads) {
       const int lo = __ldg(p.cu_seqs + g), hi = __ldg(p.cu_seqs + g + 1);
       fits &= lo >= 0 && hi >= lo && hi <= p.tok.batch;
@@ -811,6 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The rows of a group are those from its first sequence's to its last one's, and each of them is one sequence's, only
     // where all sequences' rows ascend.  Else every sequence is read by itself: those whose rows are in range are right.
     bool ascend = true;
+#pragma unroll 1
     for (int b = tid; groups > 0 && b < p.tok.batch; b += kThreads) {
       const int lo = __ldg(p.tok.cu + b), hi = __ldg(p.tok.cu + b + 1);
       ascend &= lo >= 0 && hi >= lo && hi <= p.tok.n_tokens;
