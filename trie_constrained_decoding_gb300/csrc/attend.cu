@@ -524,6 +524,10 @@ __device__ __forceinline__ int prefix_of(const AttendParams& p, int g) {
 }
 
 // What a sequence has for itself is short (attend_rest_kernel) up to so many rows (tokens and heads of a group) and slots.
+// Rows: the place that its queries have.  Slots, own ones of each sequence up to 1000, in us, short and long: one token of
+// 64 sequences behind 8000 84 and 103, of 24 sequences 55 and 58, 8 tokens of 256 sequences behind 2000 259 and 343; up
+// to 1500, long and short: 123 and 100, 66 and 62, 420 and 327; up to 4000: 225 and 191, 100 and 101, 817 and 670.  (So
+// the border could lie higher, at 3000 and more where items are many.)
 constexpr int kRestRows = 64, kRestSlots = 1024;
 
 // A line of the work: a sequence, or (SH: there are groups with a common prefix) first
@@ -1570,7 +1574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // What it measured (32 query and 8 key-value heads of 128): one token of 64 sequences
 // with 20 to 300 slots 20 us; 3 to 16 tokens of 256 sequences with 50 to 500 slots 72 us,
-// 4.4 TB/s.  Calls as a whole, behind 8003 and 1001 to 4001 shared slots: 49 and 198 us,
+// 4.4 TB/s.  Calls as a whole, behind 8003 and 1001 to 4001 shared slots: 49 and 196 us,
 // with these items in the kernel above 59 and 278.  Bound: latencies where items begin
 // and end.  (A form of it with the matrix instructions of single warps, mma.sync,
 // three CTAs an SM, took 104 us for the drafts.)

@@ -20,7 +20,7 @@
 // the cluster's meeting, the epilogue).  In continuous runs, us: one token of 2048 x 2048
 // 4.3 to 4.5, or 4.65 to 4.9 where the weights of 40 layers pass in turn (340 MB, more than L2); 64 of 4096 x 6144
 // 13.5 (3.7 TB/s); one gated of 2048 x 8192 13.2 (5.1 TB/s); 64 gated of 4096 x 14336 38.8 to
-// 40.6 (6.1 to 5.8 TB/s; alone with cold caches 44.0, 5.4 TB/s).  24 steps of weights asked for at
+// 40.6 (6.1 to 5.8 TB/s; alone with cold caches 44 to 45.4, 5.2 to 5.4 TB/s).  24 steps of weights asked for at
 // the start instead of the ring's: 3 to 9 % slower.  Weights told to leave L2 first: 1 to 2 %
 // slower where 40 layers' pass in turn, one token 8 %.  (With four layers, some of whose weights
 // then stay in L2, it looks up to 9 % faster.)
